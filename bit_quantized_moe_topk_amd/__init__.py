@@ -11,6 +11,13 @@ Calls, in the order a layer uses them:
     grp        = group(idx, E, has_shared)                  # optional
     ex         = Experts(qtype, E, has_shared, H, I, codes, hi, dm)
     y          = ffn_q(x, ex, idx, gates, grouping=grp, mode="fast" | "check")
+
+Experts in microscaled 4-bit blocks, and a router in training:
+    w  = mx4_quantize(weights)                              # [E (+ 1), N, K] -> Mx4
+    y  = mx4_experts_matmul(x, w, grp, tokens=T)            # [A, N], in the groups' order
+    dx = mx4_experts_matmul_backward(dy, w, grp, tokens=T)
+    bl = balance_loss(logits, idx);  dlogits = balance_loss_backward(logits, bl, d_losses)
+The *_backward calls are explicit: no call here records a graph for autograd.
 """
 from __future__ import annotations
 
@@ -24,7 +31,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, -1, -2, -3, -4
-F32, BF16 = 0, 1
+F32, BF16, MX4 = 0, 1, 4
 Q2, Q3 = 2, 3
 FAST, CHECK_F32 = 0, 2
 MAX_E = 2048
@@ -87,6 +94,26 @@ def lib() -> C.CDLL:
         L.moe_layer_hidden_workspace_size.restype = sz
         L.moe_layer_hidden.argtypes = [P, i32, i32, P, P, P, i32, P, P, P, P, i32, P, sz, P]
         L.moe_layer_hidden.restype = C.c_int
+        i64, u = C.c_int64, P
+        sigs = {
+            "moe_mx4_quantize": [P, i32, i64, i32, i32, u, u, P],
+            "moe_mx4_dequantize": [u, u, i32, i32, i32, P, P],
+            "moe_mx4_matmul": [P, u, i32, i64, i32, u, u, i32, i32, P, i32, P],
+            "moe_mx4_matmul_backward": [P, i32, i64, i32, u, u, i32, i32, P, i32, P],
+            "moe_mx4_experts_matmul": [P, u, i32, i64, i32, i32, i32, i32, i32, P, P, u, u, i32, i32, P,
+                                       i32, P],
+            "moe_mx4_experts_matmul_backward": [P, i32, i64, i32, i32, i32, i32, i32, P, P, u, u, i32,
+                                                i32, P, i32, P, sz, P],
+            "moe_balance_loss": [P, i32, i64, i32, i32, i32, P, P, P, P, P, P, sz, P],
+            "moe_balance_loss_backward": [P, i32, i64, i32, i32, i32, P, P, P, P, P, P],
+        }
+        for name, args in sigs.items():
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = C.c_int
+        L.moe_mx4_experts_matmul_backward_workspace_size.argtypes = [i32] * 5
+        L.moe_mx4_experts_matmul_backward_workspace_size.restype = sz
+        L.moe_balance_loss_workspace_size.argtypes = [i32] * 3
+        L.moe_balance_loss_workspace_size.restype = sz
         L.moe_profile_begin.argtypes = [i32]
         L.moe_profile_begin.restype = C.c_int
         L.moe_profile_end.argtypes = []
@@ -201,6 +228,7 @@ class Grouping:
     offsets: torch.Tensor  # int32 [E+2]
     perm: torch.Tensor     # int32 [A]
     slot_of: torch.Tensor  # int32 [A]
+    has_shared: bool | None = None  # set by group() and route_group()
 
 
 def group(idx: torch.Tensor, E: int, has_shared: bool) -> Grouping:
@@ -220,6 +248,7 @@ def group(idx: torch.Tensor, E: int, has_shared: bool) -> Grouping:
                                         nbytes, _stream()))
     g.perm = g.perm[:A]
     g.slot_of = g.slot_of[:A]
+    g.has_shared = bool(has_shared)
     return g
 
 
@@ -242,6 +271,7 @@ def route_group(logits: torch.Tensor, k: int, has_shared: bool):
         _ptr(g.offsets), _ptr(g.perm), _ptr(g.slot_of), _ptr(ws), nbytes, _stream()))
     g.perm = g.perm[:A]
     g.slot_of = g.slot_of[:A]
+    g.has_shared = bool(has_shared)
     return idx, gates, g
 
 
@@ -454,5 +484,307 @@ def layer_static(logits: torch.Tensor, x: torch.Tensor, ex: "Experts", k: int, m
     return idx, gates, y
 
 
+# ---- microscaled 4-bit operands ---------------------------------------------------
+
+_FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Runs a library call on the current stream of the tensors' device."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != OK:
+        raise MoeError(name, st)
+
+
+def _rows(name: str, t: torch.Tensor, n: int | None = None):
+    """Checks rows of float values ([R, n], values adjacent): (type code, elements from row to row)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    code = _FLOATS.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    if t.dim() != 2 or (n is not None and t.shape[1] != n):
+        raise ValueError(f"{name} must be [rows, {'n' if n is None else n}]: got {tuple(t.shape)}")
+    R, m = t.shape
+    ld, inner = t.stride()
+    if R <= 1:
+        ld = m
+    if (inner != 1 and m > 1) or ld < m:
+        raise ValueError(f"{name} must have adjacent values in each row, and rows that do not overlap")
+    return code, ld
+
+
+def _int32(name: str, t: torch.Tensor, dev: torch.device, n: int | None = None):
+    _need_cuda(name, t, torch.int32)
+    if t.device != dev or (n is not None and t.numel() < n):
+        raise ValueError(f"{name} must be on {dev}" + (f" and hold {n} values" if n else ""))
+
+
+def _result(out, shape, dtype, dev: torch.device) -> torch.Tensor:
+    if dtype not in _FLOATS:
+        raise TypeError(f"results are float32 or bfloat16, not {dtype}")
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need_cuda("out", out, dtype)
+    if tuple(out.shape) != tuple(shape) or out.device != dev:
+        raise ValueError(f"out must be {tuple(shape)} on {dev}")
+    return out
+
+
+class Mx4:
+    """Rows of K values in microscaled 4-bit blocks: codes uint8 [..., 16 B], scales uint8 [..., B],
+    B = ceil(K / 32) blocks a row (the layout is in include/moe.h). [N, K] is a matrix or N rows of
+    activations, [E, N, K] one matrix for each expert."""
+
+    __slots__ = ("codes", "scales", "K")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int):
+        _need_cuda("codes", codes, torch.uint8)
+        _need_cuda("scales", scales, torch.uint8)
+        if K < 1 or codes.dim() < 2 or scales.shape[-1] != (K + 31) // 32 \
+                or codes.shape[-1] != 16 * scales.shape[-1] or codes.shape[:-1] != scales.shape[:-1]:
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold rows of {K}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales, self.K = codes, scales, K
+
+    @property
+    def shape(self) -> tuple:
+        return (*self.codes.shape[:-1], self.K)
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+
+def mx4_quantize(x: torch.Tensor, out: Mx4 | None = None) -> Mx4:
+    """Rows x ([..., K], float32 or bfloat16) as microscaled 4-bit blocks (moe_mx4_quantize). More than
+    two dimensions must be contiguous; of two, rows may lie further apart."""
+    if isinstance(x, torch.Tensor) and x.dim() > 2 and not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if not isinstance(x, torch.Tensor) or x.dim() < 2 or x.shape[-1] < 1:
+        raise ValueError("x must be a tensor [..., K] of two dimensions or more")
+    K = x.shape[-1]
+    flat = x if x.dim() == 2 else x.reshape(-1, K)
+    code, ld = _rows("x", flat)
+    if out is None:
+        B = (K + 31) // 32
+        out = Mx4(torch.empty((*x.shape[:-1], 16 * B), dtype=torch.uint8, device=x.device),
+                  torch.empty((*x.shape[:-1], B), dtype=torch.uint8, device=x.device), K)
+    elif out.shape != tuple(x.shape) or out.device != x.device:
+        raise ValueError(f"out must be an Mx4 of {tuple(x.shape)} on {x.device}")
+    _call("moe_mx4_quantize", x.device, flat.data_ptr(), code, ld, flat.shape[0], K, out.codes.data_ptr(),
+          out.scales.data_ptr())
+    return out
+
+
+def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of q, [..., K], in float32 or bfloat16 (exact in both)."""
+    y = _result(out, q.shape, dtype, q.device)
+    _call("moe_mx4_dequantize", q.device, q.codes.data_ptr(), q.scales.data_ptr(), q.codes.shape[:-1].numel(), q.K,
+          _FLOATS[dtype], y.data_ptr())
+    return y
+
+
+def _product_rows(x, K: int):
+    """A product's rows: (data, scales, type code, row distance, rows, device, result type)."""
+    if isinstance(x, Mx4):
+        if x.codes.dim() != 2 or x.K != K:
+            raise ValueError(f"x must be rows of {K} values: got {x.shape}")
+        return x.codes.data_ptr(), x.scales.data_ptr(), MX4, 0, x.codes.shape[0], x.device, torch.bfloat16
+    code, ld = _rows("x", x, K)
+    return x.data_ptr(), None, code, ld, x.shape[0], x.device, x.dtype
+
+
+def _matrix(w: Mx4, dims: int) -> int:
+    if not isinstance(w, Mx4) or w.codes.dim() != dims or w.codes.shape[-2] < 1:
+        raise ValueError(f"w must be an Mx4 of {dims} dimensions, with a row at least")
+    return w.codes.shape[-2]
+
+
+def _same(name: str, w: Mx4, dev: torch.device):
+    if w.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+
+
+def mx4_matmul(x, w: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """x W^T: [T, N] for rows x ([T, K]: float32, bfloat16, or an Mx4) and a matrix w ([N, K])
+    (moe_mx4_matmul). The result has x's type (an Mx4: bfloat16) unless `dtype` says otherwise."""
+    N = _matrix(w, 2)
+    p, s, code, ld, T, dev, own = _product_rows(x, w.K)
+    _same("w", w, dev)
+    y = _result(out, (T, N), dtype or own, dev)
+    _call("moe_mx4_matmul", dev, p, s, code, ld, T, w.codes.data_ptr(), w.scales.data_ptr(), N, w.K, y.data_ptr(),
+          _FLOATS[y.dtype])
+    return y
+
+
+def mx4_matmul_backward(dy: torch.Tensor, w: Mx4, dtype: torch.dtype | None = None,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of mx4_matmul for its rows: dy W, [T, K], for dy [T, N] (float32 or bfloat16; the
+    result has its type unless `dtype` says otherwise). w is not trained."""
+    N = _matrix(w, 2)
+    code, ld = _rows("dy", dy, N)
+    _same("w", w, dy.device)
+    dx = _result(out, (dy.shape[0], w.K), dtype or dy.dtype, dy.device)
+    _call("moe_mx4_matmul_backward", dy.device, dy.data_ptr(), code, ld, dy.shape[0], w.codes.data_ptr(),
+          w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dx.dtype])
+    return dx
+
+
+def _groups(grouping: Grouping, w: Mx4, tokens: int | None, dev: torch.device):
+    """(T, k, E, has_shared, A) of a grouping and the experts it is for. Without `tokens` every row of the
+    groups counts as a token of its own."""
+    E, A, n = grouping.counts.numel() - 1, grouping.perm.numel(), w.codes.shape[0]
+    if n not in (E, E + 1) or E < 1 or (grouping.has_shared is not None and grouping.has_shared != (n == E + 1)):
+        raise ValueError(f"w holds {n} experts, the grouping is for {E}"
+                         + (" and a shared one" if grouping.has_shared else ""))
+    _int32("grouping.offsets", grouping.offsets, dev, n + 1)
+    shared = n - E
+    if tokens is None:
+        # one assignment a row; the shared expert's group is one of the groups
+        return A, 1, n, 0, A
+    if tokens < 0 or (A % tokens if tokens else A) or (tokens and A // tokens - shared < 1):
+        raise ValueError(f"the grouping's {A} rows do not belong to {tokens} tokens")
+    return tokens, max(1, A // tokens - shared if tokens else 1), E, shared, A
+
+
+def mx4_experts_matmul(x, w: Mx4, grouping: Grouping, tokens: int | None = None, dtype: torch.dtype | None = None,
+                       out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows grouped by expert, each times its expert's matrix (moe_mx4_experts_matmul): [A, N] in the
+    groups' order. w: [E, N, K], or [E + 1, N, K] with the shared expert last. x ([.., K]: float32,
+    bfloat16, or an Mx4) holds the A rows in the groups' order, or, where `tokens` gives their number,
+    one row a token. Rows of `out` that are in no group are left as they were."""
+    N = _matrix(w, 3)
+    p, s, code, ld, R, dev, own = _product_rows(x, w.K)
+    _same("w", w, dev)
+    T, k, E, shared, A = _groups(grouping, w, tokens, dev)
+    if R != T:
+        raise ValueError(f"x has {R} rows, expected {T}")
+    gather = tokens is not None
+    if gather:
+        _int32("grouping.perm", grouping.perm, dev, A)
+    y = _result(out, (A, N), dtype or own, dev)
+    _call("moe_mx4_experts_matmul", dev, p, s, code, ld, T, k, E, shared, int(gather), grouping.offsets.data_ptr(),
+          grouping.perm.data_ptr() if gather else None, w.codes.data_ptr(), w.scales.data_ptr(), N, w.K, y.data_ptr(),
+          _FLOATS[y.dtype])
+    return y
+
+
+def mx4_experts_matmul_backward(dy: torch.Tensor, w: Mx4, grouping: Grouping, tokens: int | None = None,
+                                dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of mx4_experts_matmul for x: dy [A, N] in the groups' order -> [A, K], or, where
+    `tokens` gives their number, [tokens, K], the sum over each token's assignments. w is not trained."""
+    N = _matrix(w, 3)
+    code, ld = _rows("dy", dy, N)
+    dev = dy.device
+    _same("w", w, dev)
+    T, k, E, shared, A = _groups(grouping, w, tokens, dev)
+    if dy.shape[0] != A:
+        raise ValueError(f"dy has {dy.shape[0]} rows, expected {A}")
+    gather = tokens is not None
+    if gather:
+        _int32("grouping.slot_of", grouping.slot_of, dev, A)
+    dx = _result(out, (T, w.K), dtype or dy.dtype, dev)
+    n = lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, w.K, int(gather))
+    if workspace is None:
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    else:
+        _need_cuda("workspace", workspace, torch.uint8)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+    _call("moe_mx4_experts_matmul_backward", dev, dy.data_ptr(), code, ld, T, k, E, shared, int(gather),
+          grouping.offsets.data_ptr(), grouping.slot_of.data_ptr() if gather else None, w.codes.data_ptr(),
+          w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dx.dtype],
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+    return dx
+
+
+# ---- balance loss ---------------------------------------------------------------------
+
+
+@dataclass
+class BalanceLoss:
+    losses: torch.Tensor  # float32 [2]: balance loss, z loss
+    counts: torch.Tensor  # int32 [E]: assignments of the kept tokens to each expert
+    kept: torch.Tensor    # int32 [1]: how many tokens the mask keeps
+    k: int                # experts per token
+
+
+def _token_mask(mask: torch.Tensor | None, T: int, dev: torch.device):
+    if mask is None:
+        return None
+    _need_cuda("token_mask", mask, (torch.bool, torch.uint8))
+    if mask.numel() != T or mask.device != dev:
+        raise ValueError(f"token_mask must hold {T} values on {dev}")
+    return mask.data_ptr()
+
+
+def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, out: BalanceLoss | None = None) -> BalanceLoss:
+    """Per-expert counts, balance loss and z loss of a routed batch (moe_balance_loss): logits [T, E]
+    (float32 or bfloat16), idx int32 [T, k] as route_topk gives it, token_mask bool [T] (False: a token
+    that does not count, as padding)."""
+    code, ld = _rows("logits", logits)
+    T, E = logits.shape
+    dev = logits.device
+    _int32("idx", idx, dev)
+    if idx.dim() != 2 or idx.shape[0] != T:
+        raise ValueError(f"idx must be [{T}, k]: got {tuple(idx.shape)}")
+    k = idx.shape[1]
+    keep = _token_mask(token_mask, T, dev)
+    if out is None:
+        out = BalanceLoss(torch.empty(2, dtype=torch.float32, device=dev),
+                          torch.empty(E, dtype=torch.int32, device=dev),
+                          torch.empty(1, dtype=torch.int32, device=dev), k)
+    else:
+        _need_cuda("out.losses", out.losses, torch.float32)
+        _int32("out.counts", out.counts, dev)
+        _int32("out.kept", out.kept, dev)
+        if out.losses.numel() != 2 or out.counts.numel() != E or out.kept.numel() != 1 or out.losses.device != dev:
+            raise ValueError("out does not match the logits")
+        out.k = k
+    n = lib().moe_balance_loss_workspace_size(T, k, E)
+    if workspace is None:
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda("workspace", workspace, torch.uint8)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+    _call("moe_balance_loss", dev, logits.data_ptr(), code, ld, T, E, k, idx.data_ptr(), keep, out.losses.data_ptr(),
+          out.counts.data_ptr(), out.kept.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def balance_loss_backward(logits: torch.Tensor, loss: BalanceLoss, d_losses: torch.Tensor,
+                          token_mask: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of balance_loss for the logits, [T, E] in their type, from the gradients d_losses
+    (float32 [2], on the device) of its two losses; `loss` and `token_mask` as the forward call had them."""
+    code, ld = _rows("logits", logits)
+    T, E = logits.shape
+    dev = logits.device
+    _need_cuda("d_losses", d_losses, torch.float32)
+    if d_losses.numel() != 2 or d_losses.device != dev:
+        raise ValueError(f"d_losses must hold 2 values on {dev}")
+    _int32("loss.counts", loss.counts, dev)
+    _int32("loss.kept", loss.kept, dev, 1)
+    if loss.counts.numel() != E:
+        raise ValueError(f"loss is for {loss.counts.numel()} experts, the logits for {E}")
+    keep = _token_mask(token_mask, T, dev)
+    d = _result(out, (T, E), logits.dtype, dev)
+    _call("moe_balance_loss_backward", dev, logits.data_ptr(), code, ld, T, E, loss.k, keep, loss.counts.data_ptr(),
+          loss.kept.data_ptr(), d_losses.data_ptr(), d.data_ptr())
+    return d
+
+
 __all__ = ["layer", "layer_static", "profile_begin", "profile_end", "router_logits", "route_topk", "route_group", "group", "Grouping", "Experts", "ffn_q", "lib", "status_string",
-           "MoeError", "Q2", "Q3", "F32", "BF16", "FAST", "CHECK_F32", "MAX_E", "LIB_PATH"]
+           "MoeError", "Q2", "Q3", "F32", "BF16", "FAST", "CHECK_F32", "MAX_E", "LIB_PATH",
+           "MX4", "Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_matmul_backward",
+           "mx4_experts_matmul", "mx4_experts_matmul_backward", "BalanceLoss", "balance_loss",
+           "balance_loss_backward"]

@@ -1,0 +1,229 @@
+// Products of few rows with a microscaled matrix: y[s][n] = sum_k x[row(s)][k]
+// W[e(s)][n][k], and the gradient dx[s][k] = sum_n dy[s][n] W[e(s)][n][k].
+//
+// Up to 16 rows of one group and a strip of the matrix per workgroup, on
+// 16x16 matrix-core tiles. Weights go from memory to registers, where they
+// become bf16 exactly; float32 rows enter as three exact bf16 parts, so that
+// every product is exact and only the float32 sums round. Bound by the
+// matrix's bytes: each is read once per 16 rows.
+#include "mx4.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRows = 16;   // rows of a group per workgroup
+constexpr int kStrip = 16;  // matrix rows per workgroup (forward)
+constexpr int kCols = 128;  // matrix columns per workgroup (gradient)
+
+// The group and rows of this workgroup: block x takes rows 16 x .. of the one
+// matrix; with groups, block x works if row x is the first of a 16 of its group.
+struct Unit {
+  int e, s0, M;
+};
+__device__ inline Unit unit_of(const Mx4Args& a) {
+  Unit u;
+  if (!a.offsets) {
+    u.e = 0;
+    u.s0 = blockIdx.x * kRows;
+    u.M = min(kRows, a.A - u.s0);
+    return u;
+  }
+  u.s0 = blockIdx.x;
+  u.e = mx4_group_of(a.offsets, a.E_tot, u.s0);
+  u.M = 0;
+  if (u.e < a.E_tot) {
+    const int first = u.e ? a.offsets[u.e] : max(a.offsets[0], 0);
+    if (u.s0 >= first && (u.s0 - first) % kRows == 0)
+      u.M = min(kRows, min(a.offsets[u.e + 1], a.A) - u.s0);
+  }
+  return u;
+}
+
+__device__ inline void store_out(const Mx4Args& a, size_t i, float v) {
+  if (a.ydtype == 1) static_cast<uint16_t*>(a.y)[i] = (uint16_t)f32_to_bf16_bits(v);
+  else static_cast<float*>(a.y)[i] = v;
+}
+
+// Four waves share K in chunks of 128: lane (r, g) holds block g of a chunk of
+// matrix row r (its 16 bytes of codes, one scale) and of x's row r. A product
+// step takes eight values of each of the four blocks; the order of K within a
+// chunk is the same for both operands, which is all that matters. Microscaled
+// rows go through the 4-bit matrix cores, one product a chunk.
+template <int XT>
+__global__ __launch_bounds__(256) void rows_forward(Mx4Args a, bool vec) {
+  __shared__ float part[4][kRows * kStrip];
+  const Unit u = unit_of(a);
+  if (u.M <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int nb = mx4_blocks(a.K), n0 = blockIdx.y * kStrip;
+  const size_t wrow = (size_t)u.e * a.N + min(n0 + r, a.N - 1);
+  const uint4* wc = reinterpret_cast<const uint4*>(a.wc) + wrow * nb;
+  const uint8_t* ws = a.ws + wrow * nb;
+  const int xr = r < u.M ? mx4_row(a, u.s0 + r) : -1;
+  floatx4_t acc = {};
+  for (int b0 = 4 * wave; b0 < nb; b0 += 16) {
+    const int b = b0 + g;
+    uint4 c = make_uint4(0, 0, 0, 0);
+    uint32_t sw = 0;
+    if (b < nb) {
+      c = wc[b];
+      sw = ws[b];
+    }
+    if constexpr (XT == kMx4) {
+      uint4 xc = make_uint4(0, 0, 0, 0);
+      uint32_t sx = 0;
+      if (b < nb && xr >= 0) {
+        xc = reinterpret_cast<const uint4*>(a.x)[(size_t)xr * nb + b];
+        sx = a.xs[(size_t)xr * nb + b];
+      }
+      int8v_t A = {}, B = {};
+      A[0] = c.x; A[1] = c.y; A[2] = c.z; A[3] = c.w;
+      B[0] = xc.x; B[1] = xc.y; B[2] = xc.z; B[3] = xc.w;
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, 0, (int)sw, 0, (int)sx);
+    } else {
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+      const float sc = mx4_scale(sw);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8_t wf = mx4_frag(w[i], sc);
+        const int k = 32 * b + 8 * i;
+        if constexpr (XT == 1) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (xr >= 0 && k < a.K) v = load8_bf16(static_cast<const uint16_t*>(a.x) + xr * a.ldx, k, a.K, vec);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, v), acc, 0, 0, 0);
+        } else {
+          float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (xr >= 0 && k < a.K) load8_f32(static_cast<const float*>(a.x) + xr * a.ldx, k, a.K, vec, f);
+          uint4 h, m, l;
+          split3x8(f, h, m, l);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, l), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, m), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, h), acc, 0, 0, 0);
+        }
+      }
+    }
+  }
+  // acc[i]: matrix row 4 g + i, x's row r
+#pragma unroll
+  for (int i = 0; i < 4; ++i) part[wave][r * kStrip + 4 * g + i] = acc[i];
+  __syncthreads();
+  const int m = tid / kStrip, n = n0 + tid % kStrip;
+  if (m < u.M && n < a.N)
+    store_out(a, (size_t)(u.s0 + m) * a.N + n, (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]));
+}
+
+// Four waves share N in steps of 32. Lane (r, g) holds, for each of the eight
+// matrix rows n = 8 g + j of a step, one dword of codes: columns k0 + 8 r ..
+// + 7. Converted row by row (one scale each) the values pair up along k; two
+// rows' pairs are then regrouped along n, so that eight conversions' worth of
+// registers give the operands of eight 16x16x32 products, product c covering
+// columns k0 + 8 r + c. No transposed copy of the matrix is needed.
+template <int DT>
+__global__ __launch_bounds__(256) void rows_gradient(Mx4Args a, bool vec) {
+  __shared__ float part[4][kRows * kCols];
+  const Unit u = unit_of(a);
+  if (u.M <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
+  const int nb = mx4_blocks(a.K), k0 = blockIdx.y * kCols;
+  const int kc = k0 + 8 * r;
+  const bool inside = kc < 32 * nb;
+  const size_t row0 = (size_t)u.e * a.N;
+  const int xr = r < u.M ? mx4_row(a, u.s0 + r) : -1;
+  floatx4_t acc[8] = {};
+  for (int n0 = 32 * wave; n0 < a.N; n0 += 128) {
+    uint32_t p[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int n = n0 + 8 * g + j;
+      uint32_t w = 0, sw = 0;
+      if (inside && n < a.N) {
+        w = reinterpret_cast<const uint32_t*>(a.wc)[(row0 + n) * nb * 4 + kc / 8];
+        sw = a.ws[(row0 + n) * nb + kc / 32];
+      }
+      const float sc = mx4_scale(sw);
+      p[j][0] = mx4_pair<0>(w, sc);
+      p[j][1] = mx4_pair<1>(w, sc);
+      p[j][2] = mx4_pair<2>(w, sc);
+      p[j][3] = mx4_pair<3>(w, sc);
+    }
+    const int n = n0 + 8 * g;
+    uint4 d[3];
+    if constexpr (DT == 1) {
+      d[0] = make_uint4(0, 0, 0, 0);
+      if (xr >= 0 && n < a.N) d[0] = load8_bf16(static_cast<const uint16_t*>(a.x) + xr * a.ldx, n, a.N, vec);
+    } else {
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (xr >= 0 && n < a.N) load8_f32(static_cast<const float*>(a.x) + xr * a.ldx, n, a.N, vec, f);
+      split3x8(f, d[0], d[1], d[2]);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      auto two = [&](int j) {
+        return c & 1 ? hi_pair(p[j][c / 2], p[j + 1][c / 2]) : lo_pair(p[j][c / 2], p[j + 1][c / 2]);
+      };
+      const bf16x8_t wf = __builtin_bit_cast(bf16x8_t, make_uint4(two(0), two(2), two(4), two(6)));
+#pragma unroll
+      for (int q = DT == 1 ? 0 : 2; q >= 0; --q)
+        acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, d[q]), wf, acc[c], 0, 0, 0);
+    }
+  }
+  // acc[c][i]: row 4 g + i, column k0 + 8 r + c
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[wave][(4 * g + i) * kCols + 8 * r + c] = acc[c][i];
+  __syncthreads();
+  for (int i = tid; i < u.M * kCols; i += 256) {
+    const int k = k0 + i % kCols;
+    if (k < a.K)
+      store_out(a, (size_t)(u.s0 + i / kCols) * a.K + k, (part[0][i] + part[1][i]) + (part[2][i] + part[3][i]));
+  }
+}
+
+// dx[t] = the sum of a token's rows of part, in the order of its assignments
+// (the shared expert's last); float32 sums, one rounding.
+template <bool BF>
+__global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part, const int32_t* __restrict__ slot_of,
+                                                  int T, int k, int has_shared, int A, int K, void* __restrict__ y) {
+  const int t = blockIdx.x;
+  for (int c = blockIdx.y * 256 + threadIdx.x; c < K; c += gridDim.y * 256) {
+    float v = 0.f;
+    for (int j = 0; j < k + has_shared; ++j) {
+      const int s = slot_of[j < k ? (size_t)t * k + j : (size_t)T * k + t];
+      if ((unsigned)s < (unsigned)A) v += part[(size_t)s * K + c];
+    }
+    if (BF) static_cast<uint16_t*>(y)[(size_t)t * K + c] = (uint16_t)f32_to_bf16_bits(v);
+    else static_cast<float*>(y)[(size_t)t * K + c] = v;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
+  const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.N + kStrip - 1) / kStrip);
+  const bool vec = a.xdtype != kMx4 && rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
+  if (a.xdtype == kMx4) MOE_LAUNCH("mx4_rows", s, rows_forward<kMx4>, g, dim3(256), 0, s, a, vec);
+  else if (a.xdtype == 1) MOE_LAUNCH("mx4_rows", s, rows_forward<1>, g, dim3(256), 0, s, a, vec);
+  else MOE_LAUNCH("mx4_rows", s, rows_forward<0>, g, dim3(256), 0, s, a, vec);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
+  const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.K + kCols - 1) / kCols);
+  const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
+  if (a.xdtype == 1) MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<1>, g, dim3(256), 0, s, a, vec);
+  else MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<0>, g, dim3(256), 0, s, a, vec);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, int T, int k, int has_shared, int A,
+                                 int K, void* y, int ydtype, hipStream_t s) {
+  const dim3 g(T, (K + 1023) / 1024);
+  if (ydtype == 1)
+    MOE_LAUNCH("mx4_sum_tokens", s, sum_tokens<true>, g, dim3(256), 0, s, part, slot_of, T, k, has_shared, A, K, y);
+  else
+    MOE_LAUNCH("mx4_sum_tokens", s, sum_tokens<false>, g, dim3(256), 0, s, part, slot_of, T, k, has_shared, A, K, y);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -48,6 +48,7 @@ extern "C" {
 /* ---- enums -------------------------------------------------------------- */
 #define MOE_F32 0  /* activations x and output y are float32               */
 #define MOE_BF16 1 /* activations x and output y are bfloat16 (uint16 bits) */
+#define MOE_MX4 4  /* rows of microscaled 4-bit blocks (moe_mx4_* calls only)  */
 
 #define MOE_Q2 2 /* 2-bit codes, w = d*q + m, q in 0..3, 32-weight blocks */
 #define MOE_Q3 3 /* 3-bit codes, w = d*q + m, q in 0..7, 32-weight blocks */
@@ -333,6 +334,130 @@ size_t moe_expert_gateup_fp8_workspace_size(const moe_experts *ex, int32_t T);
  * E4M3 operands. Other errors as moe_ffn_q. */
 int moe_expert_gateup_fp8(const void *x, int32_t T, const moe_experts *ex, int32_t expert, float *h,
                           void *ws, size_t ws_bytes, void *stream);
+
+/* ---- microscaled 4-bit operands ------------------------------------------- */
+
+/* A matrix of R rows of K values as microscaled 4-bit blocks, B = ceil(K / 32)
+ * blocks a row, each 32 consecutive values of it (the last may hold fewer):
+ *   codes : [R][B][16] bytes. Value j (0..31) of a block is in byte j/2, at bits
+ *           4*(j%2); bit 3 of its code is the sign, bits 0..2 pick the magnitude
+ *           0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   scales: [R][B] bytes. Byte s stands for 2^(s - 127); the value is the signed
+ *           magnitude times that. s = 255: every value of the block is NaN.
+ * Codes past K in a row's last block are zero. codes is 16-byte aligned. */
+
+/* Quantises x ([rows][K], MOE_F32 or MOE_BF16, ld elements from row to row,
+ * ld >= K). The scale of a block is the power of two that brings its largest
+ * magnitude into [4, 8): byte floor(log2 max) - 2 + 127, at least 0 (also for a
+ * block of zeros). Magnitudes over the scale go to the nearest of the eight,
+ * ties to the even code, past 6 to 6; zeros keep their sign. A block that holds
+ * a NaN or an infinity becomes NaN (byte 255, codes 0). rows == 0: no launch. */
+int moe_mx4_quantize(const void *x, int32_t xdtype, int64_t ld, int32_t rows, int32_t K,
+                     uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values that codes and scales stand for: y [rows][K], MOE_F32 or MOE_BF16,
+ * both exact (magnitudes from 2^128 on are infinite). */
+int moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t K,
+                       int32_t ydtype, void *y, void *stream);
+
+/* y[t][n] = sum_k x[t][k] * W[n][k] for T rows and one microscaled matrix W of
+ * N rows of K values.
+ *   x  : [T][K], MOE_F32 or MOE_BF16, ldx elements from row to row (>= K), or
+ *        MOE_MX4: codes, with their scales in x_scales (ldx is not used).
+ *        x_scales is NULL for the other types.
+ *   y  : [T][N], MOE_F32 or MOE_BF16.
+ * Every product is exact (float32 x enters the matrix cores as three bf16
+ * parts); sums are float32 in a fixed order, with one rounding to y's type. So
+ * results are reproducible run to run. T == 0: no launch. */
+int moe_mx4_matmul(const void *x, const uint8_t *x_scales, int32_t xdtype, int64_t ldx, int32_t T,
+                   const uint8_t *w_codes, const uint8_t *w_scales, int32_t N, int32_t K, void *y,
+                   int32_t ydtype, void *stream);
+
+/* The gradient of moe_mx4_matmul for its rows: dx[t][k] = sum_n dy[t][n] *
+ * W[n][k]. dy: [T][N], MOE_F32 or MOE_BF16, ldd elements from row to row (>= N);
+ * dx: [T][K], MOE_F32 or MOE_BF16. The matrix is not trained: it has no
+ * gradient. */
+int moe_mx4_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t T,
+                            const uint8_t *w_codes, const uint8_t *w_scales, int32_t N, int32_t K,
+                            void *dx, int32_t dxdtype, void *stream);
+
+/* The same products for rows grouped by expert (moe_group, moe_route_group):
+ * row s of [offsets[e], offsets[e+1]) is multiplied by matrix e of the E_tot =
+ * E + has_shared matrices (w_codes [E_tot][N][B][16], w_scales [E_tot][N][B];
+ * the shared expert's last). A = T*(k + has_shared) rows.
+ *   gather == 0: x holds the A rows in the groups' order.
+ *   gather == 1: x holds T rows, one a token; row s of the groups is the row of
+ *                the token of assignment perm[s].
+ *   y     : [A][N] in the groups' order. Rows that are in no group (from
+ *           offsets[E_tot] on) are left as they were.
+ * E_tot is at most MOE_MAX_E + 1, A at most 2^23, N and K at most 2^19.
+ * offsets: [E_tot + 1] (moe_group writes one more), perm: [A]; perm may be NULL
+ * when gather == 0. Values of perm outside [0, A) are not detected; the kernels
+ * stay in bounds and take a row of zeros for them, and offsets are cut to
+ * [0, A]. Types and rounding as moe_mx4_matmul. */
+int moe_mx4_experts_matmul(const void *x, const uint8_t *x_scales, int32_t xdtype, int64_t ldx,
+                           int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t gather,
+                           const int32_t *offsets, const int32_t *perm, const uint8_t *w_codes,
+                           const uint8_t *w_scales, int32_t N, int32_t K, void *y, int32_t ydtype,
+                           void *stream);
+
+/* Workspace bytes moe_mx4_experts_matmul_backward needs (0 unless gather). */
+size_t moe_mx4_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int32_t has_shared,
+                                                      int32_t K, int32_t gather);
+
+/* The gradient of moe_mx4_experts_matmul for its rows. dy: [A][N] in the
+ * groups' order, ldd elements from row to row.
+ *   gather == 0: dx [A][K]; rows in no group are left as they were.
+ *   gather == 1: dx [T][K]; the sum over the token's assignments, in the order
+ *                j = 0 .. k-1, then the shared expert's, kept in float32 in ws
+ *                ([A][K]) and rounded once. slot_of: [A] as moe_group writes it
+ *                (else it may be NULL); values outside [0, A) add nothing.
+ * ws: at least ..._workspace_size bytes (any content). */
+int moe_mx4_experts_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t T, int32_t k,
+                                    int32_t E, int32_t has_shared, int32_t gather,
+                                    const int32_t *offsets, const int32_t *slot_of,
+                                    const uint8_t *w_codes, const uint8_t *w_scales, int32_t N,
+                                    int32_t K, void *dx, int32_t dxdtype, void *ws, size_t ws_bytes,
+                                    void *stream);
+
+/* ---- balance loss ------------------------------------------------------------ */
+
+/* Workspace bytes moe_balance_loss needs (device memory, any content). */
+size_t moe_balance_loss_workspace_size(int32_t T, int32_t k, int32_t E);
+
+/* Per-expert counts of a routed batch, and the two losses that keep a router in
+ * shape. Over the n tokens that `mask` keeps (mask [T] bytes, 0 = left out;
+ * NULL: all T), p[t] the softmax of the token's E logits, lse[t] the logarithm
+ * of the sum of their exponentials:
+ *   counts[e] = entries of idx[t][0..k-1] equal to e, over the kept tokens
+ *               (entries outside [0, E) count nowhere)
+ *   kept[0]   = n
+ *   losses[0] = E * sum_e (counts[e] / (n k)) * (sum_t p[t][e] / n)   (balance)
+ *   losses[1] = sum_t lse[t]^2 / n                                    (z)
+ * n == 0: both are 0. A token whose logits are all -inf has no distribution: its
+ * p and lse count as 0. NaN and +inf logits of a kept token make the losses
+ * NaN; those of a token left out are not looked at.
+ * logits: [T][E], MOE_F32 or MOE_BF16, ld elements from row to row (>= E); idx:
+ * [T][k] int32 (moe_route_topk); counts: [E] int32; kept: [1] int32; losses: [2]
+ * float32. Sums are float32 in a fixed order: reproducible run to run.
+ * Requires 1 <= E <= MOE_MAX_E, k >= 1; T == 0 writes n = 0 and zeros.
+ * ws: at least moe_balance_loss_workspace_size bytes, any content; calls that
+ * overlap in time must not share it. */
+int moe_balance_loss(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E, int32_t k,
+                     const int32_t *idx, const uint8_t *mask, float *losses, int32_t *counts,
+                     int32_t *kept, void *ws, size_t ws_bytes, void *stream);
+
+/* The gradient for the logits: dlogits [T][E] (type and rows as `dtype`, rows E
+ * elements apart), from counts and kept as moe_balance_loss wrote them and the
+ * gradients d_losses [2] (float32, device) of the two losses:
+ *   dlogits[t][e] = p[t][e] * (d_losses[0] * E / n * (f[e] - sum_j f[j] p[t][j])
+ *                              + d_losses[1] * 2 * lse[t] / n),
+ * f[e] = counts[e] / (n k) (counts depend on idx alone and pass no gradient).
+ * Rows of tokens that mask leaves out are 0. T == 0: no launch. */
+int moe_balance_loss_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
+                              int32_t k, const uint8_t *mask, const int32_t *counts,
+                              const int32_t *kept, const float *d_losses, void *dlogits,
+                              void *stream);
 
 /* ---- whole layer without allocation --------------------------------------- */
 

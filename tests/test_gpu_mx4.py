@@ -1,0 +1,383 @@
+"""Microscaled 4-bit quantisation and products on the GPU against float64.
+
+Quantisation is exact: codes and scales equal the reference's. A product's terms are exact (a weight has two
+significant bits, a bfloat16 row eight, a float32 row enters in three exact parts), so its error is that of a float32
+sum of n terms in some order, at most (n + 2) 2^-24 sum |x w| (n = 3 K or 3 N terms for float32 rows, plus the rows
+that a token's gradient adds up), and of one rounding to the result's type, half a step (finfo.eps / 2).
+"""
+import numpy as np
+import pytest
+
+import mx4_ref
+from gpu_util import log, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def types():
+    torch = torch_cuda()
+    return {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def as64(t) -> np.ndarray:
+    return t.double().cpu().numpy()
+
+
+def check(name, got, ref, size, terms):
+    torch = torch_cuda()
+    half = torch.finfo(got.dtype).eps / 2
+    g = as64(got)
+    sums = (terms + 2) * 2.0 ** -24 * size
+    bound = sums + half * (np.abs(ref) + sums) + 1e-37
+    assert g.shape == ref.shape and np.isfinite(g).all(), name
+    worst = np.max(np.abs(g - ref) / bound, initial=0.0)
+    log(f"[mx4] {name}: error / bound {worst:.3f}")
+    assert worst <= 1, name
+
+
+def random_matrix(rng, shape, K, lo=110, hi=131):
+    """Random codes (zeros past K) and scales: an Mx4 and its values."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    B = -(-K // 32)
+    codes = rng.integers(0, 256, (*shape, 16 * B), dtype=np.uint8)
+    if K % 32:
+        n = np.arange(32 * B).reshape(-1, 2)
+        codes &= ((n[:, 0] < K) * 15 + (n[:, 1] < K) * 240).astype(np.uint8)
+    scales = rng.integers(lo, hi, (*shape, B), dtype=np.uint8)
+    return moe.Mx4(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), K), mx4_ref.values(codes, scales, K)
+
+
+def random_rows(rng, R, n, kind, strided=False):
+    """An operand of R rows and its values."""
+    torch = torch_cuda()
+    if kind == "mx4":
+        return random_matrix(rng, (R,), n)
+    v = torch.from_numpy(rng.standard_normal((R, n + 24 if strided else n)) * np.exp(rng.standard_normal((R, 1))))
+    t = v.to(types()[kind]).cuda()
+    t = t[:, 8:8 + n] if strided else t
+    return t, as64(t)
+
+
+def grouping_of(rng, T, k, E, shared, skew=0.0, quiet=0):
+    """A grouping by the framework; `quiet` experts get nothing."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    logits = rng.standard_normal((T, E)) - skew * np.log(1 + np.arange(E))
+    if quiet:
+        logits[:, rng.permutation(E)[:quiet]] -= 100
+    idx, _ = moe.route_topk(torch.from_numpy(logits.astype(np.float32)).cuda(), k)
+    return moe.group(idx, E, shared)
+
+
+# ---- quantisation ---------------------------------------------------------------------
+
+
+def nasty(rng, rows, K):
+    v = rng.standard_normal((rows, K)) * np.exp(4 * rng.standard_normal((rows, 1)))
+    v = v.astype(np.float32)
+    flat = v.reshape(-1)
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6, 7, 7.999, 4, -0.25, -0.75, -5, 0.0, -0.0], np.float32)
+    flat[: min(flat.size, 16)] = ties[: min(flat.size, 16)]
+    for i, s in enumerate((2.0 ** -126, 2.0 ** -149, 3e38, 1e-38, 0.0, 2.0 ** -124)):
+        if i < rows - 1:
+            v[i + 1] = (rng.standard_normal(K) * s).clip(-3.4e38, 3.4e38).astype(np.float32)
+    if rows > 8:
+        v[8, 0], v[7, K - 1], v[8, K // 2] = np.nan, np.inf, -np.inf
+    return v
+
+
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 32), (3, 31), (9, 33), (17, 100), (33, 256), (70, 1000), (2, 4096)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_quantize_is_exact(rows, K, kind):
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    x = torch.from_numpy(nasty(np.random.default_rng(rows * K), rows, K)).to(types()[kind])
+    codes, scales = mx4_ref.quantize(x.float().numpy())
+    wide = torch.zeros((rows, K + 9), dtype=x.dtype).cuda()
+    wide[:, 5:5 + K] = x.cuda()
+    for name, t in (("adjacent", x.cuda()), ("strided", wide[:, 5:5 + K])):
+        q = moe.mx4_quantize(t)
+        assert np.array_equal(q.scales.cpu().numpy(), scales), name
+        assert np.array_equal(q.codes.cpu().numpy(), codes), name
+    want = mx4_ref.values(codes, scales, K)
+    for dt in types().values():
+        got = moe.mx4_dequantize(q, dt)
+        assert got.dtype == dt and np.array_equal(as64(got), want, equal_nan=True)
+
+
+def test_dequantize_every_code_and_scale():
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    codes = np.tile(np.arange(16, dtype=np.uint8) * 17, (256, 1))
+    scales = np.arange(256, dtype=np.uint8)[:, None]
+    q = moe.Mx4(torch.from_numpy(codes).cuda(), torch.from_numpy(scales.copy()).cuda(), 32)
+    with np.errstate(over="ignore"):
+        want = mx4_ref.values(codes, scales, 32).astype(np.float32).astype(np.float64)
+    for dt in types().values():
+        assert np.array_equal(as64(moe.mx4_dequantize(q, dt)), want, equal_nan=True)
+
+
+def test_quantize_three_dimensions_and_out():
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    x = torch.randn(3, 5, 70, device="cuda")
+    q = moe.mx4_quantize(x)
+    assert q.shape == (3, 5, 70) and q.codes.shape == (3, 5, 48) and q.scales.shape == (3, 5, 3)
+    again = moe.mx4_quantize(2 * x, out=moe.Mx4(torch.empty_like(q.codes), torch.empty_like(q.scales), 70))
+    assert torch.equal(again.codes, q.codes) and torch.equal(again.scales, q.scales + 1)
+    assert moe.mx4_quantize(x[:, :0].contiguous()).shape == (3, 0, 70)
+
+
+# ---- one matrix -----------------------------------------------------------------------
+
+SIZES = [(1, 1, 1), (1, 1024, 2048), (3, 17, 33), (4, 256, 96), (16, 130, 64), (17, 500, 1000), (33, 64, 2048),
+         (65, 48, 160), (100, 1000, 31), (130, 257, 544), (300, 384, 512)]
+
+
+@pytest.mark.parametrize("T,N,K", SIZES)
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx4"])
+def test_matmul(T, N, K, kind):
+    torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T * N + K)
+    w, wv = random_matrix(rng, (N,), K)
+    for strided in (False, True)[: 1 if kind == "mx4" else 2]:
+        x, xv = random_rows(rng, T, K, kind, strided)
+        ref, size = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+        for dt in types().values():
+            y = moe.mx4_matmul(x, w, dtype=dt)
+            assert y.dtype == dt
+            check(f"{kind} {T}x{N}x{K} strided={strided} -> {dt}", y, ref, size, K * (3 if kind == "f32" else 1))
+
+
+@pytest.mark.parametrize("T,N,K", SIZES)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_matmul_backward(T, N, K, kind):
+    torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + N * K)
+    w, wv = random_matrix(rng, (N,), K)
+    for strided in (False, True):
+        d, dv = random_rows(rng, T, N, kind, strided)
+        ref, size = dv @ wv, np.abs(dv) @ np.abs(wv)
+        for dt in types().values():
+            check(f"gradient {kind} {T}x{N}x{K} strided={strided} -> {dt}", moe.mx4_matmul_backward(d, w, dtype=dt), ref,
+                  size, N * (3 if kind == "f32" else 1))
+
+
+def test_gradient_against_differences():
+    """The product is linear in x, so a difference quotient is exact up to its own roundings: with x, h and the
+    weights small integers over powers of two every sum here is exact in float32, and so both sides are equal."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(5)
+    T, N, K = 5, 40, 70
+    w, _ = random_matrix(rng, (N,), K, lo=127, hi=128)
+    x = torch.from_numpy(rng.integers(-8, 9, (T, K))).float().cuda()
+    d = torch.from_numpy(rng.integers(-8, 9, (T, N))).float().cuda()
+    g = moe.mx4_matmul_backward(d, w)
+    for k in range(0, K, 7):
+        h = torch.zeros_like(x)
+        h[:, k] = 2
+        quotient = ((moe.mx4_matmul(x + h, w) - moe.mx4_matmul(x - h, w)) * d).sum(1) / 4
+        assert torch.equal(quotient, g[:, k])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx4"])
+def test_special_values(kind):
+    """NaN blocks reach their own outputs alone; infinities and huge, tiny and subnormal rows keep their class."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(11)
+    T, N, K = 20, 40, 128
+    w, wv = random_matrix(rng, (N,), K, 120, 126)
+    w.scales[7, 2] = 255
+    x, xv = random_rows(rng, T, K, kind)
+    if kind == "mx4":
+        x.scales[3, 1] = 255
+        x.scales[5], xv[5] = 0, xv[5] * 2.0 ** (-x.scales[5].cpu().numpy().astype(float)).repeat(32)
+    else:
+        x[3, 40] = float("nan")
+        x[4, 9] = float("inf")
+        x[5] *= 2.0 ** -120
+        x[6] *= 2.0 ** 100
+        xv = as64(x)
+    y = as64(moe.mx4_matmul(x, w, dtype=torch.float32))
+    assert np.isnan(y[3]).all() and np.isnan(y[:, 7]).all()
+    rest = np.delete(np.arange(N), 7)
+    if kind != "mx4":
+        bad = y[4][rest]
+        assert not np.isfinite(bad[wv[rest, 9] != 0]).any() and np.isnan(bad[wv[rest, 9] == 0]).all()
+    rows = np.delete(np.arange(T), [3, 4] if kind != "mx4" else [3])
+    ref, size = xv[rows] @ wv[rest].T, np.abs(xv[rows]) @ np.abs(wv[rest]).T
+    err = np.abs(y[np.ix_(rows, rest)] - ref) / ((3 * K + 3) * 2.0 ** -24 * size + 2.0 ** -148)
+    assert err.max() <= 1, err.max()
+    if kind != "mx4":
+        d, dv = random_rows(rng, T, N, kind)
+        d[:, 7] = 0
+        d[2, 3] = float("nan")
+        g = as64(moe.mx4_matmul_backward(d, w, dtype=torch.float32))
+        assert np.isnan(g[2]).all() and np.isnan(g[:, 64:96]).all()   # 0 times NaN is NaN
+        assert np.isfinite(np.delete(g, 2, 0)[:, :64]).all() and np.isfinite(np.delete(g, 2, 0)[:, 96:]).all()
+
+
+def test_results_repeat_and_leave_the_rest_alone():
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(3)
+    for T, N, K in ((5, 70, 300), (200, 300, 256)):
+        w, _ = random_matrix(rng, (N,), K)
+        x, _ = random_rows(rng, T, K, "bf16")
+        room = torch.full((T + 2, N), 7.0, device="cuda", dtype=torch.bfloat16)
+        y = moe.mx4_matmul(x, w, out=room[1:-1])
+        assert (room[0] == 7).all() and (room[-1] == 7).all()
+        for _ in range(3):
+            assert torch.equal(moe.mx4_matmul(x, w), y)
+        d, _ = random_rows(rng, T, N, "f32")
+        g = moe.mx4_matmul_backward(d, w)
+        for _ in range(3):
+            assert torch.equal(moe.mx4_matmul_backward(d, w), g)
+    assert moe.mx4_matmul(x[:0], w).shape == (0, N) and moe.mx4_matmul_backward(d[:0], w).shape == (0, K)
+
+
+# ---- experts --------------------------------------------------------------------------
+
+GROUPS = [  # T, k, E, shared, N, K, skew, experts that get nothing
+    (1, 1, 1, False, 16, 32, 0, 0), (1, 2, 8, True, 40, 70, 0, 3), (4, 10, 64, True, 128, 256, 1, 20),
+    (37, 3, 5, False, 100, 96, 1, 1), (64, 8, 300, True, 64, 64, 1, 100), (130, 2, 4, True, 272, 160, 1, 1),
+    (300, 4, 16, False, 130, 288, 0.5, 4), (1500, 2, 6, True, 64, 128, 2, 2)]
+
+
+@pytest.mark.parametrize("T,k,E,shared,N,K,skew,quiet", GROUPS)
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx4"])
+def test_experts_matmul(T, k, E, shared, N, K, skew, quiet, kind):
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T * k + N)
+    g = grouping_of(rng, T, k, E, shared, skew, quiet)
+    off, perm, A = g.offsets.cpu().numpy(), g.perm.cpu().numpy(), T * (k + shared)
+    w, wv = random_matrix(rng, (E + shared, N), K)
+    terms = K * (3 if kind == "f32" else 1)
+    x, xv = random_rows(rng, T, K, kind)
+    ref, size = mx4_ref.grouped(xv[mx4_ref.token_rows(perm, T, k)], wv, off)
+    y = moe.mx4_experts_matmul(x, w, g, tokens=T)
+    check(f"experts {kind} T={T} by token", y, ref, size, terms)
+    assert torch.equal(moe.mx4_experts_matmul(x, w, g, tokens=T), y)
+    x, xv = random_rows(rng, A, K, kind)
+    ref, size = mx4_ref.grouped(xv, wv, off)
+    for dt in types().values():
+        check(f"experts {kind} T={T} in order -> {dt}", moe.mx4_experts_matmul(x, w, g, dtype=dt), ref, size, terms)
+
+
+@pytest.mark.parametrize("T,k,E,shared,N,K,skew,quiet", GROUPS)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_experts_matmul_backward(T, k, E, shared, N, K, skew, quiet, kind):
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T * k + K)
+    g = grouping_of(rng, T, k, E, shared, skew, quiet)
+    off, perm, A = g.offsets.cpu().numpy(), g.perm.cpu().numpy(), T * (k + shared)
+    w, wv = random_matrix(rng, (E + shared, N), K)
+    d, dv = random_rows(rng, A, N, kind, strided=True)
+    ref, size = mx4_ref.grouped(dv, wv.transpose(0, 2, 1), off)
+    terms = N * (3 if kind == "f32" else 1)
+    for dt in types().values():
+        check(f"experts gradient {kind} T={T} in order -> {dt}", moe.mx4_experts_matmul_backward(d, w, g, dtype=dt), ref,
+              size, terms)
+    dx, total = np.zeros((T, K)), np.zeros((T, K))
+    np.add.at(dx, mx4_ref.token_rows(perm, T, k), ref)
+    np.add.at(total, mx4_ref.token_rows(perm, T, k), size)
+    got = moe.mx4_experts_matmul_backward(d, w, g, tokens=T)
+    assert got.shape == (T, K)
+    check(f"experts gradient {kind} T={T} by token", got, dx, total, terms + k + 1)
+    assert torch.equal(moe.mx4_experts_matmul_backward(d, w, g, tokens=T), got)
+
+
+def test_rows_of_no_group_stay_and_bad_ids_stay_in_bounds():
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(9)
+    E, N, K, A = 4, 32, 64, 40
+    w, wv = random_matrix(rng, (E, N), K)
+    off = torch.tensor([0, 0, 7, 7, 29, 29], dtype=torch.int32, device="cuda")
+    g = moe.Grouping(torch.zeros(E + 1, dtype=torch.int32, device="cuda"), off,
+                     torch.arange(A, dtype=torch.int32, device="cuda"), torch.arange(A, dtype=torch.int32, device="cuda"))
+    x, xv = random_rows(rng, A, K, "bf16")
+    room = torch.full((A, N), 7.0, device="cuda", dtype=torch.bfloat16)
+    y = moe.mx4_experts_matmul(x, w, g, out=room)
+    ref, size = mx4_ref.grouped(xv, wv, off.cpu().numpy())
+    check("seven and 22 rows", y[:29], ref[:29], size[:29], K)
+    assert (room[29:] == 7).all()
+    d, _ = random_rows(rng, A, N, "bf16")
+    room = torch.full((A, K), 7.0, device="cuda", dtype=torch.bfloat16)
+    moe.mx4_experts_matmul_backward(d, w, g, out=room)
+    assert (room[29:] == 7).all() and not (room[:29] == 7).all()
+    # ids past the assignments read as rows of zeros
+    g.perm[3], g.perm[20] = 1 << 30, -5
+    y = moe.mx4_experts_matmul(x, w, g, tokens=A)
+    assert not y[3].any() and not y[20].any()
+    check("rows beside bad ids", y[4:20], ref[4:20], size[4:20], K)
+    # offsets past the rows are cut
+    g.offsets = torch.tensor([0, 0, 7, 7, 1 << 30, 29], dtype=torch.int32, device="cuda")
+    ref, size = mx4_ref.grouped(xv, wv, np.array([0, 0, 7, 7, A]))
+    check("a cut offset", moe.mx4_experts_matmul(x, w, g), ref, size, K)
+
+
+def test_experts_refusals():
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(2)
+    g = grouping_of(rng, 6, 2, 4, True)
+    w, _ = random_matrix(rng, (5, 16), 64)
+    x, _ = random_rows(rng, 6, 64, "bf16")
+    flat, _ = random_matrix(rng, (16,), 64)
+    four, _ = random_matrix(rng, (4, 16), 64)
+    bad = [lambda: moe.mx4_experts_matmul(x, flat, g, tokens=6), lambda: moe.mx4_experts_matmul(x, four, g, tokens=6),
+           lambda: moe.mx4_experts_matmul(x, w, g), lambda: moe.mx4_experts_matmul(x, w, g, tokens=5),
+           lambda: moe.mx4_experts_matmul(x[:, :32], w, g, tokens=6), lambda: moe.mx4_experts_matmul(x[:5], w, g, tokens=6),
+           lambda: moe.mx4_experts_matmul(x.t(), w, g, tokens=6), lambda: moe.mx4_matmul(x, w),
+           lambda: moe.mx4_matmul(x[:, ::2], flat), lambda: moe.mx4_matmul(x[:1].expand(4, 64), flat),
+           lambda: moe.mx4_matmul(x, flat, out=torch.empty(6, 17, device="cuda", dtype=torch.bfloat16)),
+           lambda: moe.mx4_matmul_backward(x, flat), lambda: moe.mx4_experts_matmul_backward(x, w, g, tokens=6),
+           lambda: moe.Mx4(w.codes[..., :16], w.scales, 64), lambda: moe.Mx4(w.codes, w.scales, 65),
+           lambda: moe.Mx4(w.codes.transpose(0, 1), w.scales.transpose(0, 1), 64)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: moe.mx4_quantize(x.half()), lambda: moe.mx4_matmul(x.half(), flat),
+              lambda: moe.mx4_matmul(x, flat, dtype=torch.float16)):
+        with pytest.raises(TypeError):
+            f()
+    with pytest.raises(moe.MoeError) as e:
+        moe.mx4_experts_matmul_backward(torch.zeros(18, 16, device="cuda"), w, g, tokens=6,
+                                        workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == moe.ERR_WORKSPACE
+
+
+def test_offsets_past_32_bits():
+    """More than 4 GiB of codes, and more than 2^31 results: the last expert's rows and the last rows are right."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(4)
+    E, N, K = 2049, 2048, 2048
+    last, lv = random_matrix(rng, (N,), K)
+    codes = torch.zeros((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((E, N, K // 32), dtype=torch.uint8, device="cuda")
+    codes[-1], scales[-1] = last.codes, last.scales
+    x, xv = random_rows(rng, 5, K, "bf16")
+    off = torch.zeros(E + 2, dtype=torch.int32, device="cuda")
+    off[E:] = 5
+    g = moe.Grouping(torch.zeros(E + 1, dtype=torch.int32, device="cuda"), off,
+                     torch.arange(5, dtype=torch.int32, device="cuda"), torch.arange(5, dtype=torch.int32, device="cuda"))
+    w = moe.Mx4(codes, scales, K)
+    check("last of 2049 experts", moe.mx4_experts_matmul(x, w, g), xv @ lv.T, np.abs(xv) @ np.abs(lv).T, K)
+    check("its gradient", moe.mx4_experts_matmul_backward(x, w, g), xv @ lv, np.abs(xv) @ np.abs(lv), N)
+    del codes, scales, w
+    T, N, K = (1 << 20) + 3, 2100, 32
+    w, wv = random_matrix(rng, (N,), K)
+    x = torch.randn((T, K), device="cuda").bfloat16()
+    y = moe.mx4_matmul(x, w)
+    at = [0, T // 2, T - 1]
+    xv = as64(x[at])
+    check("2^31 results", y[at], xv @ wv.T, np.abs(xv) @ np.abs(wv).T, K)

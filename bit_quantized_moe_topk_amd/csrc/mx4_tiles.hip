@@ -1,0 +1,479 @@
+// Products of many rows with a microscaled matrix on 32x32x16 matrix-core
+// tiles (bf16 weights converted in registers, bf16 or float32 rows).
+//
+// A workgroup takes up to 128 rows of one group and 256 rows of its matrix;
+// each of its four waves owns 64 matrix rows for all of the workgroup's rows.
+// A wave converts its own weights right before the products that use them
+// (four conversions for eight values, against up to four products), so the
+// matrix never enters LDS; the rows do, in stages of 64 columns, double
+// buffered, because every wave reads them all. Bound by the matrix cores.
+//
+// A group's rows are dealt to its tiles in whole runs of 32, evenly (160 rows:
+// 96 and 64, not 128 and 32): a run that is not there costs no products, and
+// the conversions, which a tile of one run would be bound by, are spread over
+// as many products as there are.
+#include "mx4.h"
+#include "sched.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTM = 128;   // rows per tile, at most
+constexpr int kTN = 256;   // matrix rows per tile
+constexpr int kTK = 64;    // columns per stage: two blocks
+constexpr int kThreads = 256;
+
+// Stage layout in LDS: rows of 64 bf16 values, the eight 16-byte chunks of row m at
+// positions q ^ ((m >> 1) & 7): the 16 rows that a quarter of a wave's fragment
+// read takes then hit all 64 banks once.
+__device__ inline int chunk_at(int m, int q) { return m * 8 + (q ^ ((m >> 1) & 7)); }
+
+struct TileInfo {
+  int e, s0, M, n0;
+};
+
+// Tiles of a launch: base[e] = the tiles before group e (of each strip of kTN matrix rows).
+struct Tiles {
+  int base[MOE_MAX_E_DEV + 2];
+  int wsum[16];
+};
+
+__device__ inline int first_row(const Mx4Args& a, int e) { return min(max(a.offsets[e], 0), a.A); }
+
+__device__ inline int tiles_init(Tiles& t, const Mx4Args& a) {
+  if (!a.offsets) return (a.A + kTM - 1) / kTM;
+  for (int e = threadIdx.x; e < a.E_tot; e += blockDim.x)
+    t.base[e] = max(0, first_row(a, e + 1) - first_row(a, e) + kTM - 1) / kTM;
+  __syncthreads();
+  const int n = block_exclusive_scan(t.base, a.E_tot, t.wsum);
+  if (threadIdx.x == 0) t.base[a.E_tot] = n;
+  __syncthreads();
+  return n;
+}
+
+__device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int item, int strips, int strip) {
+  TileInfo i;
+  const int ti = item / strips;
+  int r0 = 0, rows = a.A, of = (a.A + kTM - 1) / kTM, j = ti;
+  i.e = 0;
+  if (a.offsets) {
+    i.e = __builtin_amdgcn_readfirstlane(workmap_find(t.base, a.E_tot, ti));
+    r0 = first_row(a, i.e);
+    rows = first_row(a, i.e + 1) - r0;
+    j = ti - __builtin_amdgcn_readfirstlane(t.base[i.e]);
+    of = (rows + kTM - 1) / kTM;
+  }
+  const int runs = (rows + 31) / 32;
+  const int a0 = (int)((long long)j * runs / of) * 32, a1 = (int)((long long)(j + 1) * runs / of) * 32;
+  i.s0 = r0 + a0;
+  i.M = min(a1, rows) - a0;
+  i.n0 = (item - ti * strips) * strip;
+  return i;
+}
+
+// One stage's products: R runs of 32 rows, 64 matrix rows, 64 columns. Lane
+// half h holds block h of the stage (codes c, scale sc), so product step kk
+// takes values 8 kk .. + 7 of both blocks.
+template <int R, int P>
+__device__ inline void stage_products(const uint4* xs, const uint4 (&c)[2], const float (&sc)[2],
+                                      floatx16_t (&acc)[4][2]) {
+  const int lane = threadIdx.x & 63, hq = 4 * (lane >> 5), r = lane & 31;
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    bf16x8_t w[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      w[j] = mx4_frag(kk == 0 ? c[j].x : kk == 1 ? c[j].y : kk == 2 ? c[j].z : c[j].w, sc[j]);
+#pragma unroll
+    for (int p = P - 1; p >= 0; --p)
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const bf16x8_t x = __builtin_bit_cast(bf16x8_t, xs[p * kTM * 8 + chunk_at(32 * i + r, hq + kk)]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
+      }
+  }
+}
+
+// Stores one run of 32 rows: acc[j][v] is matrix row n0 + 32 j + 8 (v / 4) +
+// 4 h + v % 4, row s0 + lane % 32. 16-bit results go through LDS of the
+// wave's own (lo: rows 0 .. 15, hi: the others; row r's sixteen 8-byte pieces
+// at positions piece ^ 2 (r & 7)), so that each lane stores 16 bytes and eight
+// lanes a whole 128-byte line.
+__device__ inline void store_run(const Mx4Args& a, const floatx16_t (&acc)[2], uint4* lo, uint4* hi, int s0, int M,
+                                 int n0) {
+  const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+  if (a.ydtype == 1) {
+    uint2* o = reinterpret_cast<uint2*>(r < 16 ? lo : hi) + 16 * (r & 15);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint2 v;
+        v.x = f32_to_bf16_bits(acc[j][4 * q]) | f32_to_bf16_bits(acc[j][4 * q + 1]) << 16;
+        v.y = f32_to_bf16_bits(acc[j][4 * q + 2]) | f32_to_bf16_bits(acc[j][4 * q + 3]) << 16;
+        o[(8 * j + 2 * q + h) ^ (2 * (r & 7))] = v;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int mm = 8 * u + (lane >> 3), n = n0 + 8 * (lane & 7);
+      const uint4 v = (u < 2 ? lo + 64 * u : hi + 64 * (u - 2))[lane ^ (mm & 7)];
+      if (mm < M && n < a.N) {
+        uint16_t* y = static_cast<uint16_t*>(a.y) + (size_t)(s0 + mm) * a.N + n;
+        if (wide) {
+          *reinterpret_cast<uint4*>(y) = v;
+        } else {
+          const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            if (n + z < a.N) y[z] = (uint16_t)(p[z / 2] >> (16 * (z & 1)));
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else if (r < M) {
+    float* y = static_cast<float*>(a.y) + (size_t)(s0 + r) * a.N;
+    const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = n0 + 32 * j + 8 * q + 4 * h;
+        if (wide) {
+          if (n < a.N)
+            *reinterpret_cast<float4*>(y + n) =
+                make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
+        } else {
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            if (n + z < a.N) y[n + z] = acc[j][4 * q + z];
+        }
+      }
+  }
+}
+
+// Any K, stride and alignment, and float32 rows (P = 3 bf16 parts a value; bf16: 1): rows pass
+// through registers on their way to LDS, zeros in place of columns past K.
+template <int P>
+__global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Args a, bool vec) {
+  __shared__ uint4 xs[2][P * kTM * 8];
+  __shared__ uint4 stg[4][256];
+  __shared__ Tiles tiles;
+  const int strips = (a.N + kTN - 1) / kTN;
+  const int items = tiles_init(tiles, a) * strips;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
+  const int nb = mx4_blocks(a.K), S = (nb + 1) / 2;
+  // consecutive items on one XCD (workgroup g runs on XCD g % 8): they share rows, or a matrix
+  const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
+  for (int item = pos; item < items; item += G) {
+    const TileInfo t = tile_of(tiles, a, item, strips, kTN);
+    const int R = (t.M + 31) / 32;
+    // this wave's weights: matrix rows n0 + 64 wave + 32 j + r (past N: the last one, not stored)
+    const uint4* wc[2];
+    const uint8_t* ws[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const size_t row = (size_t)t.e * a.N + min(t.n0 + 64 * wave + 32 * j + r, a.N - 1);
+      wc[j] = reinterpret_cast<const uint4*>(a.wc) + row * nb;
+      ws[j] = a.ws + row * nb;
+    }
+    // rows of a stage: thread: row tid / 2, chunks 4 (tid % 2) .. + 3
+    const int m = tid >> 1;
+    const int xr = m < t.M ? mx4_row(a, t.s0 + m) : -1;
+    const char* row = xr < 0 ? nullptr : static_cast<const char*>(a.x) + (size_t)xr * a.ldx * (P == 1 ? 2 : 4);
+    auto load_rows = [&](int s, int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 4 * (tid & 1); q < 4 * (tid & 1) + 4; ++q) {
+        const int k = s * kTK + 8 * q;
+        if constexpr (P == 1) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (row && k < a.K) v = load8_bf16(reinterpret_cast<const uint16_t*>(row), k, a.K, vec);
+          xs[b][chunk_at(m, q)] = v;
+        } else {
+          float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (row && k < a.K) load8_f32(reinterpret_cast<const float*>(row), k, a.K, vec, f);
+          uint4 v0, v1, v2;
+          split3x8(f, v0, v1, v2);
+          xs[b][chunk_at(m, q)] = v0;
+          xs[b][kTM * 8 + chunk_at(m, q)] = v1;
+          xs[b][2 * kTM * 8 + chunk_at(m, q)] = v2;
+        }
+      }
+    };
+    auto load_w = [&](int s, uint4 (&c)[2], float (&sc)[2]) __attribute__((always_inline)) {
+      const int b = 2 * s + h;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        c[j] = make_uint4(0, 0, 0, 0);
+        uint32_t v = 0;
+        if (b < nb) {
+          c[j] = wc[j][b];
+          v = ws[j][b];
+        }
+        sc[j] = mx4_scale(v);
+      }
+    };
+    floatx16_t acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = floatx16_t{};
+    uint4 c[2], cn[2];
+    float sc[2], scn[2];
+    load_rows(0, 0);
+    load_w(0, c, sc);
+    __syncthreads();
+    auto run = [&](auto RR) __attribute__((always_inline)) {
+      constexpr int RN = decltype(RR)::value;
+      for (int s = 0; s < S; ++s) {
+        if (s + 1 < S) {
+          load_rows(s + 1, (s + 1) & 1);
+          load_w(s + 1, cn, scn);
+        }
+        stage_products<RN, P>(xs[s & 1], c, sc, acc);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          c[j] = cn[j];
+          sc[j] = scn[j];
+        }
+        __syncthreads();
+      }
+    };
+    if (R == 4) run(std::integral_constant<int, 4>{});
+    else if (R == 3) run(std::integral_constant<int, 3>{});
+    else if (R == 2) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 1>{});
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < R) store_run(a, acc[i], stg[wave], stg[wave] + 128, t.s0 + 32 * i, t.M - 32 * i, t.n0 + 64 * wave);
+  }
+}
+
+// ---- rows and matrix streamed through LDS ---------------------------------------
+//
+// The same products where rows can be read 16 bytes at a time and K is a
+// multiple of 128. Eight waves, one workgroup per CU. Rows, codes and scales
+// come by direct global-to-LDS loads in steps of 128 columns, double buffered:
+// a step's loads are in flight for the whole step before it, and the first
+// step of the next tile is loaded during the last one of this tile, so the
+// matrix cores wait for memory at the first tile alone. (With the codes loaded
+// straight into registers one 64-column stage ahead, 32 bytes from each of 32
+// matrix rows at a time, those loads took a quarter of the kernel's time.)
+// The workgroup is WN waves across 64 WN matrix rows by 8 / WN waves down its
+// 128 rows; each converts the weights it multiplies.
+
+constexpr int kStep = 128;  // columns per step: four blocks
+
+__device__ const uint4 zero_page[16] = {};
+
+__device__ inline uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
+}
+
+// Direct loads as instructions of their own: lane l's bytes land at LDS
+// address `to` + 16 l (4 l). The compiler would make every LDS read wait for
+// all of them; here step_done() is the one wait, at the end of a step. (m0 has
+// no other user in these kernels.)
+template <int OFF>
+__device__ inline void stream16(const void* src, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
+               :: "s"(to - OFF), "v"(src), "n"(OFF) : "memory");  // (the offset counts on both sides)
+}
+__device__ inline void stream16(const void* base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(to), "v"(off), "s"(base) : "memory");
+}
+__device__ inline void stream4(const void* base, uint32_t off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+               :: "s"(to), "v"(off), "s"(base) : "memory");
+}
+// This wave's direct loads have landed and its LDS reads are done; then the same for every wave.
+__device__ inline void step_done() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int WN>
+struct StreamBuf {
+  uint4 x[2][kTM * 8];        // two 64-column stages (chunk_at)
+  uint4 w[64 * WN * 4];       // matrix row n: its four blocks, block c at position c ^ ((n >> 2) & 3)
+  uint32_t s[64 * WN];        // its four scales
+};
+
+template <int WN>
+__global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
+  constexpr int kRuns = WN / 2;  // runs of 32 rows per wave
+  constexpr int kWL = WN / 2;    // code loads per wave and step (16 matrix rows each)
+  __shared__ StreamBuf<WN> buf[2];
+  __shared__ Tiles tiles;
+  constexpr int strip = 64 * WN;
+  const int strips = (a.N + strip - 1) / strip;
+  const int items = tiles_init(tiles, a) * strips;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r = lane & 31, wn = wave % WN, wm = wave / WN;
+  const int nb = mx4_blocks(a.K), P = a.K / kStep;
+  const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
+  if (pos >= items) return;
+
+  // load cursor: this lane's rows (rows 16 wave + 8 u + l / 8, chunk l % 8 of the stage as placed)
+  // and matrix rows (8 WN wave + 16 i + l / 4, block l % 4 as placed), as they advance by steps
+  const char* xp[2];
+  uint32_t xstep[2], woff[kWL], soff;
+  const char *wbase, *sbase;
+  int row_next[2];
+  auto row_of = [&](int u) { return 16 * wave + 8 * u + (lane >> 3); };
+  auto fetch_rows = [&](const TileInfo& t) {  // the row numbers of a tile, to be used later
+#pragma unroll
+    for (int u = 0; u < 2; ++u) row_next[u] = row_of(u) < t.M ? mx4_row(a, t.s0 + row_of(u)) : -1;
+  };
+  auto aim = [&](const TileInfo& t) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int q = (lane & 7) ^ ((row_of(u) >> 1) & 7);
+      xp[u] = row_next[u] < 0 ? reinterpret_cast<const char*>(zero_page) + 16 * q
+                              : static_cast<const char*>(a.x) + 2 * (row_next[u] * a.ldx + 8 * q);
+      xstep[u] = row_next[u] < 0 ? 0 : 2 * kStep;
+    }
+    wbase = reinterpret_cast<const char*>(a.wc) + (size_t)t.e * a.N * nb * 16;
+    sbase = reinterpret_cast<const char*>(a.ws) + (size_t)t.e * a.N * nb;
+#pragma unroll
+    for (int i = 0; i < kWL; ++i) {
+      const int n = 8 * WN * wave + 16 * i + (lane >> 2);
+      woff[i] = (uint32_t)min(t.n0 + n, a.N - 1) * (nb * 16) + 16 * ((lane & 3) ^ ((n >> 2) & 3));
+    }
+    soff = (uint32_t)min(t.n0 + 8 * WN * wave + lane, a.N - 1) * nb;
+  };
+  auto load = [&](int b) __attribute__((always_inline)) {
+    StreamBuf<WN>& B = buf[b];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      stream16<0>(xp[u], lds_offset(B.x[0]) + 1024 * (2 * wave + u));
+      stream16<128>(xp[u], lds_offset(B.x[1]) + 1024 * (2 * wave + u));
+      xp[u] += xstep[u];
+    }
+#pragma unroll
+    for (int i = 0; i < kWL; ++i) stream16(wbase, woff[i], lds_offset(B.w) + 1024 * (kWL * wave + i));
+    if (WN == 8 || lane < 8 * WN) stream4(sbase, soff, lds_offset(B.s) + 32 * WN * wave);
+    wbase += 64;
+    sbase += 4;
+  };
+
+  int item = pos;
+  TileInfo t = tile_of(tiles, a, item, strips, strip);
+  fetch_rows(t);
+  aim(t);
+  load(0);
+  int b = 0;
+  step_done();
+  for (;;) {
+    const int next = item + G;
+    TileInfo tn = t;
+    if (next < items) {
+      tn = tile_of(tiles, a, next, strips, strip);
+      fetch_rows(tn);
+    }
+    const int live = min(max((t.M + 31) / 32 - kRuns * wm, 0), kRuns);
+    floatx16_t acc[kRuns][2];
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = floatx16_t{};
+    auto products = [&](auto LL) __attribute__((always_inline)) {
+      constexpr int L = decltype(LL)::value;
+      const StreamBuf<WN>& B = buf[b];
+      uint32_t sw[2];
+      const uint4* wr[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = 64 * wn + 32 * j + r;
+        sw[j] = B.s[n] >> (8 * h);
+        wr[j] = B.w + 4 * n;
+      }
+      const int sw4 = (r >> 2) & 3, hq = 4 * h;
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        uint4 c[2];
+        float sc[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          c[j] = wr[j][(2 * st + h) ^ sw4];
+          sc[j] = mx4_scale((sw[j] >> (16 * st)) & 255u);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          bf16x8_t w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            w[j] = mx4_frag(kk == 0 ? c[j].x : kk == 1 ? c[j].y : kk == 2 ? c[j].z : c[j].w, sc[j]);
+#pragma unroll
+          for (int i = 0; i < L; ++i) {
+            const bf16x8_t x =
+                __builtin_bit_cast(bf16x8_t, B.x[st][chunk_at(32 * (kRuns * wm + i) + r, hq + kk)]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
+          }
+        }
+      }
+    };
+    // one loop for each number of live runs (a switch inside the loop makes the compiler move accumulators)
+    auto run = [&](auto LL) __attribute__((always_inline)) {
+      for (int p = 1; p < P; ++p) {
+        load(b ^ 1);
+        if constexpr (decltype(LL)::value > 0) products(LL);
+        step_done();
+        b ^= 1;
+      }
+      if (next < items) {
+        aim(tn);
+        load(b ^ 1);
+      }
+      if constexpr (decltype(LL)::value > 0) products(LL);
+      step_done();
+      b ^= 1;
+    };
+    if (live == kRuns) run(std::integral_constant<int, kRuns>{});
+    else if (kRuns > 3 && live == 3) run(std::integral_constant<int, kRuns < 3 ? 0 : 3>{});
+    else if (kRuns > 2 && live == 2) run(std::integral_constant<int, kRuns < 2 ? 0 : 2>{});
+    else if (kRuns > 1 && live == 1) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 0>{});
+    // The part of the buffer just used up (b ^ 1) that this wave fills is free until it does so
+    // again, after its stores.
+    uint4 *lo = buf[b ^ 1].x[0] + 128 * wave, *hi = buf[b ^ 1].x[1] + 128 * wave;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i)
+      if (i < live)
+        store_run(a, acc[i], lo, hi, t.s0 + 32 * (kRuns * wm + i), t.M - 32 * (kRuns * wm + i), t.n0 + 64 * wn);
+    if (next >= items) break;
+    item = next;
+    t = tn;
+  }
+}
+
+}  // namespace
+
+// Tiles from this many rows a group on average.
+bool mx4_tiles_pay(const Mx4Args& a) { return a.xdtype != kMx4 && a.A >= 32LL * a.E_tot; }
+
+hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s) {
+  const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
+  // streamed: 32-bit offsets within one matrix
+  const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && (long long)a.N * a.K < (1LL << 32);
+  const int strip = !even ? kTN : a.N > 256 ? 512 : a.N > 128 ? 256 : 128;
+  const long long strips = (a.N + strip - 1) / strip;
+  const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * strips;
+  const int cap = (even ? 1 : 2) * device_cus();
+  const dim3 g((unsigned)(most < cap ? most : cap));
+  if (!even && a.xdtype == 1) MOE_LAUNCH("mx4_tiles", s, tiles_forward<1>, g, dim3(kThreads), 0, s, a, vec);
+  else if (!even) MOE_LAUNCH("mx4_tiles", s, tiles_forward<3>, g, dim3(kThreads), 0, s, a, vec);
+  else if (strip == 512) MOE_LAUNCH("mx4_tiles_stream", s, tiles_stream<8>, g, dim3(512), 0, s, a);
+  else if (strip == 256) MOE_LAUNCH("mx4_tiles_stream", s, tiles_stream<4>, g, dim3(512), 0, s, a);
+  else MOE_LAUNCH("mx4_tiles_stream", s, tiles_stream<2>, g, dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

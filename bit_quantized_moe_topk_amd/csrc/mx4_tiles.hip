@@ -48,7 +48,7 @@ __device__ inline int tiles_init(Tiles& t, const Mx4Args& a) {
   const int n = block_exclusive_scan(t.base, a.E_tot, t.wsum);
   if (threadIdx.x == 0) t.base[a.E_tot] = n;
   __syncthreads();
-  return n;
+  return __builtin_amdgcn_readfirstlane(n);
 }
 
 __device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int item, int strips, int strip) {
@@ -58,8 +58,8 @@ __device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int item, i
   i.e = 0;
   if (a.offsets) {
     i.e = __builtin_amdgcn_readfirstlane(workmap_find(t.base, a.E_tot, ti));
-    r0 = first_row(a, i.e);
-    rows = first_row(a, i.e + 1) - r0;
+    r0 = __builtin_amdgcn_readfirstlane(first_row(a, i.e));
+    rows = __builtin_amdgcn_readfirstlane(first_row(a, i.e + 1)) - r0;
     j = ti - __builtin_amdgcn_readfirstlane(t.base[i.e]);
     of = (rows + kTM - 1) / kTM;
   }
@@ -97,45 +97,43 @@ __device__ inline void stage_products(const uint4* xs, const uint4 (&c)[2], cons
 }
 
 // Stores one run of 32 rows: acc[j][v] is matrix row n0 + 32 j + 8 (v / 4) +
-// 4 h + v % 4, row s0 + lane % 32. 16-bit results go through LDS of the
-// wave's own (lo: rows 0 .. 15, hi: the others; row r's sixteen 8-byte pieces
-// at positions piece ^ 2 (r & 7)), so that each lane stores 16 bytes and eight
-// lanes a whole 128-byte line.
-__device__ inline void store_run(const Mx4Args& a, const floatx16_t (&acc)[2], uint4* lo, uint4* hi, int s0, int M,
-                                 int n0) {
+// 4 h + v % 4, row s0 + r. For 16-bit results the lane halves swap quads, so
+// that each lane holds eight neighbours (h 0: of an even quad pair, h 1: of
+// the odd one) and stores 16 bytes.
+__device__ inline uint32_t pack_bf16(float a, float b) {
+  typedef float float2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{a, b}), bf16x2_t));
+}
+
+__device__ inline void store_run(const Mx4Args& a, const floatx16_t (&acc)[2], int s0, int M, int n0) {
   const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
   if (a.ydtype == 1) {
-    uint2* o = reinterpret_cast<uint2*>(r < 16 ? lo : hi) + 16 * (r & 15);
+    uint16_t* y = static_cast<uint16_t*>(a.y) + (size_t)(s0 + r) * a.N;
+    const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint2 v;
-        v.x = f32_to_bf16_bits(acc[j][4 * q]) | f32_to_bf16_bits(acc[j][4 * q + 1]) << 16;
-        v.y = f32_to_bf16_bits(acc[j][4 * q + 2]) | f32_to_bf16_bits(acc[j][4 * q + 3]) << 16;
-        o[(8 * j + 2 * q + h) ^ (2 * (r & 7))] = v;
-      }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+      for (int q = 0; q < 4; q += 2) {
+        uint32_t p[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int mm = 8 * u + (lane >> 3), n = n0 + 8 * (lane & 7);
-      const uint4 v = (u < 2 ? lo + 64 * u : hi + 64 * (u - 2))[lane ^ (mm & 7)];
-      if (mm < M && n < a.N) {
-        uint16_t* y = static_cast<uint16_t*>(a.y) + (size_t)(s0 + mm) * a.N + n;
-        if (wide) {
-          *reinterpret_cast<uint4*>(y) = v;
-        } else {
-          const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+        for (int z = 0; z < 2; ++z) {
+          const auto s = __builtin_amdgcn_permlane32_swap(pack_bf16(acc[j][4 * q + 2 * z], acc[j][4 * q + 2 * z + 1]),
+                                                          pack_bf16(acc[j][4 * q + 2 * z + 4], acc[j][4 * q + 2 * z + 5]),
+                                                          false, false);
+          p[z] = s[0];
+          p[2 + z] = s[1];
+        }
+        const int n = n0 + 32 * j + 8 * (q + h);
+        if (r < M) {
+          if (wide) {
+            if (n < a.N) *reinterpret_cast<uint4*>(y + n) = make_uint4(p[0], p[1], p[2], p[3]);
+          } else {
 #pragma unroll
-          for (int z = 0; z < 8; ++z)
-            if (n + z < a.N) y[z] = (uint16_t)(p[z / 2] >> (16 * (z & 1)));
+            for (int z = 0; z < 8; ++z)
+              if (n + z < a.N) y[n + z] = (uint16_t)(p[z / 2] >> (16 * (z & 1)));
+          }
         }
       }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   } else if (r < M) {
     float* y = static_cast<float*>(a.y) + (size_t)(s0 + r) * a.N;
     const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
@@ -162,7 +160,6 @@ __device__ inline void store_run(const Mx4Args& a, const floatx16_t (&acc)[2], u
 template <int P>
 __global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Args a, bool vec) {
   __shared__ uint4 xs[2][P * kTM * 8];
-  __shared__ uint4 stg[4][256];
   __shared__ Tiles tiles;
   const int strips = (a.N + kTN - 1) / kTN;
   const int items = tiles_init(tiles, a) * strips;
@@ -250,7 +247,7 @@ __global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Arg
     else run(std::integral_constant<int, 1>{});
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < R) store_run(a, acc[i], stg[wave], stg[wave] + 128, t.s0 + 32 * i, t.M - 32 * i, t.n0 + 64 * wave);
+      if (i < R) store_run(a, acc[i], t.s0 + 32 * i, t.M - 32 * i, t.n0 + 64 * wave);
   }
 }
 
@@ -259,17 +256,15 @@ __global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Arg
 // The same products where rows can be read 16 bytes at a time and K is a
 // multiple of 128. Eight waves, one workgroup per CU. Rows, codes and scales
 // come by direct global-to-LDS loads in steps of 128 columns, double buffered:
-// a step's loads are in flight for the whole step before it, and the first
-// step of the next tile is loaded during the last one of this tile, so the
-// matrix cores wait for memory at the first tile alone. (With the codes loaded
+// as soon as a step is read its buffer takes the step after next, so a load has
+// a whole step to land, and the loads run on across tiles: the matrix cores
+// wait for memory at the first tile alone. (With the codes loaded
 // straight into registers one 64-column stage ahead, 32 bytes from each of 32
 // matrix rows at a time, those loads took a quarter of the kernel's time.)
 // The workgroup is WN waves across 64 WN matrix rows by 8 / WN waves down its
 // 128 rows; each converts the weights it multiplies.
 
 constexpr int kStep = 128;  // columns per step: four blocks
-
-__device__ const uint4 zero_page[16] = {};
 
 __device__ inline uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
@@ -279,18 +274,13 @@ __device__ inline uint32_t lds_offset(const void* p) {
 // address `to` + 16 l (4 l). The compiler would make every LDS read wait for
 // all of them; here step_done() is the one wait, at the end of a step. (m0 has
 // no other user in these kernels.)
-template <int OFF>
-__device__ inline void stream16(const void* src, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off offset:%2"
-               :: "s"(to - OFF), "v"(src), "n"(OFF) : "memory");  // (the offset counts on both sides)
-}
 __device__ inline void stream16(const void* base, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(to), "v"(off), "s"(base) : "memory");
+               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base) : "memory");
 }
 __device__ inline void stream4(const void* base, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(to), "v"(off), "s"(base) : "memory");
+               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base) : "memory");
 }
 // This wave's direct loads have landed and its LDS reads are done; then the same for every wave.
 __device__ inline void step_done() {
@@ -319,25 +309,24 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
   if (pos >= items) return;
 
-  // load cursor: this lane's rows (rows 16 wave + 8 u + l / 8, chunk l % 8 of the stage as placed)
-  // and matrix rows (8 WN wave + 16 i + l / 4, block l % 4 as placed), as they advance by steps
-  const char* xp[2];
-  uint32_t xstep[2], woff[kWL], soff;
-  const char *wbase, *sbase;
+  // load cursor: this lane's rows (rows 16 wave + 8 u + l / 8, chunk l % 8 of the stage as placed;
+  // those past the tile's repeat its last, and are not stored) and matrix rows (8 WN wave + 16 i +
+  // l / 4, block l % 4 as placed), and the bases that advance by steps
+  uint32_t xoff[2], woff[kWL], soff;
+  const char *xbase, *wbase, *sbase;
   int row_next[2];
   auto row_of = [&](int u) { return 16 * wave + 8 * u + (lane >> 3); };
   auto fetch_rows = [&](const TileInfo& t) {  // the row numbers of a tile, to be used later
 #pragma unroll
-    for (int u = 0; u < 2; ++u) row_next[u] = row_of(u) < t.M ? mx4_row(a, t.s0 + row_of(u)) : -1;
+    for (int u = 0; u < 2; ++u) row_next[u] = max(mx4_row(a, t.s0 + min(row_of(u), t.M - 1)), 0);
   };
   auto aim = [&](const TileInfo& t) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int q = (lane & 7) ^ ((row_of(u) >> 1) & 7);
-      xp[u] = row_next[u] < 0 ? reinterpret_cast<const char*>(zero_page) + 16 * q
-                              : static_cast<const char*>(a.x) + 2 * (row_next[u] * a.ldx + 8 * q);
-      xstep[u] = row_next[u] < 0 ? 0 : 2 * kStep;
+      xoff[u] = (uint32_t)row_next[u] * (uint32_t)(2 * a.ldx) + 16 * q;
     }
+    xbase = static_cast<const char*>(a.x);
     wbase = reinterpret_cast<const char*>(a.wc) + (size_t)t.e * a.N * nb * 16;
     sbase = reinterpret_cast<const char*>(a.ws) + (size_t)t.e * a.N * nb;
 #pragma unroll
@@ -351,10 +340,10 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
     StreamBuf<WN>& B = buf[b];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      stream16<0>(xp[u], lds_offset(B.x[0]) + 1024 * (2 * wave + u));
-      stream16<128>(xp[u], lds_offset(B.x[1]) + 1024 * (2 * wave + u));
-      xp[u] += xstep[u];
+      stream16(xbase, xoff[u], lds_offset(B.x[0]) + 1024 * (2 * wave + u));
+      stream16(xbase + 128, xoff[u], lds_offset(B.x[1]) + 1024 * (2 * wave + u));
     }
+    xbase += 256;
 #pragma unroll
     for (int i = 0; i < kWL; ++i) stream16(wbase, woff[i], lds_offset(B.w) + 1024 * (kWL * wave + i));
     if (WN == 8 || lane < 8 * WN) stream4(sbase, soff, lds_offset(B.s) + 32 * WN * wave);
@@ -362,18 +351,17 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
     sbase += 4;
   };
 
-  int item = pos;
-  TileInfo t = tile_of(tiles, a, item, strips, strip);
+  int item = pos, b = 0;
+  TileInfo t = tile_of(tiles, a, item, strips, strip), tn = t;
   fetch_rows(t);
   aim(t);
   load(0);
-  int b = 0;
+  load(1);
   step_done();
   for (;;) {
-    const int next = item + G;
-    TileInfo tn = t;
-    if (next < items) {
-      tn = tile_of(tiles, a, next, strips, strip);
+    const bool more = item + G < items;
+    if (more) {
+      tn = tile_of(tiles, a, item + G, strips, strip);
       fetch_rows(tn);
     }
     const int live = min(max((t.M + 31) / 32 - kRuns * wm, 0), kRuns);
@@ -382,74 +370,78 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
     for (int i = 0; i < kRuns; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = floatx16_t{};
-    auto products = [&](auto LL) __attribute__((always_inline)) {
-      constexpr int L = decltype(LL)::value;
-      const StreamBuf<WN>& B = buf[b];
-      uint32_t sw[2];
-      const uint4* wr[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = 64 * wn + 32 * j + r;
-        sw[j] = B.s[n] >> (8 * h);
-        wr[j] = B.w + 4 * n;
-      }
-      const int sw4 = (r >> 2) & 3, hq = 4 * h;
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        uint4 c[2];
-        float sc[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          c[j] = wr[j][(2 * st + h) ^ sw4];
-          sc[j] = mx4_scale((sw[j] >> (16 * st)) & 255u);
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          bf16x8_t w[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[j] = mx4_frag(kk == 0 ? c[j].x : kk == 1 ? c[j].y : kk == 2 ? c[j].z : c[j].w, sc[j]);
-#pragma unroll
-          for (int i = 0; i < L; ++i) {
-            const bf16x8_t x =
-                __builtin_bit_cast(bf16x8_t, B.x[st][chunk_at(32 * (kRuns * wm + i) + r, hq + kk)]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
-          }
-        }
-      }
-    };
     // one loop for each number of live runs (a switch inside the loop makes the compiler move accumulators)
     auto run = [&](auto LL) __attribute__((always_inline)) {
-      for (int p = 1; p < P; ++p) {
-        load(b ^ 1);
-        if constexpr (decltype(LL)::value > 0) products(LL);
+      constexpr int L = decltype(LL)::value;
+      // next: the load that follows (0: two steps on; 1, 2: the next tile's first and second)
+      auto step = [&](auto next) __attribute__((always_inline)) {
+        const StreamBuf<WN>& B = buf[b];
+        uint32_t sw[2];
+        uint4 c[2];
+        bf16x8_t x[4][L > 0 ? L : 1];
+        auto products = [&](int st, int kk) __attribute__((always_inline)) {
+          bf16x8_t w[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 v = c[j];
+            w[j] = mx4_frag(kk == 0 ? v.x : kk == 1 ? v.y : kk == 2 ? v.z : v.w,
+                            mx4_scale((sw[j] >> (16 * st)) & 255u));
+          }
+#pragma unroll
+          for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x[kk][i], acc[i][j], 0, 0, 0);
+        };
+        auto read = [&](int st, int kk) __attribute__((always_inline)) {
+#pragma unroll
+          for (int i = 0; i < L; ++i)
+            x[kk][i] = __builtin_bit_cast(bf16x8_t, B.x[st][chunk_at(32 * (kRuns * wm + i) + r, 4 * h + kk)]);
+        };
+        if constexpr (L > 0) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int n = 64 * wn + 32 * j + r;
+            sw[j] = B.s[n] >> (8 * h);
+            c[j] = B.w[4 * n + (h ^ ((r >> 2) & 3))];
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            read(0, kk);
+            products(0, kk);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) c[j] = B.w[4 * (64 * wn + 32 * j + r) + ((2 + h) ^ ((r >> 2) & 3))];
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            read(1, kk);
+            products(1, kk);
+          }
+        }
+        // everything is read: the buffer takes the step after next, which has a step to land
         step_done();
+        if (decltype(next)::value == 0 || more) {
+          if (decltype(next)::value == 1) aim(tn);
+          load(b);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         b ^= 1;
-      }
-      if (next < items) {
-        aim(tn);
-        load(b ^ 1);
-      }
-      if constexpr (decltype(LL)::value > 0) products(LL);
-      step_done();
-      b ^= 1;
+      };
+      for (int p = 2; p < P; ++p) step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
     };
     if (live == kRuns) run(std::integral_constant<int, kRuns>{});
     else if (kRuns > 3 && live == 3) run(std::integral_constant<int, kRuns < 3 ? 0 : 3>{});
     else if (kRuns > 2 && live == 2) run(std::integral_constant<int, kRuns < 2 ? 0 : 2>{});
     else if (kRuns > 1 && live == 1) run(std::integral_constant<int, 1>{});
     else run(std::integral_constant<int, 0>{});
-    // The part of the buffer just used up (b ^ 1) that this wave fills is free until it does so
-    // again, after its stores.
-    uint4 *lo = buf[b ^ 1].x[0] + 128 * wave, *hi = buf[b ^ 1].x[1] + 128 * wave;
 #pragma unroll
     for (int i = 0; i < kRuns; ++i)
       if (i < live)
-        store_run(a, acc[i], lo, hi, t.s0 + 32 * (kRuns * wm + i), t.M - 32 * (kRuns * wm + i), t.n0 + 64 * wn);
-    if (next >= items) break;
-    item = next;
+        store_run(a, acc[i], t.s0 + 32 * (kRuns * wm + i), t.M - 32 * (kRuns * wm + i), t.n0 + 64 * wn);
+    if (!more) break;
+    item += G;
     t = tn;
   }
 }
@@ -461,8 +453,9 @@ bool mx4_tiles_pay(const Mx4Args& a) { return a.xdtype != kMx4 && a.A >= 32LL * 
 
 hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s) {
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
-  // streamed: 32-bit offsets within one matrix
-  const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && (long long)a.N * a.K < (1LL << 32);
+  // streamed: 32-bit offsets within one matrix and within the rows
+  const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && a.K >= 2 * kStep && (long long)a.N * a.K < (1LL << 32) &&
+                    (a.perm ? a.T : a.A) * a.ldx * 2 < (1LL << 32);
   const int strip = !even ? kTN : a.N > 256 ? 512 : a.N > 128 ? 256 : 128;
   const long long strips = (a.N + strip - 1) / strip;
   const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * strips;

@@ -393,8 +393,8 @@ int moe_mx4_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t 
  * E_tot is at most MOE_MAX_E + 1, A at most 2^23, N and K at most 2^19.
  * offsets: [E_tot + 1] (moe_group writes one more), perm: [A]; perm may be NULL
  * when gather == 0. Values of perm outside [0, A) are not detected; the kernels
- * stay in bounds and take a row of zeros for them, and offsets are cut to
- * [0, A]. Types and rounding as moe_mx4_matmul. */
+ * stay in bounds and the results of those rows are unspecified; offsets are cut
+ * to [0, A]. Types and rounding as moe_mx4_matmul. */
 int moe_mx4_experts_matmul(const void *x, const uint8_t *x_scales, int32_t xdtype, int64_t ldx,
                            int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t gather,
                            const int32_t *offsets, const int32_t *perm, const uint8_t *w_codes,

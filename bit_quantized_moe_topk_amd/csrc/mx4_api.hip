@@ -13,7 +13,7 @@ inline unsigned size_of(int32_t t) { return t == MOE_BF16 ? 2u : 4u; }
 
 // Limits of the launches: rows and columns of a matrix, rows of a product.
 constexpr int32_t kMaxDim = 1 << 19;
-constexpr int32_t kMaxRows = 1 << 23;
+constexpr int32_t kMaxRows = 1 << 22;
 
 // Checks that all products share. dtype: of the rows that come in (n_in values
 // each), out: of those that go out.

@@ -200,7 +200,10 @@ __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part
 }  // namespace
 
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
-  if (mx4_tiles_pay(a)) return launch_mx4_tiles(a, s);
+  if (a.A >= 32LL * a.E_tot) {
+    if (a.xdtype != kMx4) return launch_mx4_tiles(a, s);
+    if (mx4_tiles4_can(a)) return launch_mx4_tiles4(a, s);
+  }
   const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.N + kStrip - 1) / kStrip);
   const bool vec = a.xdtype != kMx4 && rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
   if (a.xdtype == kMx4) MOE_LAUNCH("mx4_rows", s, rows_forward<kMx4>, g, dim3(256), 0, s, a, vec);

@@ -7,69 +7,14 @@
 // (four conversions for eight values, against up to four products), so the
 // matrix never enters LDS; the rows do, in stages of 64 columns, double
 // buffered, because every wave reads them all. Bound by the matrix cores.
-//
-// A group's rows are dealt to its tiles in whole runs of 32, evenly (160 rows:
-// 96 and 64, not 128 and 32): a run that is not there costs no products, and
-// the conversions, which a tile of one run would be bound by, are spread over
-// as many products as there are.
-#include "mx4.h"
-#include "sched.h"
+#include "mx4_tile.h"
 
 namespace moe {
 namespace {
 
-constexpr int kTM = 128;   // rows per tile, at most
 constexpr int kTN = 256;   // matrix rows per tile
 constexpr int kTK = 64;    // columns per stage: two blocks
 constexpr int kThreads = 256;
-
-// Stage layout in LDS: rows of 64 bf16 values, the eight 16-byte chunks of row m at
-// positions q ^ ((m >> 1) & 7): the 16 rows that a quarter of a wave's fragment
-// read takes then hit all 64 banks once.
-__device__ inline int chunk_at(int m, int q) { return m * 8 + (q ^ ((m >> 1) & 7)); }
-
-struct TileInfo {
-  int e, s0, M, n0;
-};
-
-// Tiles of a launch: base[e] = the tiles before group e (of each strip of kTN matrix rows).
-struct Tiles {
-  int base[MOE_MAX_E_DEV + 2];
-  int wsum[16];
-};
-
-__device__ inline int first_row(const Mx4Args& a, int e) { return min(max(a.offsets[e], 0), a.A); }
-
-__device__ inline int tiles_init(Tiles& t, const Mx4Args& a) {
-  if (!a.offsets) return (a.A + kTM - 1) / kTM;
-  for (int e = threadIdx.x; e < a.E_tot; e += blockDim.x)
-    t.base[e] = max(0, first_row(a, e + 1) - first_row(a, e) + kTM - 1) / kTM;
-  __syncthreads();
-  const int n = block_exclusive_scan(t.base, a.E_tot, t.wsum);
-  if (threadIdx.x == 0) t.base[a.E_tot] = n;
-  __syncthreads();
-  return __builtin_amdgcn_readfirstlane(n);
-}
-
-__device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int item, int strips, int strip) {
-  TileInfo i;
-  const int ti = item / strips;
-  int r0 = 0, rows = a.A, of = (a.A + kTM - 1) / kTM, j = ti;
-  i.e = 0;
-  if (a.offsets) {
-    i.e = __builtin_amdgcn_readfirstlane(workmap_find(t.base, a.E_tot, ti));
-    r0 = __builtin_amdgcn_readfirstlane(first_row(a, i.e));
-    rows = __builtin_amdgcn_readfirstlane(first_row(a, i.e + 1)) - r0;
-    j = ti - __builtin_amdgcn_readfirstlane(t.base[i.e]);
-    of = (rows + kTM - 1) / kTM;
-  }
-  const int runs = (rows + 31) / 32;
-  const int a0 = (int)((long long)j * runs / of) * 32, a1 = (int)((long long)(j + 1) * runs / of) * 32;
-  i.s0 = r0 + a0;
-  i.M = min(a1, rows) - a0;
-  i.n0 = (item - ti * strips) * strip;
-  return i;
-}
 
 // One stage's products: R runs of 32 rows, 64 matrix rows, 64 columns. Lane
 // half h holds block h of the stage (codes c, scale sc), so product step kk
@@ -96,65 +41,6 @@ __device__ inline void stage_products(const uint4* xs, const uint4 (&c)[2], cons
   }
 }
 
-// Stores one run of 32 rows: acc[j][v] is matrix row n0 + 32 j + 8 (v / 4) +
-// 4 h + v % 4, row s0 + r. For 16-bit results the lane halves swap quads, so
-// that each lane holds eight neighbours (h 0: of an even quad pair, h 1: of
-// the odd one) and stores 16 bytes.
-__device__ inline uint32_t pack_bf16(float a, float b) {
-  typedef float float2_t __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((float2_t{a, b}), bf16x2_t));
-}
-
-__device__ inline void store_run(const Mx4Args& a, const floatx16_t (&acc)[2], int s0, int M, int n0) {
-  const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
-  if (a.ydtype == 1) {
-    uint16_t* y = static_cast<uint16_t*>(a.y) + (size_t)(s0 + r) * a.N;
-    const bool wide = a.N % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        uint32_t p[4];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const auto s = __builtin_amdgcn_permlane32_swap(pack_bf16(acc[j][4 * q + 2 * z], acc[j][4 * q + 2 * z + 1]),
-                                                          pack_bf16(acc[j][4 * q + 2 * z + 4], acc[j][4 * q + 2 * z + 5]),
-                                                          false, false);
-          p[z] = s[0];
-          p[2 + z] = s[1];
-        }
-        const int n = n0 + 32 * j + 8 * (q + h);
-        if (r < M) {
-          if (wide) {
-            if (n < a.N) *reinterpret_cast<uint4*>(y + n) = make_uint4(p[0], p[1], p[2], p[3]);
-          } else {
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-              if (n + z < a.N) y[n + z] = (uint16_t)(p[z / 2] >> (16 * (z & 1)));
-          }
-        }
-      }
-  } else if (r < M) {
-    float* y = static_cast<float*>(a.y) + (size_t)(s0 + r) * a.N;
-    const bool wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = n0 + 32 * j + 8 * q + 4 * h;
-        if (wide) {
-          if (n < a.N)
-            *reinterpret_cast<float4*>(y + n) =
-                make_float4(acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]);
-        } else {
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            if (n + z < a.N) y[n + z] = acc[j][4 * q + z];
-        }
-      }
-  }
-}
-
 // Any K, stride and alignment, and float32 rows (P = 3 bf16 parts a value; bf16: 1): rows pass
 // through registers on their way to LDS, zeros in place of columns past K.
 template <int P>
@@ -162,7 +48,7 @@ __global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Arg
   __shared__ uint4 xs[2][P * kTM * 8];
   __shared__ Tiles tiles;
   const int strips = (a.N + kTN - 1) / kTN;
-  const int items = tiles_init(tiles, a) * strips;
+  const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(xs), a) * strips;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
   const int nb = mx4_blocks(a.K), S = (nb + 1) / 2;
   // consecutive items on one XCD (workgroup g runs on XCD g % 8): they share rows, or a matrix
@@ -266,27 +152,6 @@ __global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Arg
 
 constexpr int kStep = 128;  // columns per step: four blocks
 
-__device__ inline uint32_t lds_offset(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;
-}
-
-// Direct loads as instructions of their own: lane l's bytes land at LDS
-// address `to` + 16 l (4 l). The compiler would make every LDS read wait for
-// all of them; here step_done() is the one wait, at the end of a step. (m0 has
-// no other user in these kernels.)
-__device__ inline void stream16(const void* base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base) : "memory");
-}
-__device__ inline void stream4(const void* base, uint32_t off, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base) : "memory");
-}
-// This wave's direct loads have landed and its LDS reads are done; then the same for every wave.
-__device__ inline void step_done() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 template <int WN>
 struct StreamBuf {
   uint4 x[2][kTM * 8];        // two 64-column stages (chunk_at)
@@ -302,7 +167,7 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   __shared__ Tiles tiles;
   constexpr int strip = 64 * WN;
   const int strips = (a.N + strip - 1) / strip;
-  const int items = tiles_init(tiles, a) * strips;
+  const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(buf), a) * strips;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r = lane & 31, wn = wave % WN, wm = wave / WN;
   const int nb = mx4_blocks(a.K), P = a.K / kStep;
@@ -447,9 +312,6 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
 }
 
 }  // namespace
-
-// Tiles from this many rows a group on average.
-bool mx4_tiles_pay(const Mx4Args& a) { return a.xdtype != kMx4 && a.A >= 32LL * a.E_tot; }
 
 hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s) {
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);

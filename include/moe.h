@@ -390,7 +390,7 @@ int moe_mx4_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t 
  *                the token of assignment perm[s].
  *   y     : [A][N] in the groups' order. Rows that are in no group (from
  *           offsets[E_tot] on) are left as they were.
- * E_tot is at most MOE_MAX_E + 1, A at most 2^23, N and K at most 2^19.
+ * E_tot is at most MOE_MAX_E + 1, A at most 2^22, N and K at most 2^19.
  * offsets: [E_tot + 1] (moe_group writes one more), perm: [A]; perm may be NULL
  * when gather == 0. Values of perm outside [0, A) are not detected; the kernels
  * stay in bounds and the results of those rows are unspecified; offsets are cut

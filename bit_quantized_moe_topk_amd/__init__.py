@@ -489,14 +489,21 @@ def layer_static(logits: torch.Tensor, x: torch.Tensor, ex: "Experts", k: int, m
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 
 
+# The handle of a device's current stream (the first form builds no Stream object: small products
+# take a few microseconds in all).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(name: str, dev: torch.device, *args) -> None:
     """Runs a library call on the current stream of the tensors' device."""
-    fn = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    fn = getattr(_lib or lib(), name)
+    i = dev.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(i))
     if st != OK:
         raise MoeError(name, st)
 
@@ -508,9 +515,10 @@ def _rows(name: str, t: torch.Tensor, n: int | None = None):
     code = _FLOATS.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    if t.dim() != 2 or (n is not None and t.shape[1] != n):
-        raise ValueError(f"{name} must be [rows, {'n' if n is None else n}]: got {tuple(t.shape)}")
-    R, m = t.shape
+    shape = t.shape
+    if len(shape) != 2 or (n is not None and shape[1] != n):
+        raise ValueError(f"{name} must be [rows, {'n' if n is None else n}]: got {tuple(shape)}")
+    R, m = shape
     ld, inner = t.stride()
     if R <= 1:
         ld = m
@@ -546,8 +554,9 @@ class Mx4:
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int):
         _need_cuda("codes", codes, torch.uint8)
         _need_cuda("scales", scales, torch.uint8)
-        if K < 1 or codes.dim() < 2 or scales.shape[-1] != (K + 31) // 32 \
-                or codes.shape[-1] != 16 * scales.shape[-1] or codes.shape[:-1] != scales.shape[:-1]:
+        *rows, n = codes.shape
+        *same, B = scales.shape
+        if K < 1 or not rows or B != (K + 31) // 32 or n != 16 * B or rows != same:
             raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold rows of {K}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")

@@ -185,6 +185,7 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_grad_tiles(const Mx4Args& a, hipStream_t s);
 bool mx4_tiles4_can(const Mx4Args& a);
 hipError_t launch_mx4_tiles4(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, int T, int k, int has_shared, int A,

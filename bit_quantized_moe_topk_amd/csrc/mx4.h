@@ -95,6 +95,12 @@ struct Mx4Args {
   int ydtype;
 };
 
+// About how many 128-row tiles the rows make: a group that has rows has one at least.
+inline long long mx4_row_tiles(const Mx4Args& a) {
+  const long long full = ((long long)a.A + 127) / 128, groups = a.A < a.E_tot ? a.A : a.E_tot;
+  return full > groups ? full : groups;
+}
+
 // x's row that row s of the groups reads; -1: none (an id out of range).
 __device__ inline int mx4_row(const Mx4Args& a, int s) {
   if (!a.perm) return s;

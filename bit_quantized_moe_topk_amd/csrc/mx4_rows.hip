@@ -8,6 +8,7 @@
 // matrix's bytes: each is read once per 16 rows.
 #include "mx4.h"
 
+#define TILES_PAY (mx4_row_tiles(a) * ((a.N + 127) / 128) >= 256)
 namespace moe {
 namespace {
 
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part
 }  // namespace
 
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
-  if (a.A >= 32LL * a.E_tot) {
+  if (TILES_PAY) {
     if (a.xdtype != kMx4) return launch_mx4_tiles(a, s);
     if (mx4_tiles4_can(a)) return launch_mx4_tiles4(a, s);
   }
@@ -213,6 +214,7 @@ hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
 }
 
 hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
+  if (TILES_PAY) return launch_mx4_grad_tiles(a, s);
   const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.K + kCols - 1) / kCols);
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
   if (a.xdtype == 1) MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<1>, g, dim3(256), 0, s, a, vec);

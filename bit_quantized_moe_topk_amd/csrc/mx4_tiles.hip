@@ -1,27 +1,26 @@
 // Products of many rows with a microscaled matrix on 32x32x16 matrix-core
 // tiles (bf16 weights converted in registers, bf16 or float32 rows).
 //
-// A workgroup takes up to 128 rows of one group and 256 rows of its matrix;
-// each of its four waves owns 64 matrix rows for all of the workgroup's rows.
-// A wave converts its own weights right before the products that use them
-// (four conversions for eight values, against up to four products), so the
-// matrix never enters LDS; the rows do, in stages of 64 columns, double
-// buffered, because every wave reads them all. Bound by the matrix cores.
+// A workgroup takes up to 128 rows of one group and a strip of its matrix;
+// each wave owns 64 matrix rows. A wave converts its own weights right before
+// the products that use them (four conversions for eight values, against up to
+// four products). Bound by the matrix cores, and for a few rows a group by the
+// matrix's bytes.
 #include "mx4_tile.h"
 
 namespace moe {
 namespace {
 
-constexpr int kTN = 256;   // matrix rows per tile
+constexpr int kTN = 256;   // matrix rows per tile of the general kernel: four waves across, two down
 constexpr int kTK = 64;    // columns per stage: two blocks
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 
 // One stage's products: R runs of 32 rows, 64 matrix rows, 64 columns. Lane
 // half h holds block h of the stage (codes c, scale sc), so product step kk
 // takes values 8 kk .. + 7 of both blocks.
 template <int R, int P>
-__device__ inline void stage_products(const uint4* xs, const uint4 (&c)[2], const float (&sc)[2],
-                                      floatx16_t (&acc)[4][2]) {
+__device__ inline void stage_products(const uint4* xs, int run0, const uint4 (&c)[2], const float (&sc)[2],
+                                      floatx16_t (&acc)[2][2]) {
   const int lane = threadIdx.x & 63, hq = 4 * (lane >> 5), r = lane & 31;
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
@@ -33,7 +32,7 @@ __device__ inline void stage_products(const uint4* xs, const uint4 (&c)[2], cons
     for (int p = P - 1; p >= 0; --p)
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const bf16x8_t x = __builtin_bit_cast(bf16x8_t, xs[p * kTM * 8 + chunk_at(32 * i + r, hq + kk)]);
+        const bf16x8_t x = __builtin_bit_cast(bf16x8_t, xs[p * kTM * 8 + chunk_at(32 * (run0 + i) + r, hq + kk)]);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x, acc[i][j], 0, 0, 0);
@@ -41,99 +40,118 @@ __device__ inline void stage_products(const uint4* xs, const uint4 (&c)[2], cons
   }
 }
 
-// Any K, stride and alignment, and float32 rows (P = 3 bf16 parts a value; bf16: 1): rows pass
-// through registers on their way to LDS, zeros in place of columns past K.
+// Any K, stride and alignment, and float32 rows (P = 3 bf16 parts a value;
+// bf16: 1). Rows pass through registers, zeros in place of columns past K: the
+// values of the stage after next are asked for before a stage's products and
+// go to LDS, split into their parts, before the next one's. The weights of the
+// next stage wait in registers.
 template <int P>
-__global__ __launch_bounds__(kThreads, P == 1 ? 2 : 1) void tiles_forward(Mx4Args a, bool vec) {
+__global__ __launch_bounds__(kThreads, 2) void tiles_forward(Mx4Args a, bool vec) {
   __shared__ uint4 xs[2][P * kTM * 8];
   __shared__ Tiles tiles;
   const int strips = (a.N + kTN - 1) / kTN;
   const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(xs), a) * strips;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, r = lane & 31;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r = lane & 31, wn = wave & 3, wm = wave >> 2;
   const int nb = mx4_blocks(a.K), S = (nb + 1) / 2;
   // consecutive items on one XCD (workgroup g runs on XCD g % 8): they share rows, or a matrix
   const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
   for (int item = pos; item < items; item += G) {
     const TileInfo t = tile_of(tiles, a, item, strips, kTN);
-    const int R = (t.M + 31) / 32;
-    // this wave's weights: matrix rows n0 + 64 wave + 32 j + r (past N: the last one, not stored)
+    const int R = (t.M + 31) / 32, run0 = wm ? (R + 1) / 2 : 0;
+    // this wave's weights: matrix rows n0 + 64 wn + 32 j + r (past N: the last one, not stored)
+    const int live = t.n0 + 64 * wn >= a.N ? 0 : wm ? R / 2 : (R + 1) / 2;
     const uint4* wc[2];
     const uint8_t* ws[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const size_t row = (size_t)t.e * a.N + min(t.n0 + 64 * wave + 32 * j + r, a.N - 1);
+      const size_t row = (size_t)t.e * a.N + min(t.n0 + 64 * wn + 32 * j + r, a.N - 1);
       wc[j] = reinterpret_cast<const uint4*>(a.wc) + row * nb;
       ws[j] = a.ws + row * nb;
     }
-    // rows of a stage: thread: row tid / 2, chunks 4 (tid % 2) .. + 3
-    const int m = tid >> 1;
+    // rows of a stage: thread: row tid / 4, chunks 2 (tid % 4) and + 1
+    const int m = tid >> 2, q0 = 2 * (tid & 3);
     const int xr = m < t.M ? mx4_row(a, t.s0 + m) : -1;
     const char* row = xr < 0 ? nullptr : static_cast<const char*>(a.x) + (size_t)xr * a.ldx * (P == 1 ? 2 : 4);
-    auto load_rows = [&](int s, int b) __attribute__((always_inline)) {
+    uint4 v1[2];
+    float v3[2][8];
+    auto ask = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int q = 4 * (tid & 1); q < 4 * (tid & 1) + 4; ++q) {
-        const int k = s * kTK + 8 * q;
+      for (int z = 0; z < 2; ++z) {
+        const int k = s * kTK + 8 * (q0 + z);
         if constexpr (P == 1) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (row && k < a.K) v = load8_bf16(reinterpret_cast<const uint16_t*>(row), k, a.K, vec);
-          xs[b][chunk_at(m, q)] = v;
+          v1[z] = make_uint4(0, 0, 0, 0);
+          if (row && k < a.K) v1[z] = load8_bf16(reinterpret_cast<const uint16_t*>(row), k, a.K, vec);
         } else {
-          float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (row && k < a.K) load8_f32(reinterpret_cast<const float*>(row), k, a.K, vec, f);
-          uint4 v0, v1, v2;
-          split3x8(f, v0, v1, v2);
-          xs[b][chunk_at(m, q)] = v0;
-          xs[b][kTM * 8 + chunk_at(m, q)] = v1;
-          xs[b][2 * kTM * 8 + chunk_at(m, q)] = v2;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v3[z][i] = 0.f;
+          if (row && k < a.K) load8_f32(reinterpret_cast<const float*>(row), k, a.K, vec, v3[z]);
         }
       }
     };
-    auto load_w = [&](int s, uint4 (&c)[2], float (&sc)[2]) __attribute__((always_inline)) {
+    auto put = [&](int b) __attribute__((always_inline)) {
+      if (m >= 32 * R) return;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        if constexpr (P == 1) {
+          xs[b][chunk_at(m, q0 + z)] = v1[z];
+        } else {
+          uint4 p0, p1, p2;
+          split3x8(v3[z], p0, p1, p2);
+          xs[b][chunk_at(m, q0 + z)] = p0;
+          xs[b][kTM * 8 + chunk_at(m, q0 + z)] = p1;
+          xs[b][2 * kTM * 8 + chunk_at(m, q0 + z)] = p2;
+        }
+      }
+    };
+    auto load_w = [&](int s, uint4 (&c)[2], uint32_t (&sc)[2]) __attribute__((always_inline)) {
       const int b = 2 * s + h;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         c[j] = make_uint4(0, 0, 0, 0);
-        uint32_t v = 0;
-        if (b < nb) {
+        sc[j] = 0;
+        if (live && b < nb) {
           c[j] = wc[j][b];
-          v = ws[j][b];
+          sc[j] = ws[j][b];
         }
-        sc[j] = mx4_scale(v);
       }
     };
-    floatx16_t acc[4][2];
+    floatx16_t acc[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) acc[i][j] = floatx16_t{};
     uint4 c[2], cn[2];
-    float sc[2], scn[2];
-    load_rows(0, 0);
-    load_w(0, c, sc);
+    uint32_t e[2], en[2];
+    ask(0);
+    load_w(0, c, e);
+    put(0);
+    if (S > 1) ask(1);
     __syncthreads();
     auto run = [&](auto RR) __attribute__((always_inline)) {
       constexpr int RN = decltype(RR)::value;
       for (int s = 0; s < S; ++s) {
         if (s + 1 < S) {
-          load_rows(s + 1, (s + 1) & 1);
-          load_w(s + 1, cn, scn);
+          load_w(s + 1, cn, en);
+          put((s + 1) & 1);
+          if (s + 2 < S) ask(s + 2);
         }
-        stage_products<RN, P>(xs[s & 1], c, sc, acc);
+        const float sc[2] = {mx4_scale(e[0]), mx4_scale(e[1])};
+        if constexpr (RN > 0) stage_products<RN, P>(xs[s & 1], run0, c, sc, acc);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           c[j] = cn[j];
-          sc[j] = scn[j];
+          e[j] = en[j];
         }
         __syncthreads();
       }
     };
-    if (R == 4) run(std::integral_constant<int, 4>{});
-    else if (R == 3) run(std::integral_constant<int, 3>{});
-    else if (R == 2) run(std::integral_constant<int, 2>{});
-    else run(std::integral_constant<int, 1>{});
+    if (live == 2) run(std::integral_constant<int, 2>{});
+    else if (live == 1) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 0>{});
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < R) store_run(a, acc[i], t.s0 + 32 * i, t.M - 32 * i, t.n0 + 64 * wave);
+    for (int i = 0; i < 2; ++i)
+      if (i < live) store_run(a, acc[i], t.s0 + 32 * (run0 + i), t.M - 32 * (run0 + i), t.n0 + 64 * wn);
   }
 }
 
@@ -178,6 +196,7 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   // those past the tile's repeat its last, and are not stored) and matrix rows (8 WN wave + 16 i +
   // l / 4, block l % 4 as placed), and the bases that advance by steps
   uint32_t xoff[2], woff[kWL], soff;
+  int xrows = 0;  // rows to load, in whole runs
   const char *xbase, *wbase, *sbase;
   int row_next[2];
   auto row_of = [&](int u) { return 16 * wave + 8 * u + (lane >> 3); };
@@ -192,6 +211,7 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
       xoff[u] = (uint32_t)row_next[u] * (uint32_t)(2 * a.ldx) + 16 * q;
     }
     xbase = static_cast<const char*>(a.x);
+    xrows = (t.M + 31) & ~31;
     wbase = reinterpret_cast<const char*>(a.wc) + (size_t)t.e * a.N * nb * 16;
     sbase = reinterpret_cast<const char*>(a.ws) + (size_t)t.e * a.N * nb;
 #pragma unroll
@@ -203,10 +223,12 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   };
   auto load = [&](int b) __attribute__((always_inline)) {
     StreamBuf<WN>& B = buf[b];
+    if (16 * wave < xrows) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      stream16(xbase, xoff[u], lds_offset(B.x[0]) + 1024 * (2 * wave + u));
-      stream16(xbase + 128, xoff[u], lds_offset(B.x[1]) + 1024 * (2 * wave + u));
+      for (int u = 0; u < 2; ++u) {
+        stream16(xbase, xoff[u], lds_offset(B.x[0]) + 1024 * (2 * wave + u));
+        stream16(xbase + 128, xoff[u], lds_offset(B.x[1]) + 1024 * (2 * wave + u));
+      }
     }
     xbase += 256;
 #pragma unroll
@@ -318,10 +340,13 @@ hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s) {
   // streamed: 32-bit offsets within one matrix and within the rows
   const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && a.K >= 2 * kStep && (long long)a.N * a.K < (1LL << 32) &&
                     (a.perm ? a.T : a.A) * a.ldx * 2 < (1LL << 32);
-  const int strip = !even ? kTN : a.N > 256 ? 512 : a.N > 128 ? 256 : 128;
-  const long long strips = (a.N + strip - 1) / strip;
-  const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * strips;
-  const int cap = (even ? 1 : 2) * device_cus();
+  // the widest strip that still gives every CU a tile: rows are read once a strip
+  const long long tiles = mx4_row_tiles(a);
+  const int cap = device_cus();
+  int strip = even ? 512 : kTN;
+  if (even && (tiles * ((a.N + 511) / 512) < cap || a.N <= 256)) strip = 256;
+  if (even && (tiles * ((a.N + 255) / 256) < cap || a.N <= 128)) strip = 128;
+  const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * ((a.N + strip - 1) / strip);
   const dim3 g((unsigned)(most < cap ? most : cap));
   if (!even && a.xdtype == 1) MOE_LAUNCH("mx4_tiles", s, tiles_forward<1>, g, dim3(kThreads), 0, s, a, vec);
   else if (!even) MOE_LAUNCH("mx4_tiles", s, tiles_forward<3>, g, dim3(kThreads), 0, s, a, vec);

@@ -36,7 +36,7 @@ __device__ inline uint2 load_scales(const uint8_t* row, int b, int nb) {
 // for more than it needs.
 template <bool QUADS>
 __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
-  constexpr int kLoads = QUADS ? 8 : 6;  // direct loads per wave and step
+  constexpr int kLoads = QUADS ? 6 : 4;  // direct loads per wave and step, besides the rows'
   __shared__ Buf4 buf[kBufs];
   __shared__ Tiles tiles;
   const int strips = (a.N + kN4 - 1) / kN4;
@@ -62,10 +62,12 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
     const int sr = QUADS ? 48 * wave + min(lane, 47) : min(tid, kTM + kN4 - 1);
     const uint8_t* srow = sr < kTM ? a.xs + (size_t)max(mx4_row(a, t.s0 + min(sr, t.M - 1)), 0) * nb
                                    : a.ws + ((size_t)t.e * a.N + min(t.n0 + sr - kTM, a.N - 1)) * nb;
+    const bool rows = 16 * wave < ((t.M + 31) & ~31);  // whether this wave loads rows
     auto load = [&](int p) __attribute__((always_inline)) {
       Buf4& B = buf[p % kBufs];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        if (!rows) break;
         const int m = 16 * wave + 8 * u + (lane >> 3);
         stream16(a.x, xoff[u] + 16 * min(kBlocks * p + (q ^ ((m >> 1) & 7)), nb - 1), lds_offset(B.x) + 1024 * (2 * wave + u));
       }
@@ -94,8 +96,12 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
       for (int j = 0; j < 2; ++j) acc[i][j] = floatx16_t{};
     load(0);
     if (P > 1) load(1);
-    if (P > 1) step_done<kLoads>();
-    else step_done();
+    auto done = [&](bool more) __attribute__((always_inline)) {  // all but the last load() have landed
+      if (!more) step_done();
+      else if (rows) step_done<kLoads + 2>();
+      else step_done<kLoads>();
+    };
+    done(P > 1);
     for (int p = 0; p < P; ++p) {
       if (p + 2 < P) load(p + 2);  // into step p - 1's buffer, which every wave has left
       const Buf4& B = buf[p % kBufs];
@@ -138,8 +144,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
         }
       }
       // the next step's loads have landed; this iteration's may be in flight
-      if (p + 2 < P) step_done<kLoads>();
-      else step_done();
+      done(p + 2 < P);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)

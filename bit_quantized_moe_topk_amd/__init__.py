@@ -509,7 +509,7 @@ def _call(name: str, dev: torch.device, *args) -> None:
 
 
 def _rows(name: str, t: torch.Tensor, n: int | None = None):
-    """Checks rows of float values ([R, n], values adjacent): (type code, elements from row to row)."""
+    """Checks rows of float values ([R, n], values adjacent): (type code, elements from row to row, R)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
     code = _FLOATS.get(t.dtype)
@@ -522,14 +522,14 @@ def _rows(name: str, t: torch.Tensor, n: int | None = None):
     ld, inner = t.stride()
     if R <= 1:
         ld = m
-    if (inner != 1 and m > 1) or ld < m:
+    if ld < m or (inner != 1 and m > 1):
         raise ValueError(f"{name} must have adjacent values in each row, and rows that do not overlap")
-    return code, ld
+    return code, ld, R
 
 
-def _int32(name: str, t: torch.Tensor, dev: torch.device, n: int | None = None):
-    _need_cuda(name, t, torch.int32)
-    if t.device != dev or (n is not None and t.numel() < n):
+def _int32(name: str, t: torch.Tensor, dev: torch.device, n: int = 0):
+    if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous() or t.numel() < n:
+        _need_cuda(name, t, torch.int32)
         raise ValueError(f"{name} must be on {dev}" + (f" and hold {n} values" if n else ""))
 
 
@@ -554,10 +554,9 @@ class Mx4:
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int):
         _need_cuda("codes", codes, torch.uint8)
         _need_cuda("scales", scales, torch.uint8)
-        *rows, n = codes.shape
-        *same, B = scales.shape
-        if K < 1 or not rows or B != (K + 31) // 32 or n != 16 * B or rows != same:
-            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not hold rows of {K}")
+        c, s = codes.shape, scales.shape
+        if K < 1 or len(c) < 2 or s[-1] != (K + 31) // 32 or c[-1] != 16 * s[-1] or c[:-1] != s[:-1]:
+            raise ValueError(f"codes {tuple(c)} and scales {tuple(s)} do not hold rows of {K}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
         self.codes, self.scales, self.K = codes, scales, K
@@ -580,14 +579,14 @@ def mx4_quantize(x: torch.Tensor, out: Mx4 | None = None) -> Mx4:
         raise ValueError("x must be a tensor [..., K] of two dimensions or more")
     K = x.shape[-1]
     flat = x if x.dim() == 2 else x.reshape(-1, K)
-    code, ld = _rows("x", flat)
+    code, ld, rows = _rows("x", flat)
     if out is None:
         B = (K + 31) // 32
         out = Mx4(torch.empty((*x.shape[:-1], 16 * B), dtype=torch.uint8, device=x.device),
                   torch.empty((*x.shape[:-1], B), dtype=torch.uint8, device=x.device), K)
     elif out.shape != tuple(x.shape) or out.device != x.device:
         raise ValueError(f"out must be an Mx4 of {tuple(x.shape)} on {x.device}")
-    _call("moe_mx4_quantize", x.device, flat.data_ptr(), code, ld, flat.shape[0], K, out.codes.data_ptr(),
+    _call("moe_mx4_quantize", x.device, flat.data_ptr(), code, ld, rows, K, out.codes.data_ptr(),
           out.scales.data_ptr())
     return out
 
@@ -606,18 +605,19 @@ def _product_rows(x, K: int):
         if x.codes.dim() != 2 or x.K != K:
             raise ValueError(f"x must be rows of {K} values: got {x.shape}")
         return x.codes.data_ptr(), x.scales.data_ptr(), MX4, 0, x.codes.shape[0], x.device, torch.bfloat16
-    code, ld = _rows("x", x, K)
-    return x.data_ptr(), None, code, ld, x.shape[0], x.device, x.dtype
+    code, ld, R = _rows("x", x, K)
+    return x.data_ptr(), None, code, ld, R, x.device, x.dtype
 
 
 def _matrix(w: Mx4, dims: int) -> int:
-    if not isinstance(w, Mx4) or w.codes.dim() != dims or w.codes.shape[-2] < 1:
+    shape = w.codes.shape if isinstance(w, Mx4) else ()
+    if len(shape) != dims or shape[-2] < 1:
         raise ValueError(f"w must be an Mx4 of {dims} dimensions, with a row at least")
-    return w.codes.shape[-2]
+    return shape[-2]
 
 
 def _same(name: str, w: Mx4, dev: torch.device):
-    if w.device != dev:
+    if w.codes.device != dev:
         raise ValueError(f"{name} must be on {dev}")
 
 
@@ -638,10 +638,10 @@ def mx4_matmul_backward(dy: torch.Tensor, w: Mx4, dtype: torch.dtype | None = No
     """The gradient of mx4_matmul for its rows: dy W, [T, K], for dy [T, N] (float32 or bfloat16; the
     result has its type unless `dtype` says otherwise). w is not trained."""
     N = _matrix(w, 2)
-    code, ld = _rows("dy", dy, N)
+    code, ld, T = _rows("dy", dy, N)
     _same("w", w, dy.device)
-    dx = _result(out, (dy.shape[0], w.K), dtype or dy.dtype, dy.device)
-    _call("moe_mx4_matmul_backward", dy.device, dy.data_ptr(), code, ld, dy.shape[0], w.codes.data_ptr(),
+    dx = _result(out, (T, w.K), dtype or dy.dtype, dy.device)
+    _call("moe_mx4_matmul_backward", dy.device, dy.data_ptr(), code, ld, T, w.codes.data_ptr(),
           w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dx.dtype])
     return dx
 
@@ -691,17 +691,17 @@ def mx4_experts_matmul_backward(dy: torch.Tensor, w: Mx4, grouping: Grouping, to
     """The gradient of mx4_experts_matmul for x: dy [A, N] in the groups' order -> [A, K], or, where
     `tokens` gives their number, [tokens, K], the sum over each token's assignments. w is not trained."""
     N = _matrix(w, 3)
-    code, ld = _rows("dy", dy, N)
+    code, ld, R = _rows("dy", dy, N)
     dev = dy.device
     _same("w", w, dev)
     T, k, E, shared, A = _groups(grouping, w, tokens, dev)
-    if dy.shape[0] != A:
-        raise ValueError(f"dy has {dy.shape[0]} rows, expected {A}")
+    if R != A:
+        raise ValueError(f"dy has {R} rows, expected {A}")
     gather = tokens is not None
     if gather:
         _int32("grouping.slot_of", grouping.slot_of, dev, A)
     dx = _result(out, (T, w.K), dtype or dy.dtype, dev)
-    n = lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, w.K, int(gather))
+    n = lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, w.K, 1) if gather else 0
     if workspace is None:
         workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     else:
@@ -740,18 +740,17 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tens
     """Per-expert counts, balance loss and z loss of a routed batch (moe_balance_loss): logits [T, E]
     (float32 or bfloat16), idx int32 [T, k] as route_topk gives it, token_mask bool [T] (False: a token
     that does not count, as padding)."""
-    code, ld = _rows("logits", logits)
-    T, E = logits.shape
+    code, ld, T = _rows("logits", logits)
+    E = logits.shape[1]
     dev = logits.device
     _int32("idx", idx, dev)
     if idx.dim() != 2 or idx.shape[0] != T:
         raise ValueError(f"idx must be [{T}, k]: got {tuple(idx.shape)}")
     k = idx.shape[1]
     keep = _token_mask(token_mask, T, dev)
-    if out is None:
-        out = BalanceLoss(torch.empty(2, dtype=torch.float32, device=dev),
-                          torch.empty(E, dtype=torch.int32, device=dev),
-                          torch.empty(1, dtype=torch.int32, device=dev), k)
+    if out is None:  # parts of one tensor
+        losses, kept, counts = torch.empty(E + 3, dtype=torch.int32, device=dev).split_with_sizes((2, 1, E))
+        out = BalanceLoss(losses.view(torch.float32), counts, kept, k)
     else:
         _need_cuda("out.losses", out.losses, torch.float32)
         _int32("out.counts", out.counts, dev)
@@ -759,8 +758,8 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tens
         if out.losses.numel() != 2 or out.counts.numel() != E or out.kept.numel() != 1 or out.losses.device != dev:
             raise ValueError("out does not match the logits")
         out.k = k
-    n = lib().moe_balance_loss_workspace_size(T, k, E)
     if workspace is None:
+        n = lib().moe_balance_loss_workspace_size(T, k, E)
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
     else:
         _need_cuda("workspace", workspace, torch.uint8)
@@ -775,8 +774,8 @@ def balance_loss_backward(logits: torch.Tensor, loss: BalanceLoss, d_losses: tor
                           token_mask: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """The gradient of balance_loss for the logits, [T, E] in their type, from the gradients d_losses
     (float32 [2], on the device) of its two losses; `loss` and `token_mask` as the forward call had them."""
-    code, ld = _rows("logits", logits)
-    T, E = logits.shape
+    code, ld, T = _rows("logits", logits)
+    E = logits.shape[1]
     dev = logits.device
     _need_cuda("d_losses", d_losses, torch.float32)
     if d_losses.numel() != 2 or d_losses.device != dev:

@@ -11,7 +11,8 @@
 // the logits, one wave a token, gives both losses through the two scalars
 // f . p_t and lse_t: no column sums of p, and nothing as large as the logits,
 // is kept. The gradient is one more pass that reads the logits and writes as
-// many values. Bound by those bytes; small batches by their launches.
+// many values. Bound by those bytes; small batches, which one workgroup counts
+// and sums in one launch, by its latency.
 //
 // Sums are float32 in a fixed order (per wave over its tokens, then over the
 // waves in order), counts are integers: results do not vary from run to run.
@@ -23,9 +24,13 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 4;         // tokens in flight per workgroup
+constexpr int kSmallWaves = 16;   // the same of the one-launch form
+constexpr int kSmallT = 128;      // its most tokens
+constexpr int kSmallIds = 4096;   // and ids
 constexpr int kCountIds = 4096;   // ids per counting workgroup
 constexpr int kCountGroups = 64;  // most counting workgroups
-constexpr int kRowGroups = 512;   // most workgroups of the pass over the logits
+constexpr int kRowGroups = 1024;  // most workgroups of the pass over the logits
+constexpr int kLines = 16;        // counters of finished workgroups, a line each, before the last one
 
 struct BalanceArgs {
   const void* logits;
@@ -40,47 +45,79 @@ struct BalanceArgs {
   void* dx;             // [T][E]
   int32_t* wcounts;     // workspace: [G][E + 1] counts of each counting workgroup, its kept tokens last
   float* wsums;         // [kRowGroups][2]
-  uint32_t* done;
+  uint32_t* done;       // [kLines + 1], 32 words apart
 };
 
-__device__ inline float load_logit(const BalanceArgs& a, size_t i) {
-  return a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[i] << 16)
-                : static_cast<const float*>(a.logits)[i];
-}
-
-// Counting workgroup b of G: the ids of tokens [b T / G, (b + 1) T / G) in an LDS histogram.
-__global__ __launch_bounds__(256) void balance_count(BalanceArgs a) {
-  __shared__ int32_t h[MOE_MAX_E_DEV + 1];
-  const int G = gridDim.x, b = blockIdx.x, tid = threadIdx.x;
-  for (int e = tid; e <= a.E; e += 256) h[e] = 0;
-  __syncthreads();
-  const int t0 = (int)((long long)b * a.T / G), t1 = (int)((long long)(b + 1) * a.T / G);
-  for (long long i = (long long)t0 * a.k + tid; i < (long long)t1 * a.k; i += 256) {
-    const int e = a.idx[i];
-    if ((unsigned)e < (unsigned)a.E && (!a.keep || a.keep[i / a.k])) atomicAdd(&h[e], 1);
-  }
-  int n = 0;
-  for (int t = t0 + tid; t < t1; t += 256) n += !a.keep || a.keep[t] ? 1 : 0;
-  if (n) atomicAdd(&h[a.E], n);
-  __syncthreads();
-  for (int e = tid; e <= a.E; e += 256) a.wcounts[(size_t)b * (a.E + 1) + e] = h[e];
-  if (b == 0 && tid == 0) *a.done = 0u;
-}
-
-// A token's logits in registers (column lane + 64 i in slot i), exp(x - max)
-// in their place; *lse and 1 / sum. A token whose logits are all -inf has no
-// distribution: p is 0 and lse 0.
-template <int P>
-__device__ inline void softmax_row(const BalanceArgs& a, int t, float (&x)[P], float* lse, float* inv) {
+// Columns of a lane: P of them, one at a time (lane + 64 i in slot i), or with
+// VEC in fours (4 (lane + 64 (i / 4)) + i % 4).
+template <bool VEC>
+__device__ inline int column(int i) {
   const int lane = threadIdx.x & 63;
+  return VEC ? 4 * (lane + 64 * (i >> 2)) + (i & 3) : lane + 64 * i;
+}
+
+// A token's logits as they lie in memory: P dwords, or P / 2 for bf16 in fours.
+template <int P, bool VEC>
+struct RawRow {
+  uint32_t v[P];
+};
+template <int P, bool VEC>
+__device__ inline void load_raw(const BalanceArgs& a, int t, RawRow<P, VEC>& raw) {
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+      const int c = column<VEC>(i);
+      if (c >= a.E) continue;
+      if (a.bf16) {
+        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + (size_t)t * a.ld + c);
+        raw.v[i] = u.x << 16;
+        raw.v[i + 1] = u.x & 0xFFFF0000u;
+        raw.v[i + 2] = u.y << 16;
+        raw.v[i + 3] = u.y & 0xFFFF0000u;
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const float*>(a.logits) + (size_t)t * a.ld + c);
+        raw.v[i] = u.x;
+        raw.v[i + 1] = u.y;
+        raw.v[i + 2] = u.z;
+        raw.v[i + 3] = u.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int c = column<VEC>(i);
+      if (c >= a.E) continue;
+      const size_t at = (size_t)t * a.ld + c;
+      raw.v[i] = a.bf16 ? (uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16
+                        : __float_as_uint(static_cast<const float*>(a.logits)[at]);
+    }
+  }
+}
+
+__device__ inline float wave_maxf(float v) {
+  v = fmaxf(v, __uint_as_float(dpp(__float_as_uint(v), 0xB1)));
+  v = fmaxf(v, __uint_as_float(dpp(__float_as_uint(v), 0x4E)));
+  v = fmaxf(v, __uint_as_float(dpp(__float_as_uint(v), 0x141)));
+  v = fmaxf(v, __uint_as_float(dpp(__float_as_uint(v), 0x140)));
+  const float r0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 0));
+  const float r1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 16));
+  const float r2 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 32));
+  const float r3 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 48));
+  return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
+}
+
+// exp(x - max) of a token's logits; *lse and 1 / sum. A token whose logits are
+// all -inf has no distribution: p is 0 and lse 0.
+template <int P, bool VEC>
+__device__ inline void softmax_row(const BalanceArgs& a, const RawRow<P, VEC>& raw, float (&x)[P], float* lse,
+                                   float* inv) {
   float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    x[i] = lane + 64 * i < a.E ? load_logit(a, (size_t)t * a.ld + lane + 64 * i) : -INFINITY;
+    x[i] = column<VEC>(i) < a.E ? __uint_as_float(raw.v[i]) : -INFINITY;
     top = fmaxf(top, x[i]);
   }
-#pragma unroll
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  top = wave_maxf(top);
   float sum = 0.f;
   const bool none = top == -INFINITY;
 #pragma unroll
@@ -94,20 +131,129 @@ __device__ inline void softmax_row(const BalanceArgs& a, int t, float (&x)[P], f
   *lse = sum == 0.f ? 0.f : top + logf(sum);
 }
 
-// f[slot] / (n k) of this lane's columns, from the finished counts.
-template <int P>
+// f of this lane's columns, from the finished counts.
+template <int P, bool VEC>
 __device__ inline void load_share(const int32_t* counts, int n, const BalanceArgs& a, float (&f)[P]) {
-  const int lane = threadIdx.x & 63;
   const float total = (float)n * (float)a.k;
 #pragma unroll
   for (int i = 0; i < P; ++i)
-    f[i] = lane + 64 * i < a.E && n > 0 ? (float)counts[lane + 64 * i] / total : 0.f;
+    f[i] = column<VEC>(i) < a.E && n > 0 ? (float)counts[column<VEC>(i)] / total : 0.f;
+}
+
+// Counts the ids of tokens [t0, t1) into the LDS histogram h[0 .. E], their
+// kept tokens in h[E]; the workgroup's threads together, eight loads in flight each.
+__device__ inline void count_ids(const BalanceArgs& a, int t0, int t1, int32_t* h) {
+  const int tid = threadIdx.x, n = blockDim.x;
+  for (int e = tid; e <= a.E; e += n) h[e] = 0;
+  __syncthreads();
+  const long long end = (long long)t1 * a.k;
+  for (long long i = (long long)t0 * a.k + tid; i < end; i += 8 * n) {
+    int e[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      const long long j = i + z * n;
+      e[z] = j < end ? a.idx[j] : -1;
+    }
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if ((unsigned)e[z] < (unsigned)a.E && (!a.keep || a.keep[(int)((unsigned)(i + z * n) / (unsigned)a.k)]))
+        atomicAdd(&h[e[z]], 1);
+  }
+  if (a.keep) {
+    int kept = 0;
+    for (int t = t0 + tid; t < t1; t += n) kept += a.keep[t] ? 1 : 0;
+    if (kept) atomicAdd(&h[a.E], kept);
+  } else if (tid == 0) {
+    h[a.E] = t1 - t0;
+  }
+  __syncthreads();
+}
+
+// The sums of f . p_t and lse_t^2 over tokens t0, t0 + step, ..; the next
+// token's logits are on their way while one is summed.
+template <int P, bool VEC>
+__device__ inline void sum_rows(const BalanceArgs& a, const float (&f)[P], int t0, int step, float* fp, float* zz) {
+  *fp = 0.f;
+  *zz = 0.f;
+  RawRow<P, VEC> raw, next;
+  int t = t0;
+  if (t < a.T) load_raw(a, t, raw);
+  while (t < a.T) {
+    const int tn = t + step;
+    if (tn < a.T) load_raw(a, tn, next);
+    if (!a.keep || a.keep[t]) {
+      float x[P], lse, inv, dot = 0.f;
+      softmax_row<P, VEC>(a, raw, x, &lse, &inv);
+#pragma unroll
+      for (int i = 0; i < P; ++i) dot = fmaf(f[i], x[i], dot);
+      *fp += wave_sum(dot) * inv;
+      *zz += lse * lse;
+    }
+    raw = next;
+    t = tn;
+  }
+}
+
+__device__ inline void write_losses(const BalanceArgs& a, float fp, float zz, int n) {
+  a.losses[0] = n ? fp * ((float)a.E / (float)n) : 0.f;
+  a.losses[1] = n ? zz / (float)n : 0.f;
+}
+
+// A small batch in one workgroup: counts, then the pass.
+template <int P, bool VEC>
+__global__ __launch_bounds__(64 * kSmallWaves) void balance_small(BalanceArgs a) {
+  __shared__ int32_t cnt[MOE_MAX_E_DEV + 1];
+  __shared__ float ws[kSmallWaves][2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  count_ids(a, 0, a.T, cnt);
+  for (int e = tid; e <= a.E; e += 64 * kSmallWaves) {
+    if (e < a.E) a.counts[e] = cnt[e];
+    else *a.kept = cnt[e];
+  }
+  const int n = cnt[a.E];
+  float f[P], fp, zz;
+  load_share<P, VEC>(cnt, n, a, f);
+  sum_rows<P, VEC>(a, f, wave, kSmallWaves, &fp, &zz);
+  if (lane == 0) {
+    ws[wave][0] = fp;
+    ws[wave][1] = zz;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    fp = zz = 0.f;
+    for (int w = 0; w < kSmallWaves; ++w) {
+      fp += ws[w][0];
+      zz += ws[w][1];
+    }
+    write_losses(a, fp, zz, n);
+  }
+}
+
+// Counting workgroup b of G: the ids of tokens [b T / G, (b + 1) T / G).
+__global__ __launch_bounds__(256) void balance_count(BalanceArgs a) {
+  __shared__ int32_t h[MOE_MAX_E_DEV + 1];
+  const int G = gridDim.x, b = blockIdx.x;
+  count_ids(a, (int)((long long)b * a.T / G), (int)((long long)(b + 1) * a.T / G), h);
+  for (int e = threadIdx.x; e <= a.E; e += 256) a.wcounts[(size_t)b * (a.E + 1) + e] = h[e];
+  if (b == 0 && threadIdx.x <= kLines) a.done[32 * threadIdx.x] = 0u;
+}
+
+// Whether this is the last workgroup: each counts itself on one of kLines
+// lines, the last of a line counts the line. (One counter for all of them took
+// 20 us of the pass over 8,192 tokens: adds to one address queue up.) The
+// workgroup's sums are stored past the caches, and have arrived, before.
+__device__ inline bool last_workgroup(uint32_t* done) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  const int G = gridDim.x, line = blockIdx.x % kLines;
+  const uint32_t of = (uint32_t)((G - line + kLines - 1) / kLines), lines = (uint32_t)min(G, kLines);
+  if (__hip_atomic_fetch_add(done + 32 * line, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != of - 1) return false;
+  return __hip_atomic_fetch_add(done + 32 * kLines, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == lines - 1;
 }
 
 // Pass over the logits. Every workgroup adds up the counting workgroups'
 // counts (the first also writes them out); the last one to finish adds up the
 // workgroups' sums in order.
-template <int P>
+template <int P, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void balance_rows(BalanceArgs a, int G) {
   __shared__ int32_t cnt[MOE_MAX_E_DEV + 1];
   __shared__ float ws[kWaves][2];
@@ -115,6 +261,7 @@ __global__ __launch_bounds__(64 * kWaves) void balance_rows(BalanceArgs a, int G
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e <= a.E; e += 64 * kWaves) {
     int c = 0;
+#pragma unroll 8
     for (int b = 0; b < G; ++b) c += a.wcounts[(size_t)b * (a.E + 1) + e];
     cnt[e] = c;
     if (blockIdx.x == 0) {
@@ -124,17 +271,9 @@ __global__ __launch_bounds__(64 * kWaves) void balance_rows(BalanceArgs a, int G
   }
   __syncthreads();
   const int n = cnt[a.E];
-  float f[P], fp = 0.f, zz = 0.f;
-  load_share<P>(cnt, n, a, f);
-  for (int t = blockIdx.x * kWaves + wave; t < a.T; t += gridDim.x * kWaves) {
-    if (a.keep && !a.keep[t]) continue;
-    float x[P], lse, inv, dot = 0.f;
-    softmax_row<P>(a, t, x, &lse, &inv);
-#pragma unroll
-    for (int i = 0; i < P; ++i) dot = fmaf(f[i], x[i], dot);
-    fp += wave_sum(dot) * inv;
-    zz += lse * lse;
-  }
+  float f[P], fp, zz;
+  load_share<P, VEC>(cnt, n, a, f);
+  sum_rows<P, VEC>(a, f, blockIdx.x * kWaves + wave, gridDim.x * kWaves, &fp, &zz);
   if (lane == 0) {
     ws[wave][0] = fp;
     ws[wave][1] = zz;
@@ -148,47 +287,70 @@ __global__ __launch_bounds__(64 * kWaves) void balance_rows(BalanceArgs a, int G
     }
     __hip_atomic_store(&a.wsums[2 * blockIdx.x], s0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(&a.wsums[2 * blockIdx.x + 1], s1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    last = last_workgroup(a.done);
   }
   __syncthreads();
   if (!last || wave) return;
   float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
   for (int b = lane; b < (int)gridDim.x; b += 64) {
     s0 += __hip_atomic_load(&a.wsums[2 * b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     s1 += __hip_atomic_load(&a.wsums[2 * b + 1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   s0 = wave_sum(s0);
   s1 = wave_sum(s1);
-  if (lane == 0) {
-    a.losses[0] = n ? s0 * ((float)a.E / (float)n) : 0.f;
-    a.losses[1] = n ? s1 / (float)n : 0.f;
-  }
+  if (lane == 0) write_losses(a, s0, s1, n);
 }
 
-template <int P>
+template <int P, bool VEC>
 __global__ __launch_bounds__(64 * kWaves) void balance_gradient(BalanceArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6, step = gridDim.x * kWaves;
+  int t = blockIdx.x * kWaves + wave;
+  if (t >= a.T) return;
+  RawRow<P, VEC> raw, next;
+  load_raw(a, t, raw);
   const int n = *a.kept;
   float f[P];
-  load_share<P>(a.counts, n, a, f);
+  load_share<P, VEC>(a.counts, n, a, f);
   const float cb = n ? a.d[0] * ((float)a.E / (float)n) : 0.f, cz = n ? a.d[1] * (2.f / (float)n) : 0.f;
-  for (int t = blockIdx.x * kWaves + wave; t < a.T; t += gridDim.x * kWaves) {
+  for (;;) {
+    const int tn = t + step;
+    if (tn < a.T) load_raw(a, tn, next);
     float x[P], lse = 0.f, inv = 0.f, dot = 0.f;
     const bool keep = !a.keep || a.keep[t];
     if (keep) {
-      softmax_row<P>(a, t, x, &lse, &inv);
+      softmax_row<P, VEC>(a, raw, x, &lse, &inv);
 #pragma unroll
       for (int i = 0; i < P; ++i) dot = fmaf(f[i], x[i], dot);
       dot = wave_sum(dot) * inv;
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = lane + 64 * i;
-      if (e >= a.E) continue;
-      const float v = keep ? x[i] * inv * fmaf(cb, f[i] - dot, cz * lse) : 0.f;
-      if (a.bf16) static_cast<uint16_t*>(a.dx)[(size_t)t * a.E + e] = (uint16_t)f32_to_bf16_bits(v);
-      else static_cast<float*>(a.dx)[(size_t)t * a.E + e] = v;
+    for (int i = 0; i < P; ++i) x[i] = keep ? x[i] * inv * fmaf(cb, f[i] - dot, cz * lse) : 0.f;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < P; i += 4) {
+        const int c = column<VEC>(i);
+        if (c >= a.E) continue;
+        if (a.bf16)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dx) + (size_t)t * a.E + c) =
+              make_uint2(f32_to_bf16_bits(x[i]) | f32_to_bf16_bits(x[i + 1]) << 16,
+                         f32_to_bf16_bits(x[i + 2]) | f32_to_bf16_bits(x[i + 3]) << 16);
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.dx) + (size_t)t * a.E + c) =
+              make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int c = column<VEC>(i);
+        if (c >= a.E) continue;
+        if (a.bf16) static_cast<uint16_t*>(a.dx)[(size_t)t * a.E + c] = (uint16_t)f32_to_bf16_bits(x[i]);
+        else static_cast<float*>(a.dx)[(size_t)t * a.E + c] = x[i];
+      }
     }
+    if (tn >= a.T) break;
+    raw = next;
+    t = tn;
   }
 }
 
@@ -202,33 +364,52 @@ int row_groups(int T) {
   return g < 1 ? 1 : g > kRowGroups ? kRowGroups : g;
 }
 
-template <int P>
+template <int P, bool VEC>
 void launch_rows(const BalanceArgs& a, hipStream_t s) {
-  MOE_LAUNCH("balance_rows", s, balance_rows<P>, dim3(row_groups(a.T)), dim3(64 * kWaves), 0, s, a,
-             count_groups(a.T, a.k));
+  if (a.T <= kSmallT && (long long)a.T * a.k <= kSmallIds) {
+    MOE_LAUNCH("balance_small", s, (balance_small<P, VEC>), dim3(1), dim3(64 * kSmallWaves), 0, s, a);
+    return;
+  }
+  const int G = count_groups(a.T, a.k);
+  MOE_LAUNCH("balance_count", s, balance_count, dim3(G), dim3(256), 0, s, a);
+  MOE_LAUNCH("balance_rows", s, (balance_rows<P, VEC>), dim3(row_groups(a.T)), dim3(64 * kWaves), 0, s, a, G);
 }
-template <int P>
+template <int P, bool VEC>
 void launch_grad(const BalanceArgs& a, hipStream_t s) {
   const int g = (a.T + kWaves - 1) / kWaves, most = 8 * device_cus();
-  MOE_LAUNCH("balance_gradient", s, balance_gradient<P>, dim3(g < most ? g : most), dim3(64 * kWaves), 0, s, a);
+  MOE_LAUNCH("balance_gradient", s, (balance_gradient<P, VEC>), dim3(g < most ? g : most), dim3(64 * kWaves), 0, s, a);
 }
 
-#define BALANCE_BY_E(E, CALL)            \
-  do {                                   \
-    const int per_ = ((E) + 63) / 64;    \
-    if (per_ <= 1) CALL(1);              \
-    else if (per_ <= 2) CALL(2);         \
-    else if (per_ <= 4) CALL(4);         \
-    else if (per_ <= 8) CALL(8);         \
-    else if (per_ <= 16) CALL(16);       \
-    else CALL(32);                       \
+// Columns per lane for E, in fours where every row starts and ends on a group of four.
+#define BALANCE_BY_E(E, VEC4, CALL)               \
+  do {                                            \
+    const int per_ = ((E) + 63) / 64;             \
+    if (VEC4) {                                   \
+      if (per_ <= 4) CALL(4, true);               \
+      else if (per_ <= 8) CALL(8, true);          \
+      else if (per_ <= 16) CALL(16, true);        \
+      else CALL(32, true);                        \
+    } else if (per_ <= 1) CALL(1, false);         \
+    else if (per_ <= 2) CALL(2, false);           \
+    else if (per_ <= 4) CALL(4, false);           \
+    else if (per_ <= 8) CALL(8, false);           \
+    else if (per_ <= 16) CALL(16, false);         \
+    else CALL(32, false);                         \
   } while (0)
+
+// E > 128: fewer experts fill the wave better one at a time.
+bool in_fours(const void* p, long long ld, const void* q, int E, int bf16) {
+  const unsigned size = bf16 ? 8 : 16;
+  return E > 128 && E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % size == 0 &&
+         reinterpret_cast<uintptr_t>(q) % size == 0;
+}
 
 }  // namespace
 
 // Workspace: the row workgroups' sums, the finished counter, the counts.
+constexpr size_t kSumBytes = sizeof(float) * 2 * kRowGroups, kDoneBytes = 128 * (kLines + 1);
 size_t balance_workspace_bytes(int T, int k, int E) {
-  return sizeof(float) * 2 * kRowGroups + 256 + sizeof(int32_t) * (size_t)count_groups(T, k) * (E + 1);
+  return kSumBytes + kDoneBytes + sizeof(int32_t) * (size_t)count_groups(T, k) * (E + 1);
 }
 
 hipError_t launch_balance(const void* logits, int dtype, long long ld, int T, int E, int k, const int32_t* idx,
@@ -248,11 +429,10 @@ hipError_t launch_balance(const void* logits, int dtype, long long ld, int T, in
   a.kept = kept;
   char* p = static_cast<char*>(ws);
   a.wsums = reinterpret_cast<float*>(p);
-  a.done = reinterpret_cast<uint32_t*>(p + sizeof(float) * 2 * kRowGroups);
-  a.wcounts = reinterpret_cast<int32_t*>(p + sizeof(float) * 2 * kRowGroups + 256);
-  MOE_LAUNCH("balance_count", s, balance_count, dim3(count_groups(T, k)), dim3(256), 0, s, a);
-#define ROWS(P) launch_rows<P>(a, s)
-  BALANCE_BY_E(E, ROWS);
+  a.done = reinterpret_cast<uint32_t*>(p + kSumBytes);
+  a.wcounts = reinterpret_cast<int32_t*>(p + kSumBytes + kDoneBytes);
+#define ROWS(P, V) launch_rows<P, V>(a, s)
+  BALANCE_BY_E(E, in_fours(logits, ld, nullptr, E, a.bf16), ROWS);
 #undef ROWS
   return hipGetLastError();
 }
@@ -272,8 +452,8 @@ hipError_t launch_balance_gradient(const void* logits, int dtype, long long ld, 
   a.kept = const_cast<int32_t*>(kept);
   a.d = d;
   a.dx = dx;
-#define GRAD(P) launch_grad<P>(a, s)
-  BALANCE_BY_E(E, GRAD);
+#define GRAD(P, V) launch_grad<P, V>(a, s)
+  BALANCE_BY_E(E, in_fours(logits, ld, dx, E, a.bf16), GRAD);
 #undef GRAD
   return hipGetLastError();
 }

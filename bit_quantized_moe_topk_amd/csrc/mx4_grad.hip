@@ -56,13 +56,15 @@ __device__ inline int code_at(int n, int c) {
 
 // STREAM: dy bf16, its rows readable 16 bytes at a time, N a multiple of 64,
 // scales readable four at a time: everything comes by direct loads, two stages
-// ahead in three buffers. Else through registers, one stage ahead in two.
+// ahead in three buffers. Else through registers, one stage ahead in two. The
+// loads run on across tiles.
 template <int P, int WK, bool STREAM>
 __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Args a, bool vec) {
   constexpr int kBufs = STREAM ? 3 : 2, kThreads = 128 * WK;
   constexpr int kDL = 16 / (2 * WK), kWL = kGN * 4 * WK / 64 / (2 * WK);  // direct loads a wave and stage
   __shared__ GradBuf<P, WK> buf[kBufs];
   __shared__ Tiles tiles;
+  __shared__ floatx4_t meet[2 * WK][4][64];
   constexpr int strip = 128 * WK;
   const int strips = (a.K + strip - 1) / strip;
   const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(buf), a) * strips;
@@ -70,83 +72,104 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
   const int r = lane & 15, g = lane >> 4, wk = wave % WK, wm = wave / WK;
   const int nb = mx4_blocks(a.K), S = (a.N + kGN - 1) / kGN;
   const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
-  for (int item = pos; item < items; item += G) {
-    const TileInfo t = tile_of(tiles, a, item, strips, strip);  // n0: its first column
-    const int b0 = t.n0 / 32;                                   // its first block
-    const char* wbase = reinterpret_cast<const char*>(a.wc) + (size_t)t.e * a.N * nb * 16;
-    const uint8_t* sbase = a.ws + (size_t)t.e * a.N * nb;
-    const bool rows = 8 * kDL * wave < ((t.M + 15) & ~15);  // whether this wave loads rows of dy
-    auto load = [&](int s) __attribute__((always_inline)) {
-      GradBuf<P, WK>& B = buf[s % kBufs];
-      if constexpr (STREAM) {
+  if (pos >= items) return;
+  // load cursor: stage ls of tile lt, into buffer lb
+  TileInfo lt = tile_of(tiles, a, pos, strips, strip);  // n0: its first column
+  int litem = pos, ls = 0, lb = 0;
+  bool rows = false;  // whether this wave's last load() brought rows of dy
+  // the next stage, of whatever tile it is; false: there is none
+  auto load = [&]() __attribute__((always_inline)) {
+    if (ls == S) {
+      if (litem + G >= items) return false;
+      litem += G;
+      lt = tile_of(tiles, a, litem, strips, strip);
+      ls = 0;
+    }
+    const int s = ls++, b0 = lt.n0 / 32;
+    const char* wbase = reinterpret_cast<const char*>(a.wc) + (size_t)lt.e * a.N * nb * 16;
+    const uint8_t* sbase = a.ws + (size_t)lt.e * a.N * nb;
+    GradBuf<P, WK>& B = buf[lb];
+    lb = lb + 1 == kBufs ? 0 : lb + 1;
+    rows = 8 * kDL * wave < ((lt.M + 15) & ~15);
+    if constexpr (STREAM) {
 #pragma unroll
-        for (int u = 0; u < kDL; ++u) {
-          if (!rows) break;
-          const int m = 8 * (kDL * wave + u) + (lane >> 3);
-          const int row = t.s0 + min(m, t.M - 1);
-          stream16(static_cast<const char*>(a.x) + s * 2 * kGN,
-                   (uint32_t)row * (uint32_t)(2 * a.ldx) + 16 * ((lane & 7) ^ ((m >> 1) & 7)),
-                   lds_offset(B.d[0]) + 1024 * (kDL * wave + u));
-        }
+      for (int u = 0; u < kDL; ++u) {
+        if (!rows) break;
+        const int m = 8 * (kDL * wave + u) + (lane >> 3);
+        const int row = lt.s0 + min(m, lt.M - 1);
+        stream16(static_cast<const char*>(a.x) + s * 2 * kGN,
+                 (uint32_t)row * (uint32_t)(2 * a.ldx) + 16 * ((lane & 7) ^ ((m >> 1) & 7)),
+                 lds_offset(B.d[0]) + 1024 * (kDL * wave + u));
+      }
 #pragma unroll
-        for (int u = 0; u < kWL; ++u) {
-          const int at = 64 * (kWL * wave + u) + lane, n = at / (4 * WK);
-          const int c = (at % (4 * WK)) ^ (4 * ((n >> 3) & (WK - 1)));
-          stream16(wbase, (uint32_t)(s * kGN + n) * (uint32_t)(16 * nb) + 16 * min(b0 + c, nb - 1),
-                   lds_offset(B.w) + 1024 * (kWL * wave + u));
-        }
-        if (lane < 32) {
-          const int at = 32 * wave + lane, n = at / WK, z = at % WK;
-          stream4(sbase, (uint32_t)(s * kGN + n) * nb + min(b0 + 4 * z, nb - 4), lds_offset(B.s) + 128 * wave);
-        }
-      } else {
+      for (int u = 0; u < kWL; ++u) {
+        const int at = 64 * (kWL * wave + u) + lane, n = at / (4 * WK);
+        const int c = (at % (4 * WK)) ^ (4 * ((n >> 3) & (WK - 1)));
+        stream16(wbase, (uint32_t)(s * kGN + n) * (uint32_t)(16 * nb) + 16 * min(b0 + c, nb - 1),
+                 lds_offset(B.w) + 1024 * (kWL * wave + u));
+      }
+      if (lane < 32) {
+        const int at = 32 * wave + lane, n = at / WK, z = at % WK;
+        stream4(sbase, (uint32_t)(s * kGN + n) * nb + min(b0 + 4 * z, nb - 4), lds_offset(B.s) + 128 * wave);
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < kTM * 8 / kThreads; ++i) {
-          const int at = i * kThreads + tid, m = at / 8, q = at % 8, n = s * kGN + 8 * q;
-          const size_t row = (size_t)(t.s0 + m) * a.ldx;
-          const bool there = m < t.M && n < a.N;
-          if constexpr (P == 1) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (there) v = load8_bf16(static_cast<const uint16_t*>(a.x) + row, n, a.N, vec);
-            B.d[0][chunk_at(m, q)] = v;
-          } else {
-            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (there) load8_f32(static_cast<const float*>(a.x) + row, n, a.N, vec, f);
-            split3x8(f, B.d[0][chunk_at(m, q)], B.d[P > 1 ? 1 : 0][chunk_at(m, q)], B.d[P > 1 ? 2 : 0][chunk_at(m, q)]);
-          }
-        }
-        // matrix rows past N: scales of 2^-127, zeros in dy
-#pragma unroll
-        for (int i = 0; i < kGN * 4 * WK / kThreads; ++i) {
-          const int at = i * kThreads + tid, n = at / (4 * WK), c = at % (4 * WK);
-          const size_t blk = (size_t)min(s * kGN + n, a.N - 1) * nb + min(b0 + c, nb - 1);
-          B.w[code_at<WK>(n, c)] = *reinterpret_cast<const uint4*>(wbase + 16 * blk);
-          B.s[at] = s * kGN + n < a.N ? sbase[blk] : 0;
+      for (int i = 0; i < kTM * 8 / kThreads; ++i) {
+        const int at = i * kThreads + tid, m = at / 8, q = at % 8, n = s * kGN + 8 * q;
+        const size_t row = (size_t)(lt.s0 + m) * a.ldx;
+        const bool there = m < lt.M && n < a.N;
+        if constexpr (P == 1) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (there) v = load8_bf16(static_cast<const uint16_t*>(a.x) + row, n, a.N, vec);
+          B.d[0][chunk_at(m, q)] = v;
+        } else {
+          float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (there) load8_f32(static_cast<const float*>(a.x) + row, n, a.N, vec, f);
+          split3x8(f, B.d[0][chunk_at(m, q)], B.d[P > 1 ? 1 : 0][chunk_at(m, q)], B.d[P > 1 ? 2 : 0][chunk_at(m, q)]);
         }
       }
-    };
-    const int U = (t.M + 15) / 16, u0 = wm ? (U + 1) / 2 : 0, live = wm ? U / 2 : (U + 1) / 2;
+      // matrix rows past N: scales of 2^-127, zeros in dy
+#pragma unroll
+      for (int i = 0; i < kGN * 4 * WK / kThreads; ++i) {
+        const int at = i * kThreads + tid, n = at / (4 * WK), c = at % (4 * WK);
+        const size_t blk = (size_t)min(s * kGN + n, a.N - 1) * nb + min(b0 + c, nb - 1);
+        B.w[code_at<WK>(n, c)] = *reinterpret_cast<const uint4*>(wbase + 16 * blk);
+        B.s[at] = s * kGN + n < a.N ? sbase[blk] : 0;
+      }
+    }
+    return true;
+  };
+  bool more = load();
+  if (STREAM) more = load();
+  auto done = [&]() __attribute__((always_inline)) {  // all but the last load() have landed
+    if (!STREAM || !more) step_done();
+    else if (rows) step_done<kDL + kWL + 1>();
+    else step_done<kWL + 1>();
+  };
+  done();
+  int cb = 0;  // the buffer whose turn it is
+  for (int item = pos; item < items; item += G) {
+    const TileInfo t = tile_of(tiles, a, item, strips, strip);
+    // Up to 64 rows: both waves take all of them, each half of every stage's matrix rows, so that
+    // the weights are converted once; their sums meet at the end. More: half of the rows each.
+    const int U = (t.M + 15) / 16;
+    const bool shared = U <= 4;
+    const int u0 = wm && !shared ? (U + 1) / 2 : 0, live = shared ? U : wm ? U / 2 : (U + 1) / 2;
     floatx4_t acc[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[i][c] = floatx4_t{};
-    load(0);
-    if (STREAM && S > 1) load(1);
-    auto done = [&](bool more) __attribute__((always_inline)) {  // all but the last load() have landed
-      if (!STREAM || !more) step_done();
-      else if (rows) step_done<kDL + kWL + 1>();
-      else step_done<kWL + 1>();
-    };
-    done(S > 1);
-    auto run = [&](auto LL) __attribute__((always_inline)) {
+    auto run = [&](auto LL, auto SH) __attribute__((always_inline)) {
       constexpr int L = decltype(LL)::value;
+      constexpr bool kShared = decltype(SH)::value;
       for (int s = 0; s < S; ++s) {
-        if (s + kBufs - 1 < S) load(s + kBufs - 1);
-        if constexpr (L > 0) {
-          const GradBuf<P, WK>& B = buf[s % kBufs];
+        more = load();
+        {
+          const GradBuf<P, WK>& B = buf[cb];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int z = 0; z < (kShared ? 1 : 2); ++z) {
+            const int half = kShared ? wm : z;
             uint32_t code[8];
             float sc[8];
 #pragma unroll
@@ -168,20 +191,48 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
               }
           }
         }
-        done(s + 2 < S);
+        done();
+        cb = cb + 1 == kBufs ? 0 : cb + 1;
       }
     };
-    if (live == 4) run(std::integral_constant<int, 4>{});
-    else if (live == 3) run(std::integral_constant<int, 3>{});
-    else if (live == 2) run(std::integral_constant<int, 2>{});
-    else if (live == 1) run(std::integral_constant<int, 1>{});
-    else run(std::integral_constant<int, 0>{});
+    if (shared) {
+      if (live == 4) run(std::integral_constant<int, 4>{}, std::true_type{});
+      else if (live == 3) run(std::integral_constant<int, 3>{}, std::true_type{});
+      else if (live == 2) run(std::integral_constant<int, 2>{}, std::true_type{});
+      else run(std::integral_constant<int, 1>{}, std::true_type{});
+      // of two 16-row tiles the first wave finishes the even one and the second the odd one; each
+      // gives the other its sums, four columns of eight at a time
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        if (i >= live) break;
+#pragma unroll
+        for (int c0 = 0; c0 < 8; c0 += 4) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // (branches, not indexes: accumulators stay in registers)
+            if (wm) meet[wave][c][lane] = acc[i][c0 + c];
+            else meet[wave][c][lane] = acc[i + 1][c0 + c];
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const floatx4_t o = meet[wave ^ WK][c][lane];
+            if (wm) acc[i + 1][c0 + c] += o;
+            else acc[i][c0 + c] += o;
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+      }
+    } else {
+      if (live == 4) run(std::integral_constant<int, 4>{}, std::false_type{});
+      else if (live == 3) run(std::integral_constant<int, 3>{}, std::false_type{});
+      else run(std::integral_constant<int, 2>{}, std::false_type{});
+    }
     // acc[i][c][v]: row 16 (u0 + i) + 4 g + v, column k + c: eight neighbours a lane
     const int k = t.n0 + 128 * wk + 8 * r;
     const bool wide = a.K % 8 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i >= live) continue;
+      if (i >= live || (shared && (i & 1) != wm)) continue;
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int m = 16 * (u0 + i) + 4 * g + v;

@@ -8,12 +8,10 @@
 // matrix's bytes: each is read once per 16 rows.
 #include "mx4.h"
 
-#define TILES_PAY (mx4_row_tiles(a) * ((a.N + 127) / 128) >= 256)
 namespace moe {
 namespace {
 
 constexpr int kRows = 16;   // rows of a group per workgroup
-constexpr int kStrip = 16;  // matrix rows per workgroup (forward)
 constexpr int kCols = 128;  // matrix columns per workgroup (gradient)
 
 // The group and rows of this workgroup: block x takes rows 16 x .. of the one
@@ -49,68 +47,100 @@ __device__ inline void store_out(const Mx4Args& a, size_t i, float v) {
 // matrix row r (its 16 bytes of codes, one scale) and of x's row r. A product
 // step takes eight values of each of the four blocks; the order of K within a
 // chunk is the same for both operands, which is all that matters. Microscaled
-// rows go through the 4-bit matrix cores, one product a chunk.
-template <int XT>
+// rows go through the 4-bit matrix cores, one product a chunk. A wave asks for
+// kAhead chunks of its strip's weights at once: with a few rows the time is the
+// chain from the group's offsets over those loads to the sums.
+constexpr int kAhead = 4;
+
+template <int XT, int NT>
 __global__ __launch_bounds__(256) void rows_forward(Mx4Args a, bool vec) {
-  __shared__ float part[4][kRows * kStrip];
+  __shared__ float part[4][NT][kRows * 16];
   const Unit u = unit_of(a);
   if (u.M <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-  const int nb = mx4_blocks(a.K), n0 = blockIdx.y * kStrip;
-  const size_t wrow = (size_t)u.e * a.N + min(n0 + r, a.N - 1);
-  const uint4* wc = reinterpret_cast<const uint4*>(a.wc) + wrow * nb;
-  const uint8_t* ws = a.ws + wrow * nb;
-  const int xr = r < u.M ? mx4_row(a, u.s0 + r) : -1;
-  floatx4_t acc = {};
-  for (int b0 = 4 * wave; b0 < nb; b0 += 16) {
-    const int b = b0 + g;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    uint32_t sw = 0;
-    if (b < nb) {
-      c = wc[b];
-      sw = ws[b];
-    }
-    if constexpr (XT == kMx4) {
-      uint4 xc = make_uint4(0, 0, 0, 0);
-      uint32_t sx = 0;
-      if (b < nb && xr >= 0) {
-        xc = reinterpret_cast<const uint4*>(a.x)[(size_t)xr * nb + b];
-        sx = a.xs[(size_t)xr * nb + b];
-      }
-      int8v_t A = {}, B = {};
-      A[0] = c.x; A[1] = c.y; A[2] = c.z; A[3] = c.w;
-      B[0] = xc.x; B[1] = xc.y; B[2] = xc.z; B[3] = xc.w;
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc, 4, 4, 0, (int)sw, 0, (int)sx);
-    } else {
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      const float sc = mx4_scale(sw);
+  const int nb = mx4_blocks(a.K), n0 = blockIdx.y * 16 * NT;
+  const uint4* wc[NT];
+  const uint8_t* ws[NT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8_t wf = mx4_frag(w[i], sc);
-        const int k = 32 * b + 8 * i;
-        if constexpr (XT == 1) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (xr >= 0 && k < a.K) v = load8_bf16(static_cast<const uint16_t*>(a.x) + xr * a.ldx, k, a.K, vec);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, v), acc, 0, 0, 0);
-        } else {
-          float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (xr >= 0 && k < a.K) load8_f32(static_cast<const float*>(a.x) + xr * a.ldx, k, a.K, vec, f);
-          uint4 h, m, l;
-          split3x8(f, h, m, l);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, l), acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, m), acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, h), acc, 0, 0, 0);
+  for (int j = 0; j < NT; ++j) {
+    const size_t row = (size_t)u.e * a.N + min(n0 + 16 * j + r, a.N - 1);
+    wc[j] = reinterpret_cast<const uint4*>(a.wc) + row * nb;
+    ws[j] = a.ws + row * nb;
+  }
+  const int xr = r < u.M ? mx4_row(a, u.s0 + r) : -1;
+  floatx4_t acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = floatx4_t{};
+  for (int b0 = 4 * wave; b0 < nb; b0 += 16 * kAhead) {
+    uint4 c[kAhead][NT];
+    uint32_t sw[kAhead][NT];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int b = b0 + 16 * z + g;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        c[z][j] = make_uint4(0, 0, 0, 0);
+        sw[z][j] = 0;
+        if (b < nb) {
+          c[z][j] = wc[j][b];
+          sw[z][j] = ws[j][b];
+        }
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int b = b0 + 16 * z + g;
+      if (b0 + 16 * z >= nb) break;
+      if constexpr (XT == kMx4) {
+        uint4 xc = make_uint4(0, 0, 0, 0);
+        uint32_t sx = 0;
+        if (b < nb && xr >= 0) {
+          xc = reinterpret_cast<const uint4*>(a.x)[(size_t)xr * nb + b];
+          sx = a.xs[(size_t)xr * nb + b];
+        }
+        const int8v_t B = {(int)xc.x, (int)xc.y, (int)xc.z, (int)xc.w, 0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint4 w = c[z][j];
+          const int8v_t A = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+          acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, acc[j], 4, 4, 0, (int)sw[z][j], 0, (int)sx);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = 32 * b + 8 * i;
+          uint4 v[XT == 1 ? 1 : 3];
+          if constexpr (XT == 1) {
+            v[0] = make_uint4(0, 0, 0, 0);
+            if (xr >= 0 && k < a.K) v[0] = load8_bf16(static_cast<const uint16_t*>(a.x) + xr * a.ldx, k, a.K, vec);
+          } else {
+            float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (xr >= 0 && k < a.K) load8_f32(static_cast<const float*>(a.x) + xr * a.ldx, k, a.K, vec, f);
+            split3x8(f, v[0], v[1], v[2]);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const uint4 w = c[z][j];
+            const bf16x8_t wf = mx4_frag(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w, mx4_scale(sw[z][j]));
+#pragma unroll
+            for (int p = XT == 1 ? 0 : 2; p >= 0; --p)
+              acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, __builtin_bit_cast(bf16x8_t, v[p]), acc[j], 0, 0, 0);
+          }
         }
       }
     }
   }
-  // acc[i]: matrix row 4 g + i, x's row r
+  // acc[j][i]: matrix row 16 j + 4 g + i, x's row r
 #pragma unroll
-  for (int i = 0; i < 4; ++i) part[wave][r * kStrip + 4 * g + i] = acc[i];
+  for (int j = 0; j < NT; ++j)
+    *reinterpret_cast<floatx4_t*>(&part[wave][j][16 * r + 4 * g]) = acc[j];
   __syncthreads();
-  const int m = tid / kStrip, n = n0 + tid % kStrip;
-  if (m < u.M && n < a.N)
-    store_out(a, (size_t)(u.s0 + m) * a.N + n, (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]));
+  for (int i = tid; i < 256 * NT; i += 256) {
+    const int m = (i / (16 * NT)), n = i % (16 * NT), at = 16 * m + n % 16;
+    if (m < u.M && n0 + n < a.N)
+      store_out(a, (size_t)(u.s0 + m) * a.N + n0 + n,
+                (part[0][n / 16][at] + part[1][n / 16][at]) + (part[2][n / 16][at] + part[3][n / 16][at]));
+  }
 }
 
 // Four waves share N in steps of 32. Lane (r, g) holds, for each of the eight
@@ -182,39 +212,85 @@ __global__ __launch_bounds__(256) void rows_gradient(Mx4Args a, bool vec) {
 }
 
 // dx[t] = the sum of a token's rows of part, in the order of its assignments
-// (the shared expert's last); float32 sums, one rounding.
-template <bool BF>
+// (the shared expert's last); float32 sums, one rounding. A lane adds up four
+// columns (where K is no multiple of four, one), four rows on their way at once.
+template <bool BF, int V>
 __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part, const int32_t* __restrict__ slot_of,
                                                   int T, int k, int has_shared, int A, int K, void* __restrict__ y) {
-  const int t = blockIdx.x;
-  for (int c = blockIdx.y * 256 + threadIdx.x; c < K; c += gridDim.y * 256) {
-    float v = 0.f;
-    for (int j = 0; j < k + has_shared; ++j) {
-      const int s = slot_of[j < k ? (size_t)t * k + j : (size_t)T * k + t];
-      if ((unsigned)s < (unsigned)A) v += part[(size_t)s * K + c];
+  const int t = blockIdx.x, n = k + has_shared;
+  for (int c = V * (blockIdx.y * 256 + threadIdx.x); c < K; c += V * gridDim.y * 256) {
+    float v[V] = {};
+    for (int j0 = 0; j0 < n; j0 += 4) {
+      float p[4][V];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int j = j0 + z;
+        const int s = j < n ? slot_of[j < k ? (size_t)t * k + j : (size_t)T * k + t] : -1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[z][i] = 0.f;
+        if ((unsigned)s < (unsigned)A) {
+          if constexpr (V == 4) {
+            const float4 q = *reinterpret_cast<const float4*>(part + (size_t)s * K + c);
+            p[z][0] = q.x; p[z][1] = q.y; p[z][2] = q.z; p[z][3] = q.w;
+          } else {
+            p[z][0] = part[(size_t)s * K + c];
+          }
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] += p[z][i];
     }
-    if (BF) static_cast<uint16_t*>(y)[(size_t)t * K + c] = (uint16_t)f32_to_bf16_bits(v);
-    else static_cast<float*>(y)[(size_t)t * K + c] = v;
+    const size_t at = (size_t)t * K + c;
+    if constexpr (V == 4) {
+      if (BF)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + at) =
+            make_uint2(f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
+                       f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16);
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      if (BF) static_cast<uint16_t*>(y)[at] = (uint16_t)f32_to_bf16_bits(v[0]);
+      else static_cast<float*>(y)[at] = v[0];
+    }
   }
+}
+
+// Whether the tile kernels take a product. With groups they read each matrix
+// once and need no workgroup for each row: from 32 rows on (4 tokens x 11
+// experts, [1024, 2048]: 14.8 us against 17.7; 16 tokens 31 against 40), float32
+// rows from 96 on (44 rows: 47 against 26; 176: 48 against 60), gradients
+// always (11 rows: 19 against 26). One matrix: once the 16-row units fill the
+// chip a few times over (512 rows, [1024, 2048]: 15 us against 23; float32 rows
+// at 2,048: 89 against 165; gradients: at 2,048 rows 33 against 42, float32
+// not yet: 95 against 66).
+bool tiles_pay(const Mx4Args& a, bool gradient) {
+  const bool f32 = a.xdtype == 0;
+  if (a.offsets) return gradient || a.A >= (f32 ? 96 : 32);
+  const long long units = (a.A + kRows - 1) / kRows;
+  if (gradient) return units * ((a.K + kCols - 1) / kCols) > (f32 ? 2560 : 1280);
+  return units * ((a.N + 31) / 32) > (f32 ? 3072 : 1024);
 }
 
 }  // namespace
 
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
-  if (TILES_PAY) {
+  if (tiles_pay(a, false)) {
     if (a.xdtype != kMx4) return launch_mx4_tiles(a, s);
     if (mx4_tiles4_can(a)) return launch_mx4_tiles4(a, s);
   }
-  const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.N + kStrip - 1) / kStrip);
   const bool vec = a.xdtype != kMx4 && rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
-  if (a.xdtype == kMx4) MOE_LAUNCH("mx4_rows", s, rows_forward<kMx4>, g, dim3(256), 0, s, a, vec);
-  else if (a.xdtype == 1) MOE_LAUNCH("mx4_rows", s, rows_forward<1>, g, dim3(256), 0, s, a, vec);
-  else MOE_LAUNCH("mx4_rows", s, rows_forward<0>, g, dim3(256), 0, s, a, vec);
+  constexpr int NT = 2;
+  const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.N + 16 * NT - 1) / (16 * NT));
+  if (a.xdtype == kMx4) MOE_LAUNCH("mx4_rows", s, (rows_forward<kMx4, NT>), g, dim3(256), 0, s, a, vec);
+  else if (a.xdtype == 1) MOE_LAUNCH("mx4_rows", s, (rows_forward<1, NT>), g, dim3(256), 0, s, a, vec);
+  else MOE_LAUNCH("mx4_rows", s, (rows_forward<0, NT>), g, dim3(256), 0, s, a, vec);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
-  if (TILES_PAY) return launch_mx4_grad_tiles(a, s);
+  if (tiles_pay(a, true)) return launch_mx4_grad_tiles(a, s);
   const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.K + kCols - 1) / kCols);
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
   if (a.xdtype == 1) MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<1>, g, dim3(256), 0, s, a, vec);
@@ -224,11 +300,18 @@ hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
 
 hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, int T, int k, int has_shared, int A,
                                  int K, void* y, int ydtype, hipStream_t s) {
-  const dim3 g(T, (K + 1023) / 1024);
-  if (ydtype == 1)
-    MOE_LAUNCH("mx4_sum_tokens", s, sum_tokens<true>, g, dim3(256), 0, s, part, slot_of, T, k, has_shared, A, K, y);
-  else
-    MOE_LAUNCH("mx4_sum_tokens", s, sum_tokens<false>, g, dim3(256), 0, s, part, slot_of, T, k, has_shared, A, K, y);
+  const bool four = K % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
+  const dim3 g(T, four ? (K + 1023) / 1024 : (K + 255) / 256);
+#define SUM_TOKENS(BF, V) \
+  MOE_LAUNCH("mx4_sum_tokens", s, (sum_tokens<BF, V>), g, dim3(256), 0, s, part, slot_of, T, k, has_shared, A, K, y)
+  if (ydtype == 1) {
+    if (four) SUM_TOKENS(true, 4);
+    else SUM_TOKENS(true, 1);
+  } else {
+    if (four) SUM_TOKENS(false, 4);
+    else SUM_TOKENS(false, 1);
+  }
+#undef SUM_TOKENS
   return hipGetLastError();
 }
 

@@ -101,7 +101,7 @@ def lib() -> C.CDLL:
             "moe_mx4_matmul": [P, u, i32, i64, i32, u, u, i32, i32, P, i32, P],
             "moe_mx4_matmul_backward": [P, i32, i64, i32, u, u, i32, i32, P, i32, P],
             "moe_mx4_experts_matmul": [P, u, i32, i64, i32, i32, i32, i32, i32, P, P, u, u, i32, i32, P,
-                                       i32, P],
+                                       i32, P, sz, P],
             "moe_mx4_experts_matmul_backward": [P, i32, i64, i32, i32, i32, i32, i32, P, P, u, u, i32,
                                                 i32, P, i32, P, sz, P],
             "moe_balance_loss": [P, i32, i64, i32, i32, i32, P, P, P, P, P, P, sz, P],
@@ -110,6 +110,8 @@ def lib() -> C.CDLL:
         for name, args in sigs.items():
             getattr(L, name).argtypes = args
             getattr(L, name).restype = C.c_int
+        L.moe_mx4_experts_matmul_workspace_size.argtypes = [i32] * 3
+        L.moe_mx4_experts_matmul_workspace_size.restype = sz
         L.moe_mx4_experts_matmul_backward_workspace_size.argtypes = [i32] * 5
         L.moe_mx4_experts_matmul_backward_workspace_size.restype = sz
         L.moe_balance_loss_workspace_size.argtypes = [i32] * 3
@@ -663,8 +665,21 @@ def _groups(grouping: Grouping, w: Mx4, tokens: int | None, dev: torch.device):
     return tokens, max(1, A // tokens - shared if tokens else 1), E, shared, A
 
 
+def _workspace(given: torch.Tensor | None, n: int, dev: torch.device):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of n bytes."""
+    if given is None:
+        if not n:
+            return None, 0, None
+        given = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        _need_cuda("workspace", given, torch.uint8)
+        if given.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+    return given.data_ptr(), given.numel(), given
+
+
 def mx4_experts_matmul(x, w: Mx4, grouping: Grouping, tokens: int | None = None, dtype: torch.dtype | None = None,
-                       out: torch.Tensor | None = None) -> torch.Tensor:
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Rows grouped by expert, each times its expert's matrix (moe_mx4_experts_matmul): [A, N] in the
     groups' order. w: [E, N, K], or [E + 1, N, K] with the shared expert last. x ([.., K]: float32,
     bfloat16, or an Mx4) holds the A rows in the groups' order, or, where `tokens` gives their number,
@@ -679,9 +694,10 @@ def mx4_experts_matmul(x, w: Mx4, grouping: Grouping, tokens: int | None = None,
     if gather:
         _int32("grouping.perm", grouping.perm, dev, A)
     y = _result(out, (A, N), dtype or own, dev)
+    wp, wn, keep = _workspace(workspace, lib().moe_mx4_experts_matmul_workspace_size(T, k, shared), dev)
     _call("moe_mx4_experts_matmul", dev, p, s, code, ld, T, k, E, shared, int(gather), grouping.offsets.data_ptr(),
           grouping.perm.data_ptr() if gather else None, w.codes.data_ptr(), w.scales.data_ptr(), N, w.K, y.data_ptr(),
-          _FLOATS[y.dtype])
+          _FLOATS[y.dtype], wp, wn)
     return y
 
 
@@ -701,17 +717,11 @@ def mx4_experts_matmul_backward(dy: torch.Tensor, w: Mx4, grouping: Grouping, to
     if gather:
         _int32("grouping.slot_of", grouping.slot_of, dev, A)
     dx = _result(out, (T, w.K), dtype or dy.dtype, dev)
-    n = lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, w.K, 1) if gather else 0
-    if workspace is None:
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    else:
-        _need_cuda("workspace", workspace, torch.uint8)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
+    wp, wn, keep = _workspace(
+        workspace, lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, w.K, int(gather)), dev)
     _call("moe_mx4_experts_matmul_backward", dev, dy.data_ptr(), code, ld, T, k, E, shared, int(gather),
           grouping.offsets.data_ptr(), grouping.slot_of.data_ptr() if gather else None, w.codes.data_ptr(),
-          w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dx.dtype],
-          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+          w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dx.dtype], wp, wn)
     return dx
 
 
@@ -758,15 +768,9 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tens
         if out.losses.numel() != 2 or out.counts.numel() != E or out.kept.numel() != 1 or out.losses.device != dev:
             raise ValueError("out does not match the logits")
         out.k = k
-    if workspace is None:
-        n = lib().moe_balance_loss_workspace_size(T, k, E)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
-    else:
-        _need_cuda("workspace", workspace, torch.uint8)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
+    wp, wn, keep_ws = _workspace(workspace, lib().moe_balance_loss_workspace_size(T, k, E), dev)
     _call("moe_balance_loss", dev, logits.data_ptr(), code, ld, T, E, k, idx.data_ptr(), keep, out.losses.data_ptr(),
-          out.counts.data_ptr(), out.kept.data_ptr(), workspace.data_ptr(), workspace.numel())
+          out.counts.data_ptr(), out.kept.data_ptr(), wp, wn)
     return out
 
 

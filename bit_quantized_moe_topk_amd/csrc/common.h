@@ -184,10 +184,11 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, in
                                  void* y, hipStream_t s);
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s);
-hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s);
-hipError_t launch_mx4_grad_tiles(const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);
+void launch_mx4_zero(uint32_t* counter, hipStream_t s);
+hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s);
 bool mx4_tiles4_can(const Mx4Args& a);
-hipError_t launch_mx4_tiles4(const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s);
 hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, int T, int k, int has_shared, int A,
                                  int K, void* y, int ydtype, hipStream_t s);
 // Balance loss and z loss of a router, and their gradient (balance.hip).

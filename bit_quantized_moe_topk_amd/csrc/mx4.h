@@ -93,6 +93,7 @@ struct Mx4Args {
   int N, K;
   void* y;                // [A][N] (forward), [A][K] (gradient)
   int ydtype;
+  uint32_t* counter;      // of the tiles taken, or null: tiles are dealt in turn
 };
 
 // About how many 128-row tiles the rows make: a group that has rows has one at least.

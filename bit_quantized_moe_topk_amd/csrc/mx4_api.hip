@@ -38,6 +38,11 @@ int check_groups(int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t ga
   return MOE_OK;
 }
 
+// Bytes of the counters (eight, 128 bytes apart) from which workgroups take tiles, from this many rows on (fewer tiles than
+// that many rows make are dealt in turn).
+constexpr int32_t kCounterRows = 2048;
+size_t counter_bytes(long long rows) { return rows >= kCounterRows ? 1024 : 0; }
+
 moe::Mx4Args product(const void* x, const uint8_t* xs, int32_t dtype, int64_t ld, int32_t A, const uint8_t* wc,
                      const uint8_t* ws, int32_t N, int32_t K, void* y, int32_t out) {
   moe::Mx4Args a{};
@@ -98,29 +103,38 @@ int moe_mx4_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, int32_t 
   return status_of(moe::launch_mx4_gradient(a, static_cast<hipStream_t>(stream)));
 }
 
+size_t moe_mx4_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_shared) {
+  if (check_groups(T, k, 1, has_shared, 0) != MOE_OK) return 0;
+  return counter_bytes((long long)T * (k + has_shared));
+}
+
 int moe_mx4_experts_matmul(const void* x, const uint8_t* x_scales, int32_t xdtype, int64_t ldx, int32_t T, int32_t k,
                            int32_t E, int32_t has_shared, int32_t gather, const int32_t* offsets, const int32_t* perm,
                            const uint8_t* w_codes, const uint8_t* w_scales, int32_t N, int32_t K, void* y,
-                           int32_t ydtype, void* stream) {
+                           int32_t ydtype, void* ws, size_t ws_bytes, void* stream) {
   int st = check_groups(T, k, E, has_shared, gather);
   if (st != MOE_OK) return st;
   const int32_t A = T * (k + has_shared);
   st = check_product(x, x_scales, xdtype, ldx, A, K, w_codes, w_scales, N, K, y, ydtype);
   if (st != MOE_OK || A == 0) return st;
   if (!offsets || (gather && !perm)) return MOE_ERR_INVALID_ARG;
+  const size_t need = counter_bytes(A);
+  if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   moe::Mx4Args a = product(x, x_scales, xdtype, ldx, A, w_codes, w_scales, N, K, y, ydtype);
   a.T = T;
   a.k = k;
   a.E_tot = E + has_shared;
   a.offsets = offsets;
   a.perm = gather ? perm : nullptr;
+  a.counter = need ? static_cast<uint32_t*>(ws) : nullptr;
   return status_of(moe::launch_mx4_forward(a, static_cast<hipStream_t>(stream)));
 }
 
 size_t moe_mx4_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int32_t has_shared, int32_t K,
                                                       int32_t gather) {
-  if (K < 1 || check_groups(T, k, 1, has_shared, gather) != MOE_OK || !gather) return 0;
-  return sizeof(float) * (size_t)T * (k + has_shared) * K;
+  if (K < 1 || check_groups(T, k, 1, has_shared, gather) != MOE_OK) return 0;
+  const size_t A = (size_t)T * (k + has_shared);
+  return counter_bytes(A) + (gather ? sizeof(float) * A * K : 0);
 }
 
 int moe_mx4_experts_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, int32_t T, int32_t k, int32_t E,
@@ -134,17 +148,18 @@ int moe_mx4_experts_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, 
   st = check_product(dy, nullptr, dtype, ldd, A, N, w_codes, w_scales, N, K, dx, dxdtype);
   if (st != MOE_OK || A == 0) return st;
   if (!offsets || (gather && !slot_of)) return MOE_ERR_INVALID_ARG;
-  if (gather && (!ws || !aligned(ws, 16) ||
-                 ws_bytes < moe_mx4_experts_matmul_backward_workspace_size(T, k, has_shared, K, gather)))
-    return MOE_ERR_WORKSPACE;
+  const size_t need = moe_mx4_experts_matmul_backward_workspace_size(T, k, has_shared, K, gather);
+  if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  moe::Mx4Args a = product(dy, nullptr, dtype, ldd, A, w_codes, w_scales, N, K, gather ? ws : dx,
+  void* part = gather ? static_cast<char*>(ws) + counter_bytes(A) : nullptr;
+  moe::Mx4Args a = product(dy, nullptr, dtype, ldd, A, w_codes, w_scales, N, K, gather ? part : dx,
                            gather ? MOE_F32 : dxdtype);
+  a.counter = counter_bytes(A) ? static_cast<uint32_t*>(ws) : nullptr;
   a.E_tot = E + has_shared;
   a.offsets = offsets;
   hipError_t e = moe::launch_mx4_gradient(a, s);
   if (e == hipSuccess && gather)
-    e = moe::launch_mx4_sum_tokens(static_cast<const float*>(ws), slot_of, T, k, has_shared, A, K, dx, dxdtype, s);
+    e = moe::launch_mx4_sum_tokens(static_cast<const float*>(part), slot_of, T, k, has_shared, A, K, dx, dxdtype, s);
   return status_of(e);
 }
 

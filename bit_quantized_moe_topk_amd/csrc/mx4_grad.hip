@@ -71,18 +71,23 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, wk = wave % WK, wm = wave / WK;
   const int nb = mx4_blocks(a.K), S = (a.N + kGN - 1) / kGN;
-  const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
-  if (pos >= items) return;
-  // load cursor: stage ls of tile lt, into buffer lb
-  TileInfo lt = tile_of(tiles, a, pos, strips, strip);  // n0: its first column
-  int litem = pos, ls = 0, lb = 0;
+  __shared__ int slot;
+  Deal deal{items, (int)gridDim.x, a.counter, &slot, 0u};
+  int item = deal.first();
+  if (item >= items) return;
+  deal.ask();
+  int next = deal.answer(item);
+  // load cursor: stage ls of tile lt, into buffer lb; `next` is the item that it goes to then
+  TileInfo lt = tile_of(tiles, a, item, items, strips, strip);  // n0: its first column
+  int ls = 0, lb = 0;
+  bool crossed = false;  // it is in the next item
   bool rows = false;  // whether this wave's last load() brought rows of dy
   // the next stage, of whatever tile it is; false: there is none
   auto load = [&]() __attribute__((always_inline)) {
     if (ls == S) {
-      if (litem + G >= items) return false;
-      litem += G;
-      lt = tile_of(tiles, a, litem, strips, strip);
+      if (crossed || next >= items) return false;
+      crossed = true;
+      lt = tile_of(tiles, a, next, items, strips, strip);
       ls = 0;
     }
     const int s = ls++, b0 = lt.n0 / 32;
@@ -148,8 +153,9 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
   };
   done();
   int cb = 0;  // the buffer whose turn it is
-  for (int item = pos; item < items; item += G) {
-    const TileInfo t = tile_of(tiles, a, item, strips, strip);
+  while (item < items) {
+    deal.ask();
+    const TileInfo t = tile_of(tiles, a, item, items, strips, strip);
     // Up to 64 rows: both waves take all of them, each half of every stage's matrix rows, so that
     // the weights are converted once; their sums meet at the end. More: half of the rows each.
     const int U = (t.M + 15) / 16;
@@ -263,12 +269,15 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
         }
       }
     }
+    item = next;
+    crossed = false;
+    if (item < items) next = deal.answer(item);
   }
 }
 
 }  // namespace
 
-hipError_t launch_mx4_grad_tiles(const Mx4Args& a, hipStream_t s) {
+hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s) {
   const int nb = mx4_blocks(a.K);
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
   const bool stream = a.xdtype == 1 && vec && a.N % kGN == 0 && nb % 4 == 0 &&
@@ -279,6 +288,8 @@ hipError_t launch_mx4_grad_tiles(const Mx4Args& a, hipStream_t s) {
   const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * strips;
   const int cap = (stream || a.xdtype == 0 ? 1 : 2) * device_cus();
   const dim3 g((unsigned)(most < cap ? most : cap));
+  if (most <= cap || g.x % kXcds) a.counter = nullptr;
+  else if (a.counter) launch_mx4_zero(a.counter, s);
   if (stream) MOE_LAUNCH("mx4_grad_tiles", s, (tiles_gradient<1, 4, true>), g, dim3(512), 0, s, a, vec);
   else if (a.xdtype == 1) MOE_LAUNCH("mx4_grad_tiles", s, (tiles_gradient<1, 2, false>), g, dim3(256), 0, s, a, vec);
   else MOE_LAUNCH("mx4_grad_tiles", s, (tiles_gradient<3, 2, false>), g, dim3(256), 0, s, a, vec);

@@ -273,7 +273,13 @@ bool tiles_pay(const Mx4Args& a, bool gradient) {
   return units * ((a.N + 31) / 32) > (f32 ? 3072 : 1024);
 }
 
+__global__ __launch_bounds__(256) void zero_counters(uint32_t* p) { p[threadIdx.x] = 0u; }
+
 }  // namespace
+
+void launch_mx4_zero(uint32_t* counter, hipStream_t s) {
+  MOE_LAUNCH("mx4_zero", s, zero_counters, dim3(1), dim3(256), 0, s, counter);
+}
 
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
   if (tiles_pay(a, false)) {

@@ -59,9 +59,10 @@ __device__ inline int tile_group(const Tiles& t, int E_tot, int ti) {
   return lo;
 }
 
-__device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int item, int strips, int strip) {
+// Item `id` of `items` (counted from the last group's end), strips of `strip` matrix rows.
+__device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int id, int items, int strips, int strip) {
   TileInfo i;
-  const int ti = item / strips;
+  const int item = items - 1 - id, ti = item / strips;
   int r0 = 0, rows = a.A, of = (a.A + kTM - 1) / kTM, j = ti;
   i.e = 0;
   if (a.offsets) {
@@ -78,6 +79,51 @@ __device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int item, i
   i.n0 = (item - ti * strips) * strip;
   return i;
 }
+
+// The order in which workgroups take items, the last group's first (a shared
+// expert's full tiles). Workgroup g runs on XCD g % 8, and runs of consecutive
+// items go to one XCD, where they share rows or a matrix through its L2.
+// Without counters every workgroup takes one item of each round. With them
+// (kCounters, zeroed before the launch) it takes the next of its XCD's that
+// nobody has, and when there is none another XCD's: tiles differ in cost by up
+// to four, and whoever is dealt one more, or heavier ones, has the chip wait
+// (the gradient of 1,024 tokens: 237 us dealt, 200 taken). An item is asked for
+// a whole item before it is needed, so nobody waits for the answer but at the end.
+constexpr int kXcds = 8, kCounters = kXcds;  // counters 32 words apart
+
+struct Deal {
+  int items, G;
+  uint32_t* counter;
+  int* slot;     // LDS
+  uint32_t asked;
+
+  __device__ int run() const { return G / kXcds; }  // items of a round on one XCD
+  __device__ int item_of(int xcd, uint32_t q) const {
+    const long long i = ((long long)(q / run()) * kXcds + xcd) * run() + q % run();
+    return i < items ? (int)i : 0x7FFFFFFF;
+  }
+  __device__ int first() const { return G % kXcds ? blockIdx.x : item_of(blockIdx.x % kXcds, blockIdx.x / kXcds); }
+  __device__ uint32_t take(int xcd) {
+    return run() + __hip_atomic_fetch_add(counter + 32 * xcd, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __device__ void ask() {
+    if (counter && threadIdx.x == 0) asked = take(blockIdx.x % kXcds);
+  }
+  // The item after `next`, by all threads. (Another tile's barriers lie before the next write to the slot.)
+  __device__ int answer(int next) {
+    if (!counter) return next < items ? next + G : next;
+    if (threadIdx.x == 0) {
+      int xcd = blockIdx.x % kXcds, i = item_of(xcd, asked);
+      for (int z = 1; z < kXcds && i >= items; ++z) {
+        xcd = xcd + 1 == kXcds ? 0 : xcd + 1;
+        i = item_of(xcd, take(xcd));
+      }
+      *slot = i;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    return __builtin_amdgcn_readfirstlane(*reinterpret_cast<volatile int*>(slot));
+  }
+};
 
 __device__ inline uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)p;

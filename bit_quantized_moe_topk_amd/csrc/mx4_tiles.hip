@@ -54,10 +54,13 @@ __global__ __launch_bounds__(kThreads, 2) void tiles_forward(Mx4Args a, bool vec
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r = lane & 31, wn = wave & 3, wm = wave >> 2;
   const int nb = mx4_blocks(a.K), S = (nb + 1) / 2;
-  // consecutive items on one XCD (workgroup g runs on XCD g % 8): they share rows, or a matrix
-  const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
-  for (int item = pos; item < items; item += G) {
-    const TileInfo t = tile_of(tiles, a, item, strips, kTN);
+  __shared__ int slot;
+  Deal deal{items, (int)gridDim.x, a.counter, &slot, 0u};
+  deal.ask();
+  for (int item = deal.first(), next = 0; item < items; item = next) {
+    next = deal.answer(item);
+    deal.ask();
+    const TileInfo t = tile_of(tiles, a, item, items, strips, kTN);
     const int R = (t.M + 31) / 32, run0 = wm ? (R + 1) / 2 : 0;
     // this wave's weights: matrix rows n0 + 64 wn + 32 j + r (past N: the last one, not stored)
     const int live = t.n0 + 64 * wn >= a.N ? 0 : wm ? R / 2 : (R + 1) / 2;
@@ -174,14 +177,19 @@ template <int WN>
 struct StreamBuf {
   uint4 x[2][kTM * 8];        // two 64-column stages (chunk_at)
   uint4 w[64 * WN * 4];       // matrix row n: its four blocks, block c at position c ^ ((n >> 2) & 3)
-  uint32_t s[64 * WN];        // its four scales
 };
 
-template <int WN>
+// WIDE: scales come 16 a load, for four steps (a multiple of 16 blocks, aligned),
+// and the rows' loads are not left out for runs that are not there: a load costs
+// by the 128-byte lines that it touches, and one that repeats a row touches few
+// (a chunk of 8,192 tokens: 433 us without both). Else four scales a step.
+template <int WN, bool WIDE>
 __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   constexpr int kRuns = WN / 2;  // runs of 32 rows per wave
   constexpr int kWL = WN / 2;    // code loads per wave and step (16 matrix rows each)
+  constexpr int kS = WIDE ? 4 : 1;  // dwords of scales per load and matrix row
   __shared__ StreamBuf<WN> buf[2];
+  __shared__ uint32_t scales[2][64 * WN * kS];
   __shared__ Tiles tiles;
   constexpr int strip = 64 * WN;
   const int strips = (a.N + strip - 1) / strip;
@@ -189,14 +197,20 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r = lane & 31, wn = wave % WN, wm = wave / WN;
   const int nb = mx4_blocks(a.K), P = a.K / kStep;
-  const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
-  if (pos >= items) return;
+  __shared__ int slot;
+  Deal deal{items, (int)gridDim.x, a.counter, &slot, 0u};
+  int item = deal.first();
+  if (item >= items) return;
+  deal.ask();
+  int next = deal.answer(item);
 
   // load cursor: this lane's rows (rows 16 wave + 8 u + l / 8, chunk l % 8 of the stage as placed;
   // those past the tile's repeat its last, and are not stored) and matrix rows (8 WN wave + 16 i +
   // l / 4, block l % 4 as placed), and the bases that advance by steps
   uint32_t xoff[2], woff[kWL], soff;
   int xrows = 0;  // rows to load, in whole runs
+  int lp = 0;     // step of its tile
+  int ls = 1;     // place of the last scales asked for (WIDE; else a step's go with its buffer)
   const char *xbase, *wbase, *sbase;
   int row_next[2];
   auto row_of = [&](int u) { return 16 * wave + 8 * u + (lane >> 3); };
@@ -212,6 +226,7 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
     }
     xbase = static_cast<const char*>(a.x);
     xrows = (t.M + 31) & ~31;
+    lp = 0;
     wbase = reinterpret_cast<const char*>(a.wc) + (size_t)t.e * a.N * nb * 16;
     sbase = reinterpret_cast<const char*>(a.ws) + (size_t)t.e * a.N * nb;
 #pragma unroll
@@ -223,7 +238,7 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   };
   auto load = [&](int b) __attribute__((always_inline)) {
     StreamBuf<WN>& B = buf[b];
-    if (16 * wave < xrows) {
+    if (WIDE || 16 * wave < xrows) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         stream16(xbase, xoff[u], lds_offset(B.x[0]) + 1024 * (2 * wave + u));
@@ -233,22 +248,30 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
     xbase += 256;
 #pragma unroll
     for (int i = 0; i < kWL; ++i) stream16(wbase, woff[i], lds_offset(B.w) + 1024 * (kWL * wave + i));
-    if (WN == 8 || lane < 8 * WN) stream4(sbase, soff, lds_offset(B.s) + 32 * WN * wave);
+    if constexpr (WIDE) {  // (WN 8: a matrix row a lane)
+      if (lp % 4 == 0) {
+        ls ^= 1;
+        stream16(sbase + 4 * lp, soff, lds_offset(scales[ls]) + 1024 * wave);
+      }
+    } else if (lane < 8 * WN) {
+      stream4(sbase + 4 * lp, soff, lds_offset(scales[b]) + 32 * WN * wave);
+    }
     wbase += 64;
-    sbase += 4;
+    ++lp;
   };
 
-  int item = pos, b = 0;
-  TileInfo t = tile_of(tiles, a, item, strips, strip), tn = t;
+  int b = 0, cs = 1;  // cs: place of the scales in use
+  TileInfo t = tile_of(tiles, a, item, items, strips, strip), tn = t;
   fetch_rows(t);
   aim(t);
   load(0);
   load(1);
   step_done();
   for (;;) {
-    const bool more = item + G < items;
+    const bool more = next < items;
     if (more) {
-      tn = tile_of(tiles, a, item + G, strips, strip);
+      deal.ask();
+      tn = tile_of(tiles, a, next, items, strips, strip);
       fetch_rows(tn);
     }
     const int live = min(max((t.M + 31) / 32 - kRuns * wm, 0), kRuns);
@@ -260,49 +283,53 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
     // one loop for each number of live runs (a switch inside the loop makes the compiler move accumulators)
     auto run = [&](auto LL) __attribute__((always_inline)) {
       constexpr int L = decltype(LL)::value;
+      // A step's eight product steps of 16 columns (q: stage q / 4, step q % 4 of it). The operands
+      // of one are read while the last one's products run, and those of the next step's first
+      // while this step's last do, past the barrier: the matrix cores have work across it.
+      uint32_t sw[2];
+      uint4 c[2];
+      bf16x8_t x[2][L > 0 ? L : 1];
+      auto read_w = [&](int st, uint4 (&v)[2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) v[j] = buf[b].w[4 * (64 * wn + 32 * j + r) + ((2 * st + h) ^ ((r >> 2) & 3))];
+      };
+      auto read_x = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          x[q & 1][i] =
+              __builtin_bit_cast(bf16x8_t, buf[b].x[q >> 2][chunk_at(32 * (kRuns * wm + i) + r, 4 * h + (q & 3))]);
+      };
+      auto read_first = [&](int p) __attribute__((always_inline)) {
+        if (WIDE && p % 4 == 0) cs ^= 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          sw[j] = scales[WIDE ? cs : b][kS * (64 * wn + 32 * j + r) + (WIDE ? p & 3 : 0)] >> (8 * h);
+        read_w(0, c);
+        read_x(0);
+      };
+      auto products = [&](int q, const uint4 (&v)[2], const uint32_t (&e)[2]) __attribute__((always_inline)) {
+        bf16x8_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          w[j] = mx4_frag((q & 3) == 0 ? v[j].x : (q & 3) == 1 ? v[j].y : (q & 3) == 2 ? v[j].z : v[j].w,
+                          mx4_scale((e[j] >> (16 * (q >> 2))) & 255u));
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x[q & 1][i], acc[i][j], 0, 0, 0);
+      };
       // next: the load that follows (0: two steps on; 1, 2: the next tile's first and second)
-      auto step = [&](auto next) __attribute__((always_inline)) {
-        const StreamBuf<WN>& B = buf[b];
-        uint32_t sw[2];
-        uint4 c[2];
-        bf16x8_t x[4][L > 0 ? L : 1];
-        auto products = [&](int st, int kk) __attribute__((always_inline)) {
-          bf16x8_t w[2];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint4 v = c[j];
-            w[j] = mx4_frag(kk == 0 ? v.x : kk == 1 ? v.y : kk == 2 ? v.z : v.w,
-                            mx4_scale((sw[j] >> (16 * st)) & 255u));
-          }
-#pragma unroll
-          for (int i = 0; i < L; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[j], x[kk][i], acc[i][j], 0, 0, 0);
-        };
-        auto read = [&](int st, int kk) __attribute__((always_inline)) {
-#pragma unroll
-          for (int i = 0; i < L; ++i)
-            x[kk][i] = __builtin_bit_cast(bf16x8_t, B.x[st][chunk_at(32 * (kRuns * wm + i) + r, 4 * h + kk)]);
-        };
+      auto step = [&](auto next, int p) __attribute__((always_inline)) {
+        uint4 c1[2];
+        const uint32_t e[2] = {sw[0], sw[1]};
         if constexpr (L > 0) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int n = 64 * wn + 32 * j + r;
-            sw[j] = B.s[n] >> (8 * h);
-            c[j] = B.w[4 * n + (h ^ ((r >> 2) & 3))];
-          }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            read(0, kk);
-            products(0, kk);
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) c[j] = B.w[4 * (64 * wn + 32 * j + r) + ((2 + h) ^ ((r >> 2) & 3))];
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            read(1, kk);
-            products(1, kk);
+          for (int q = 0; q < 7; ++q) {
+            if (q == 2) read_w(1, c1);
+            read_x(q + 1);
+            products(q, q < 4 ? c : c1, e);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
         // everything is read: the buffer takes the step after next, which has a step to land
@@ -311,12 +338,19 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
           if (decltype(next)::value == 1) aim(tn);
           load(b);
         }
-        __builtin_amdgcn_sched_barrier(0);
         b ^= 1;
+        if constexpr (L > 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (decltype(next)::value != 2) read_first(p + 1);
+          products(7, c1, e);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       };
-      for (int p = 2; p < P; ++p) step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
-      step(std::integral_constant<int, 2>{});
+      if constexpr (L > 0) read_first(0);
+      else if (WIDE) cs ^= (P / 4) & 1;
+      for (int p = 0; p < P - 2; ++p) step(std::integral_constant<int, 0>{}, p);
+      step(std::integral_constant<int, 1>{}, P - 2);
+      step(std::integral_constant<int, 2>{}, P - 1);
     };
     if (live == kRuns) run(std::integral_constant<int, kRuns>{});
     else if (kRuns > 3 && live == 3) run(std::integral_constant<int, kRuns < 3 ? 0 : 3>{});
@@ -328,19 +362,20 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
       if (i < live)
         store_run(a, acc[i], t.s0 + 32 * (kRuns * wm + i), t.M - 32 * (kRuns * wm + i), t.n0 + 64 * wn);
     if (!more) break;
-    item += G;
+    next = deal.answer(next);
     t = tn;
   }
 }
 
 }  // namespace
 
-hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s) {
+hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s) {
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
   // streamed: 32-bit offsets within one matrix and within the rows
   const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && a.K >= 2 * kStep && (long long)a.N * a.K < (1LL << 32) &&
                     (a.perm ? a.T : a.A) * a.ldx * 2 < (1LL << 32);
   // the widest strip that still gives every CU a tile: rows are read once a strip
+  const bool wide = a.K % 512 == 0 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
   const long long tiles = mx4_row_tiles(a);
   const int cap = device_cus();
   int strip = even ? 512 : kTN;
@@ -348,11 +383,14 @@ hipError_t launch_mx4_tiles(const Mx4Args& a, hipStream_t s) {
   if (even && (tiles * ((a.N + 255) / 256) < cap || a.N <= 128)) strip = 128;
   const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * ((a.N + strip - 1) / strip);
   const dim3 g((unsigned)(most < cap ? most : cap));
+  if (most <= cap || g.x % kXcds) a.counter = nullptr;
+  else if (a.counter) launch_mx4_zero(a.counter, s);
   if (!even && a.xdtype == 1) MOE_LAUNCH("mx4_tiles", s, tiles_forward<1>, g, dim3(kThreads), 0, s, a, vec);
   else if (!even) MOE_LAUNCH("mx4_tiles", s, tiles_forward<3>, g, dim3(kThreads), 0, s, a, vec);
-  else if (strip == 512) MOE_LAUNCH("mx4_tiles_stream", s, tiles_stream<8>, g, dim3(512), 0, s, a);
-  else if (strip == 256) MOE_LAUNCH("mx4_tiles_stream", s, tiles_stream<4>, g, dim3(512), 0, s, a);
-  else MOE_LAUNCH("mx4_tiles_stream", s, tiles_stream<2>, g, dim3(512), 0, s, a);
+  else if (strip == 512 && wide) MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<8, true>), g, dim3(512), 0, s, a);
+  else if (strip == 512) MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<8, false>), g, dim3(512), 0, s, a);
+  else if (strip == 256) MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<4, false>), g, dim3(512), 0, s, a);
+  else MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<2, false>), g, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

@@ -44,9 +44,13 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, r = lane & 31, wn = wave & 3, wm = wave >> 2;
   const int nb = mx4_blocks(a.K), P = (nb + kBlocks - 1) / kBlocks;
-  const int G = gridDim.x, pos = G % 8 ? blockIdx.x : (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8;
-  for (int item = pos; item < items; item += G) {
-    const TileInfo t = tile_of(tiles, a, item, strips, kN4);
+  __shared__ int slot;
+  Deal deal{items, (int)gridDim.x, a.counter, &slot, 0u};
+  deal.ask();
+  for (int item = deal.first(), next = 0; item < items; item = next) {
+    next = deal.answer(item);
+    deal.ask();
+    const TileInfo t = tile_of(tiles, a, item, items, strips, kN4);
     // loads of a step: rows 16 wave + 8 u + l / 8 and matrix rows 32 wave + 8 u + l / 8, the block
     // that belongs at position l % 8; scales: row tid, or matrix row tid - 128
     uint32_t xoff[2], woff[4];
@@ -160,13 +164,15 @@ bool mx4_tiles4_can(const Mx4Args& a) {
   return a.xdtype == kMx4 && (a.perm ? a.T : a.A) * row < (1LL << 32) && a.N * row < (1LL << 32);
 }
 
-hipError_t launch_mx4_tiles4(const Mx4Args& a, hipStream_t s) {
+hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s) {
   const int nb = mx4_blocks(a.K);
   const bool quads = nb % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.ws) | reinterpret_cast<uintptr_t>(a.xs)) & 3) == 0;
   const long long strips = (a.N + kN4 - 1) / kN4;
   const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * strips;
   const int cap = device_cus();
   const dim3 g((unsigned)(most < cap ? most : cap));
+  if (most <= cap || g.x % kXcds) a.counter = nullptr;
+  else if (a.counter) launch_mx4_zero(a.counter, s);
   if (quads) MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<true>, g, dim3(kThreads4), 0, s, a);
   else MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<false>, g, dim3(kThreads4), 0, s, a);
   return hipGetLastError();

@@ -381,6 +381,9 @@ int moe_mx4_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t 
                             const uint8_t *w_codes, const uint8_t *w_scales, int32_t N, int32_t K,
                             void *dx, int32_t dxdtype, void *stream);
 
+/* Workspace bytes moe_mx4_experts_matmul needs (0 for a few rows). */
+size_t moe_mx4_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_shared);
+
 /* The same products for rows grouped by expert (moe_group, moe_route_group):
  * row s of [offsets[e], offsets[e+1]) is multiplied by matrix e of the E_tot =
  * E + has_shared matrices (w_codes [E_tot][N][B][16], w_scales [E_tot][N][B];
@@ -394,14 +397,16 @@ int moe_mx4_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t 
  * offsets: [E_tot + 1] (moe_group writes one more), perm: [A]; perm may be NULL
  * when gather == 0. Values of perm outside [0, A) are not detected; the kernels
  * stay in bounds and the results of those rows are unspecified; offsets are cut
- * to [0, A]. Types and rounding as moe_mx4_matmul. */
+ * to [0, A]. Types and rounding as moe_mx4_matmul. ws: at least ..._workspace_size
+ * bytes (any content, 16-byte aligned); calls that overlap in time must not
+ * share it. Results do not depend on which workgroup takes which rows. */
 int moe_mx4_experts_matmul(const void *x, const uint8_t *x_scales, int32_t xdtype, int64_t ldx,
                            int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t gather,
                            const int32_t *offsets, const int32_t *perm, const uint8_t *w_codes,
                            const uint8_t *w_scales, int32_t N, int32_t K, void *y, int32_t ydtype,
-                           void *stream);
+                           void *ws, size_t ws_bytes, void *stream);
 
-/* Workspace bytes moe_mx4_experts_matmul_backward needs (0 unless gather). */
+/* Workspace bytes moe_mx4_experts_matmul_backward needs. */
 size_t moe_mx4_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int32_t has_shared,
                                                       int32_t K, int32_t gather);
 
@@ -412,7 +417,7 @@ size_t moe_mx4_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int3
  *                j = 0 .. k-1, then the shared expert's, kept in float32 in ws
  *                ([A][K]) and rounded once. slot_of: [A] as moe_group writes it
  *                (else it may be NULL); values outside [0, A) add nothing.
- * ws: at least ..._workspace_size bytes (any content). */
+ * ws: at least ..._workspace_size bytes (any content, 16-byte aligned). */
 int moe_mx4_experts_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t T, int32_t k,
                                     int32_t E, int32_t has_shared, int32_t gather,
                                     const int32_t *offsets, const int32_t *slot_of,

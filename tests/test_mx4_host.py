@@ -74,11 +74,15 @@ def test_experts_refusals():
 
     def call(**kw):
         a = dict(x=FAKE, xs=None, t=moe.BF16, ld=64, T=4, k=2, E=8, sh=1, ga=1, off=FAKE, perm=FAKE, wc=FAKE, ws=FAKE,
-                 N=16, K=64, y=FAKE, yt=moe.BF16)
+                 N=16, K=64, y=FAKE, yt=moe.BF16, wk=None, nb=0)
         a.update(kw)
         return f(*a.values(), None)
 
     assert call(T=0, x=None, off=None, perm=None, wc=None, ws=None, y=None) == OK
+    assert moe.lib().moe_mx4_experts_matmul_workspace_size(4, 2, 1) == 0
+    need = moe.lib().moe_mx4_experts_matmul_workspace_size(4096, 2, 1)
+    assert need > 0
+    assert call(T=4096) == WSP and call(T=4096, wk=FAKE, nb=need - 1) == WSP and call(T=4096, wk=ODD, nb=need) == WSP
     for bad in (dict(T=-1), dict(k=0), dict(E=0), dict(sh=2), dict(ga=2), dict(off=None), dict(perm=None), dict(N=0),
                 dict(ld=63), dict(t=moe.MX4), dict(xs=FAKE), dict(y=None)):
         assert call(**bad) == INV, bad

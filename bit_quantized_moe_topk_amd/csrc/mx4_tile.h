@@ -25,9 +25,11 @@ struct TileInfo {
 
 // Tiles of a launch: base[e] = the tiles before group e (of one strip of matrix
 // rows). 16 bits do: at most 2^22 rows in tiles of up to 128, and one more a group.
-struct Tiles {
-  uint16_t base[MOE_MAX_E_DEV + 4];
+template <int CAP>
+struct TilesOf {
+  uint16_t base[CAP];
 };
+typedef TilesOf<MOE_MAX_E_DEV + 4> Tiles;
 
 // Memory that tiles_init needs besides, free afterwards (past a barrier).
 struct TilesScratch {
@@ -37,7 +39,8 @@ struct TilesScratch {
 
 __device__ inline int first_row(const Mx4Args& a, int e) { return min(max(a.offsets[e], 0), a.A); }
 
-__device__ inline int tiles_init(Tiles& t, TilesScratch& w, const Mx4Args& a) {
+template <int CAP>
+__device__ inline int tiles_init(TilesOf<CAP>& t, TilesScratch& w, const Mx4Args& a) {
   if (!a.offsets) return (a.A + kTM - 1) / kTM;
   for (int e = threadIdx.x; e < a.E_tot; e += blockDim.x)
     w.base[e] = max(0, first_row(a, e + 1) - first_row(a, e) + kTM - 1) / kTM;
@@ -49,7 +52,8 @@ __device__ inline int tiles_init(Tiles& t, TilesScratch& w, const Mx4Args& a) {
 }
 
 // The last group whose first tile is at most ti.
-__device__ inline int tile_group(const Tiles& t, int E_tot, int ti) {
+template <int CAP>
+__device__ inline int tile_group(const TilesOf<CAP>& t, int E_tot, int ti) {
   int lo = 0, hi = E_tot;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -60,7 +64,8 @@ __device__ inline int tile_group(const Tiles& t, int E_tot, int ti) {
 }
 
 // Item `id` of `items` (counted from the last group's end), strips of `strip` matrix rows.
-__device__ inline TileInfo tile_of(const Tiles& t, const Mx4Args& a, int id, int items, int strips, int strip) {
+template <int CAP>
+__device__ inline TileInfo tile_of(const TilesOf<CAP>& t, const Mx4Args& a, int id, int items, int strips, int strip) {
   TileInfo i;
   const int item = items - 1 - id, ti = item / strips;
   int r0 = 0, rows = a.A, of = (a.A + kTM - 1) / kTM, j = ti;
@@ -141,7 +146,11 @@ __device__ inline void stream4(const void* base, uint32_t off, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(off), "s"(base) : "memory");
 }
-__device__ inline void stream4(const void* src, uint32_t to) {  // an address of each lane's own
+__device__ inline void stream16(const void* src, uint32_t to) {  // an address of each lane's own
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(src) : "memory");
+}
+__device__ inline void stream4(const void* src, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :: "s"(__builtin_amdgcn_readfirstlane(to)), "v"(src) : "memory");
 }

@@ -189,7 +189,7 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
   constexpr int kWL = WN / 2;    // code loads per wave and step (16 matrix rows each)
   constexpr int kS = WIDE ? 4 : 1;  // dwords of scales per load and matrix row
   __shared__ StreamBuf<WN> buf[2];
-  __shared__ uint32_t scales[2][64 * WN * kS];
+  __shared__ __attribute__((aligned(16))) uint32_t scales[2][64 * WN * kS];
   __shared__ Tiles tiles;
   constexpr int strip = 64 * WN;
   const int strips = (a.N + strip - 1) / strip;

@@ -20,7 +20,6 @@ constexpr int kThreads4 = 512;
 struct Buf4 {
   uint4 x[kTM * kBlocks];   // row m: its eight blocks, as chunk_at places them
   uint4 w[kN4 * kBlocks];
-  uint32_t s[2][kTM + kN4];  // scales of the rows, then of the matrix rows: four blocks and four
 };
 
 // Eight scale bytes from block b of a row of nb.
@@ -31,14 +30,25 @@ __device__ inline uint2 load_scales(const uint8_t* row, int b, int nb) {
   return make_uint2(v[0] | v[1] << 8 | v[2] << 16 | v[3] << 24, v[4] | v[5] << 8 | v[6] << 16 | v[7] << 24);
 }
 
-// QUADS: scales can be read four bytes at a time (a multiple of four blocks,
-// aligned) and come as direct loads too; else through registers, which waits
-// for more than it needs.
-template <bool QUADS>
+// How scales come. A direct load costs by the 128-byte lines that it touches,
+// so the fewer loads bring a row's scales the better.
+//   kBytes : a byte at a time through registers (any K), which also waits for
+//            more than it needs
+//   kQuads : four at a time (a multiple of four blocks, aligned), two loads a step
+//   kWide  : sixteen at a time (a multiple of 16 blocks, aligned), a load for two
+//            steps; what LDS is left holds up to kWideGroups groups' tiles
+enum Scales { kBytes, kQuads, kWide };
+constexpr int kWideGroups = 2040;
+
+template <int S>
 __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
-  constexpr int kLoads = QUADS ? 6 : 4;  // direct loads per wave and step, besides the rows'
+  constexpr int kCodes = 4;                                         // direct loads a wave and step, of codes,
+  constexpr int kScaleLoads = S == kQuads ? 2 : S == kWide ? 1 : 0;  // and of scales (kWide: every other step)
+  constexpr int kRowsS = kTM + kN4;  // the rows' scales, then the matrix rows'
   __shared__ Buf4 buf[kBufs];
-  __shared__ Tiles tiles;
+  // kWide: two places of 16 a row; else per buffer four blocks and four
+  __shared__ __attribute__((aligned(16))) uint32_t scale[S == kWide ? 2 * 4 * kRowsS : kBufs * 2 * kRowsS];
+  __shared__ TilesOf<S == kWide ? kWideGroups : MOE_MAX_E_DEV + 4> tiles;
   const int strips = (a.N + kN4 - 1) / kN4;
   const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(buf), a) * strips;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -63,7 +73,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) woff[u] = (uint32_t)min(t.n0 + 32 * wave + 8 * u + (lane >> 3), a.N - 1) * (16 * nb);
     const char* wbase = reinterpret_cast<const char*>(a.wc) + (size_t)t.e * a.N * nb * 16;
-    const int sr = QUADS ? 48 * wave + min(lane, 47) : min(tid, kTM + kN4 - 1);
+    const int sr = S != kBytes ? 48 * wave + min(lane, 47) : min(tid, kRowsS - 1);
     const uint8_t* srow = sr < kTM ? a.xs + (size_t)max(mx4_row(a, t.s0 + min(sr, t.M - 1)), 0) * nb
                                    : a.ws + ((size_t)t.e * a.N + min(t.n0 + sr - kTM, a.N - 1)) * nb;
     const bool rows = 16 * wave < ((t.M + 31) & ~31);  // whether this wave loads rows
@@ -80,16 +90,19 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
         const int n = 32 * wave + 8 * u + (lane >> 3);
         stream16(wbase, woff[u] + 16 * min(kBlocks * p + (q ^ ((n >> 1) & 7)), nb - 1), lds_offset(B.w) + 1024 * (4 * wave + u));
       }
-      if constexpr (QUADS) {
+      uint32_t* sc = scale + (S == kWide ? (p >> 1 & 1) * 4 * kRowsS : p % kBufs * 2 * kRowsS);
+      if constexpr (S == kWide) {
+        if (p % 2 == 0 && lane < 48) stream16(srow + 8 * p, lds_offset(sc) + 768 * wave);
+      } else if constexpr (S == kQuads) {
         if (lane < 48) {
 #pragma unroll
           for (int z = 0; z < 2; ++z)
-            stream4(srow + min(kBlocks * p + 4 * z, nb - 4), lds_offset(B.s[z]) + 192 * wave);
+            stream4(srow + min(kBlocks * p + 4 * z, nb - 4), lds_offset(sc + z * kRowsS) + 192 * wave);
         }
-      } else if (tid < kTM + kN4) {
+      } else if (tid < kRowsS) {
         const uint2 v = load_scales(srow, kBlocks * p, nb);
-        B.s[0][tid] = v.x;
-        B.s[1][tid] = v.y;
+        sc[tid] = v.x;
+        sc[kRowsS + tid] = v.y;
       }
     };
     const int R = (t.M + 31) / 32, run0 = wm ? (R + 1) / 2 : 0, live = wm ? R / 2 : (R + 1) / 2;
@@ -100,12 +113,18 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
       for (int j = 0; j < 2; ++j) acc[i][j] = floatx16_t{};
     load(0);
     if (P > 1) load(1);
-    auto done = [&](bool more) __attribute__((always_inline)) {  // all but the last load() have landed
-      if (!more) step_done();
-      else if (rows) step_done<kLoads + 2>();
-      else step_done<kLoads>();
+    // all but the last load(), of step p, have landed
+    auto done = [&](int p) __attribute__((always_inline)) {
+      if (p >= P) step_done();
+      else if (S == kWide && p % 2) {
+        if (rows) step_done<kCodes + 2>();
+        else step_done<kCodes>();
+      } else {
+        if (rows) step_done<kCodes + 2 + kScaleLoads>();
+        else step_done<kCodes + kScaleLoads>();
+      }
     };
-    done(P > 1);
+    done(1);
     for (int p = 0; p < P; ++p) {
       if (p + 2 < P) load(p + 2);  // into step p - 1's buffer, which every wave has left
       const Buf4& B = buf[p % kBufs];
@@ -115,16 +134,16 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
         const uint32_t m0 = left >= 4 ? ~0u : (1u << 8 * left) - 1u;
         const uint32_t m1 = left >= 8 ? ~0u : left <= 4 ? 0u : (1u << 8 * (left - 4)) - 1u;
         uint2 sw[2], sx[2];
+        const uint32_t* sc = scale + (S == kWide ? (p >> 1 & 1) * 4 * kRowsS : p % kBufs * 2 * kRowsS);
+        auto scales_of = [&](int row) {
+          const uint2 v = S == kWide ? *reinterpret_cast<const uint2*>(sc + 4 * row + 2 * (p & 1))
+                                     : make_uint2(sc[row], sc[kRowsS + row]);
+          return make_uint2(v.x & m0, v.y & m1);
+        };
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int n = kTM + 64 * wn + 32 * j + r;
-          sw[j] = make_uint2(B.s[0][n] & m0, B.s[1][n] & m1);
-        }
+        for (int j = 0; j < 2; ++j) sw[j] = scales_of(kTM + 64 * wn + 32 * j + r);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int m = 32 * min(run0 + i, 3) + r;
-          sx[i] = make_uint2(B.s[0][m] & m0, B.s[1][m] & m1);
-        }
+        for (int i = 0; i < 2; ++i) sx[i] = scales_of(32 * min(run0 + i, 3) + r);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           int8v_t w[2], x[2];
@@ -148,7 +167,7 @@ __global__ __launch_bounds__(kThreads4, 2) void tiles_mx4(Mx4Args a) {
         }
       }
       // the next step's loads have landed; this iteration's may be in flight
-      done(p + 2 < P);
+      done(p + 2);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -166,15 +185,19 @@ bool mx4_tiles4_can(const Mx4Args& a) {
 
 hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s) {
   const int nb = mx4_blocks(a.K);
-  const bool quads = nb % 4 == 0 && ((reinterpret_cast<uintptr_t>(a.ws) | reinterpret_cast<uintptr_t>(a.xs)) & 3) == 0;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.ws) | reinterpret_cast<uintptr_t>(a.xs);
   const long long strips = (a.N + kN4 - 1) / kN4;
   const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * strips;
   const int cap = device_cus();
   const dim3 g((unsigned)(most < cap ? most : cap));
   if (most <= cap || g.x % kXcds) a.counter = nullptr;
   else if (a.counter) launch_mx4_zero(a.counter, s);
-  if (quads) MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<true>, g, dim3(kThreads4), 0, s, a);
-  else MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<false>, g, dim3(kThreads4), 0, s, a);
+  if (nb % 16 == 0 && at % 16 == 0 && a.E_tot <= kWideGroups)
+    MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<kWide>, g, dim3(kThreads4), 0, s, a);
+  else if (nb % 4 == 0 && at % 4 == 0)
+    MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<kQuads>, g, dim3(kThreads4), 0, s, a);
+  else
+    MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<kBytes>, g, dim3(kThreads4), 0, s, a);
   return hipGetLastError();
 }
 

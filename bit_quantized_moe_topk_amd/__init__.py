@@ -22,6 +22,7 @@ The *_backward calls are explicit: no call here records a graph for autograd.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass
 
@@ -665,6 +666,12 @@ def _groups(grouping: Grouping, w: Mx4, tokens: int | None, dev: torch.device):
     return tokens, max(1, A // tokens - shared if tokens else 1), E, shared, A
 
 
+@functools.lru_cache(maxsize=256)
+def _bytes(name: str, *sizes: int) -> int:
+    """A *_workspace_size call's answer, which depends on the sizes alone."""
+    return getattr(lib(), name)(*sizes)
+
+
 def _workspace(given: torch.Tensor | None, n: int, dev: torch.device):
     """(pointer, bytes, tensor) of the caller's workspace, or of a new one of n bytes."""
     if given is None:
@@ -694,7 +701,7 @@ def mx4_experts_matmul(x, w: Mx4, grouping: Grouping, tokens: int | None = None,
     if gather:
         _int32("grouping.perm", grouping.perm, dev, A)
     y = _result(out, (A, N), dtype or own, dev)
-    wp, wn, keep = _workspace(workspace, lib().moe_mx4_experts_matmul_workspace_size(T, k, shared), dev)
+    wp, wn, keep = _workspace(workspace, _bytes("moe_mx4_experts_matmul_workspace_size", T, k, shared), dev)
     _call("moe_mx4_experts_matmul", dev, p, s, code, ld, T, k, E, shared, int(gather), grouping.offsets.data_ptr(),
           grouping.perm.data_ptr() if gather else None, w.codes.data_ptr(), w.scales.data_ptr(), N, w.K, y.data_ptr(),
           _FLOATS[y.dtype], wp, wn)
@@ -718,7 +725,7 @@ def mx4_experts_matmul_backward(dy: torch.Tensor, w: Mx4, grouping: Grouping, to
         _int32("grouping.slot_of", grouping.slot_of, dev, A)
     dx = _result(out, (T, w.K), dtype or dy.dtype, dev)
     wp, wn, keep = _workspace(
-        workspace, lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, w.K, int(gather)), dev)
+        workspace, _bytes("moe_mx4_experts_matmul_backward_workspace_size", T, k, shared, w.K, int(gather)), dev)
     _call("moe_mx4_experts_matmul_backward", dev, dy.data_ptr(), code, ld, T, k, E, shared, int(gather),
           grouping.offsets.data_ptr(), grouping.slot_of.data_ptr() if gather else None, w.codes.data_ptr(),
           w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dx.dtype], wp, wn)
@@ -768,7 +775,7 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tens
         if out.losses.numel() != 2 or out.counts.numel() != E or out.kept.numel() != 1 or out.losses.device != dev:
             raise ValueError("out does not match the logits")
         out.k = k
-    wp, wn, keep_ws = _workspace(workspace, lib().moe_balance_loss_workspace_size(T, k, E), dev)
+    wp, wn, keep_ws = _workspace(workspace, _bytes("moe_balance_loss_workspace_size", T, k, E), dev)
     _call("moe_balance_loss", dev, logits.data_ptr(), code, ld, T, E, k, idx.data_ptr(), keep, out.losses.data_ptr(),
           out.counts.data_ptr(), out.kept.data_ptr(), wp, wn)
     return out

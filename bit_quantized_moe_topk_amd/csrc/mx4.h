@@ -110,12 +110,18 @@ __device__ inline int mx4_row(const Mx4Args& a, int s) {
 }
 
 // The group of row s: how many of offsets[1 .. E_tot] are at most s (one wave,
-// every lane gets it). E_tot: the row is behind the last group.
+// every lane gets it; 512 offsets on their way at once). E_tot: the row is
+// behind the last group.
 __device__ inline int mx4_group_of(const int32_t* __restrict__ offsets, int E_tot, int s) {
   const int lane = threadIdx.x & 63;
   int e = 0;
-  for (int b = 0; b < E_tot; b += 64)
-    e += __popcll(__ballot(b + lane < E_tot && offsets[1 + b + lane] <= s));
+  for (int b = 0; b < E_tot; b += 512) {
+    int v[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) v[z] = offsets[min(b + 64 * z + lane, E_tot - 1) + 1];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) e += __popcll(__ballot(b + 64 * z + lane < E_tot && v[z] <= s));
+  }
   return e;
 }
 

@@ -43,7 +43,7 @@ __device__ inline void store_out(const Mx4Args& a, size_t i, float v) {
   else static_cast<float*>(a.y)[i] = v;
 }
 
-// Four waves share K in chunks of 128: lane (r, g) holds block g of a chunk of
+// Four waves share K in whole chunks of 128: lane (r, g) holds block g of a chunk of
 // matrix row r (its 16 bytes of codes, one scale) and of x's row r. A product
 // step takes eight values of each of the four blocks; the order of K within a
 // chunk is the same for both operands, which is all that matters. Microscaled
@@ -71,17 +71,18 @@ __global__ __launch_bounds__(256) void rows_forward(Mx4Args a, bool vec) {
   floatx4_t acc[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j] = floatx4_t{};
-  for (int b0 = 4 * wave; b0 < nb; b0 += 16 * kAhead) {
+  const int share = 4 * ((nb + 15) / 16), end = min(nb, share * (wave + 1));  // blocks of a wave, whole chunks
+  for (int b0 = share * wave; b0 < end; b0 += 4 * kAhead) {
     uint4 c[kAhead][NT];
     uint32_t sw[kAhead][NT];
 #pragma unroll
     for (int z = 0; z < kAhead; ++z) {
-      const int b = b0 + 16 * z + g;
+      const int b = b0 + 4 * z + g;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         c[z][j] = make_uint4(0, 0, 0, 0);
         sw[z][j] = 0;
-        if (b < nb) {
+        if (b < end) {
           c[z][j] = wc[j][b];
           sw[z][j] = ws[j][b];
         }
@@ -89,12 +90,12 @@ __global__ __launch_bounds__(256) void rows_forward(Mx4Args a, bool vec) {
     }
 #pragma unroll
     for (int z = 0; z < kAhead; ++z) {
-      const int b = b0 + 16 * z + g;
-      if (b0 + 16 * z >= nb) break;
+      const int b = b0 + 4 * z + g;
+      if (b0 + 4 * z >= end) break;
       if constexpr (XT == kMx4) {
         uint4 xc = make_uint4(0, 0, 0, 0);
         uint32_t sx = 0;
-        if (b < nb && xr >= 0) {
+        if (b < end && xr >= 0) {
           xc = reinterpret_cast<const uint4*>(a.x)[(size_t)xr * nb + b];
           sx = a.xs[(size_t)xr * nb + b];
         }

@@ -24,7 +24,8 @@ struct TileInfo {
 };
 
 // Tiles of a launch: base[e] = the tiles before group e (of one strip of matrix
-// rows). 16 bits do: at most 2^22 rows in tiles of up to 128, and one more a group.
+// rows). 16 bits do for 2^22 rows in tiles of up to 128, and one more a group
+// (tiles of 32 are for few rows).
 template <int CAP>
 struct TilesOf {
   uint16_t base[CAP];
@@ -33,22 +34,44 @@ typedef TilesOf<MOE_MAX_E_DEV + 4> Tiles;
 
 // Memory that tiles_init needs besides, free afterwards (past a barrier).
 struct TilesScratch {
-  int base[MOE_MAX_E_DEV + 4];
+  int first[MOE_MAX_E_DEV + 4];  // first row of each group, and the end
   int wsum[16];
 };
 
 __device__ inline int first_row(const Mx4Args& a, int e) { return min(max(a.offsets[e], 0), a.A); }
 
-template <int CAP>
+template <int TM = kTM, int CAP>
 __device__ inline int tiles_init(TilesOf<CAP>& t, TilesScratch& w, const Mx4Args& a) {
-  if (!a.offsets) return (a.A + kTM - 1) / kTM;
-  for (int e = threadIdx.x; e < a.E_tot; e += blockDim.x)
-    w.base[e] = max(0, first_row(a, e + 1) - first_row(a, e) + kTM - 1) / kTM;
+  if (!a.offsets) return (a.A + TM - 1) / TM;
+  constexpr int kAtOnce = 8;  // offsets on their way per thread
+  const int tid = threadIdx.x, nt = blockDim.x;
+  for (int e0 = tid; e0 <= a.E_tot; e0 += kAtOnce * nt) {
+    int v[kAtOnce];
+#pragma unroll
+    for (int z = 0; z < kAtOnce; ++z) v[z] = a.offsets[min(e0 + z * nt, a.E_tot)];
+#pragma unroll
+    for (int z = 0; z < kAtOnce; ++z)
+      if (e0 + z * nt <= a.E_tot) w.first[e0 + z * nt] = min(max(v[z], 0), a.A);
+  }
   __syncthreads();
-  const int n = block_exclusive_scan(w.base, a.E_tot, w.wsum);
-  for (int e = threadIdx.x; e < a.E_tot; e += blockDim.x) t.base[e] = (uint16_t)min(w.base[e], 65535);
+  // this thread's groups are neighbours: their tiles, the sum of all before, and the places
+  const int per = (a.E_tot + nt - 1) / nt, lo = min(a.E_tot, tid * per), hi = min(a.E_tot, lo + per);
+  int n = 0;
+  for (int e = lo; e < hi; ++e) n += max(0, w.first[e + 1] - w.first[e] + TM - 1) / TM;
+  const int incl = wave_inclusive_scan(n);
+  if ((tid & 63) == 63) w.wsum[tid >> 6] = incl;
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(min(n, 65535));  // more only where groups overlap, as they must not
+  int at = incl - n, all = 0;
+  for (int i = 0; i < nt >> 6; ++i) {
+    if (i < tid >> 6) at += w.wsum[i];
+    all += w.wsum[i];
+  }
+  for (int e = lo; e < hi; ++e) {
+    t.base[e] = (uint16_t)min(at, 65535);
+    at += max(0, w.first[e + 1] - w.first[e] + TM - 1) / TM;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(min(all, 65535));  // more only where groups overlap, as they must not
 }
 
 // The last group whose first tile is at most ti.
@@ -64,18 +87,18 @@ __device__ inline int tile_group(const TilesOf<CAP>& t, int E_tot, int ti) {
 }
 
 // Item `id` of `items` (counted from the last group's end), strips of `strip` matrix rows.
-template <int CAP>
+template <int TM = kTM, int CAP>
 __device__ inline TileInfo tile_of(const TilesOf<CAP>& t, const Mx4Args& a, int id, int items, int strips, int strip) {
   TileInfo i;
   const int item = items - 1 - id, ti = item / strips;
-  int r0 = 0, rows = a.A, of = (a.A + kTM - 1) / kTM, j = ti;
+  int r0 = 0, rows = a.A, of = (a.A + TM - 1) / TM, j = ti;
   i.e = 0;
   if (a.offsets) {
     i.e = __builtin_amdgcn_readfirstlane(tile_group(t, a.E_tot, ti));
     r0 = __builtin_amdgcn_readfirstlane(first_row(a, i.e));
     rows = __builtin_amdgcn_readfirstlane(first_row(a, i.e + 1)) - r0;
     j = ti - __builtin_amdgcn_readfirstlane((int)t.base[i.e]);
-    of = (rows + kTM - 1) / kTM;
+    of = (rows + TM - 1) / TM;
   }
   const int runs = (rows + 31) / 32;
   const int a0 = (int)((long long)j * runs / of) * 32, a1 = (int)((long long)(j + 1) * runs / of) * 32;

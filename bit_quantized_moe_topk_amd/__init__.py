@@ -564,6 +564,15 @@ class Mx4:
             raise ValueError("codes and scales must be on one device")
         self.codes, self.scales, self.K = codes, scales, K
 
+    @classmethod
+    def _new(cls, shape, K: int, dev: torch.device) -> "Mx4":
+        """Room for rows [*shape, K]."""
+        self, B = object.__new__(cls), (K + 31) // 32
+        self.codes = torch.empty((*shape, 16 * B), dtype=torch.uint8, device=dev)
+        self.scales = torch.empty((*shape, B), dtype=torch.uint8, device=dev)
+        self.K = K
+        return self
+
     @property
     def shape(self) -> tuple:
         return (*self.codes.shape[:-1], self.K)
@@ -584,9 +593,7 @@ def mx4_quantize(x: torch.Tensor, out: Mx4 | None = None) -> Mx4:
     flat = x if x.dim() == 2 else x.reshape(-1, K)
     code, ld, rows = _rows("x", flat)
     if out is None:
-        B = (K + 31) // 32
-        out = Mx4(torch.empty((*x.shape[:-1], 16 * B), dtype=torch.uint8, device=x.device),
-                  torch.empty((*x.shape[:-1], B), dtype=torch.uint8, device=x.device), K)
+        out = Mx4._new(x.shape[:-1], K, x.device)
     elif out.shape != tuple(x.shape) or out.device != x.device:
         raise ValueError(f"out must be an Mx4 of {tuple(x.shape)} on {x.device}")
     _call("moe_mx4_quantize", x.device, flat.data_ptr(), code, ld, rows, K, out.codes.data_ptr(),

@@ -374,13 +374,13 @@ hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s) {
   // streamed: 32-bit offsets within one matrix and within the rows
   const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && a.K >= 2 * kStep && (long long)a.N * a.K < (1LL << 32) &&
                     (a.perm ? a.T : a.A) * a.ldx * 2 < (1LL << 32);
+  const bool wide = a.K % 512 == 0 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
+  const long long tiles = mx4_row_tiles(a);
+  const int cap = device_cus();
   // The widest strip that still gives every CU a tile: rows are read once a strip. Of groups some
   // stay empty, so with long rows, where a CU without a tile costs more than a tile too many, half
   // as many more are asked for ([1024, 2048], 8 tokens x 11: 16.3 us against 20.9 in strips of 256;
   // 16 tokens 21 against 30 in strips of 512; [2048, 512], 4 tokens: 10.4 against 13.9 the other way).
-  const bool wide = a.K % 512 == 0 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
-  const long long tiles = mx4_row_tiles(a);
-  const int cap = device_cus();
   int strip = even ? 512 : kTN;
   const int want = a.offsets && a.K >= 1024 ? cap + cap / 2 : cap;
   if (even && (tiles * ((a.N + 511) / 512) < want || a.N <= 256)) strip = 256;

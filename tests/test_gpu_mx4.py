@@ -166,6 +166,48 @@ def test_matmul_backward(T, N, K, kind):
                   size, N * (3 if kind == "f32" else 1))
 
 
+# Rows enough for the tile kernels, each form of them: strips of 512, 256 and 128 matrix rows, scales
+# four and sixteen at a time, one at a time; columns in no whole step or block; rows that end a run,
+# a tile, or one past it.
+MANY = [(33000, 260, 512), (33025, 260, 384), (33000, 130, 256), (1100, 1040, 512), (1153, 1040, 384), (1100, 1040, 100),
+        (2000, 800, 72), (4100, 513, 640)]
+
+
+@pytest.mark.parametrize("T,N,K", MANY)
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx4"])
+def test_matmul_many_rows(T, N, K, kind):
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + N + K)
+    w, wv = random_matrix(rng, (N,), K)
+    x, xv = random_rows(rng, T, K, kind, strided=kind == "bf16" and T % 2 == 1)
+    ref, size = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    y = moe.mx4_matmul(x, w)
+    check(f"{kind} {T}x{N}x{K}", y, ref, size, K * (3 if kind == "f32" else 1))
+    assert torch.equal(moe.mx4_matmul(x, w), y)
+    if kind != "f32":
+        check(f"{kind} {T}x{N}x{K} -> f32", moe.mx4_matmul(x, w, dtype=torch.float32), ref, size, K)
+
+
+MANY_BACK = [(1300, 192, 2176), (1301, 64, 2176), (1300, 200, 2176), (1300, 192, 2100), (2600, 70, 2100), (33000, 128, 512)]
+
+
+@pytest.mark.parametrize("T,N,K", MANY_BACK)
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_matmul_backward_many_rows(T, N, K, kind):
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + N + K)
+    w, wv = random_matrix(rng, (N,), K)
+    d, dv = random_rows(rng, T, N, kind)
+    ref, size = dv @ wv, np.abs(dv) @ np.abs(wv)
+    g = moe.mx4_matmul_backward(d, w)
+    check(f"gradient {kind} {T}x{N}x{K}", g, ref, size, N * (3 if kind == "f32" else 1))
+    assert torch.equal(moe.mx4_matmul_backward(d, w), g)
+    if kind == "bf16":
+        check(f"gradient {kind} {T}x{N}x{K} -> f32", moe.mx4_matmul_backward(d, w, dtype=torch.float32), ref, size, N)
+
+
 def test_gradient_against_differences():
     """The product is linear in x, so a difference quotient is exact up to its own roundings: with x, h and the
     weights small integers over powers of two every sum here is exact in float32, and so both sides are equal."""
@@ -246,7 +288,10 @@ def test_results_repeat_and_leave_the_rest_alone():
 GROUPS = [  # T, k, E, shared, N, K, skew, experts that get nothing
     (1, 1, 1, False, 16, 32, 0, 0), (1, 2, 8, True, 40, 70, 0, 3), (4, 10, 64, True, 128, 256, 1, 20),
     (37, 3, 5, False, 100, 96, 1, 1), (64, 8, 300, True, 64, 64, 1, 100), (130, 2, 4, True, 272, 160, 1, 1),
-    (300, 4, 16, False, 130, 288, 0.5, 4), (1500, 2, 6, True, 64, 128, 2, 2)]
+    (300, 4, 16, False, 130, 288, 0.5, 4), (1500, 2, 6, True, 64, 128, 2, 2),
+    # more tiles than CUs, taken from the queues; long and short rows; a crowded group among empty ones
+    (1200, 3, 400, True, 600, 512, 0.3, 50), (1100, 2, 300, True, 640, 384, 0, 0), (900, 6, 2047, True, 128, 256, 0.5, 900),
+    (700, 3, 300, True, 576, 1024, 3, 0)]
 
 
 @pytest.mark.parametrize("T,k,E,shared,N,K,skew,quiet", GROUPS)

@@ -264,6 +264,52 @@ def test_special_values(kind):
         assert np.isfinite(np.delete(g, 2, 0)[:, :64]).all() and np.isfinite(np.delete(g, 2, 0)[:, 96:]).all()
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 40, 70), (9, 33, 130), (40, 300, 100), (300, 300, 100), (1100, 1040, 33), (1100, 200, 2100)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_what_lies_around_the_rows_is_not_read_into_them(T, N, K, kind):
+    """Rows cut out of a wider array of NaN, products and gradients of them: every result is a number."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + N + K)
+    w, wv = random_matrix(rng, (N,), K)
+    terms = 3 if kind == "f32" else 1
+    for n, ref_of, call in ((K, wv.T, moe.mx4_matmul), (N, wv, moe.mx4_matmul_backward)):
+        for lead in (8, 3):
+            room = torch.full((T + 2, n + 48), float("nan"), device="cuda", dtype=types()[kind])
+            x = room[1:-1, lead:lead + n]
+            x.copy_(torch.from_numpy(rng.standard_normal((T, n))))
+            xv = as64(x)
+            check(f"{call.__name__} {kind} {T}x{N}x{K} among NaN", call(x, w), xv @ ref_of, np.abs(xv) @ np.abs(ref_of), n * terms)
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 520, 512), (300, 520, 384), (1100, 1040, 512), (1100, 1040, 100), (2100, 1100, 1024)])
+@pytest.mark.parametrize("kind", ["bf16", "f32", "mx4"])
+def test_special_values_of_many_rows(T, N, K, kind):
+    """NaN blocks, infinities and overflow reach their own outputs alone in the tile kernels too."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + N + K)
+    w, wv = random_matrix(rng, (N,), K, 120, 126)
+    w.scales[7, 2], w.scales[N - 1, -1] = 255, 255
+    rest = np.setdiff1d(np.arange(N), [7, N - 1])
+    x, xv = random_rows(rng, T, K, kind)
+    if kind == "mx4":
+        x.scales[T - 1, 1] = 255
+        lost = [T - 1]
+    else:
+        x[T - 1, K - 1], x[4, 9] = float("nan"), float("inf")
+        x[6] *= 2.0 ** 100
+        xv, lost = as64(x), [4, T - 1]
+    y = as64(moe.mx4_matmul(x, w, dtype=torch.float32))
+    assert np.isnan(y[T - 1]).all() and np.isnan(y[:, [7, N - 1]]).all()
+    if kind != "mx4":
+        bad = y[4][rest]
+        assert not np.isfinite(bad[wv[rest, 9] != 0]).any() and np.isnan(bad[wv[rest, 9] == 0]).all()
+    rows = np.setdiff1d(np.arange(T), lost)
+    ref, size = xv[rows] @ wv[rest].T, np.abs(xv[rows]) @ np.abs(wv[rest]).T
+    assert (np.abs(y[np.ix_(rows, rest)] - ref) <= (3 * K + 3) * 2.0 ** -24 * size + 2.0 ** -148).all()
+
+
 def test_results_repeat_and_leave_the_rest_alone():
     torch = torch_cuda()
     import bit_quantized_moe_topk_amd as moe

@@ -34,7 +34,8 @@ int check_product(const void* x, const uint8_t* xs, int32_t dtype, int64_t ld, i
 int check_groups(int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t gather) {
   if (T < 0 || k < 1 || E < 1 || (has_shared != 0 && has_shared != 1) || (gather != 0 && gather != 1))
     return MOE_ERR_INVALID_ARG;
-  if (E + has_shared > MOE_MAX_E + 1 || (long long)T * (k + has_shared) > kMaxRows) return MOE_ERR_UNSUPPORTED;
+  if (E > MOE_MAX_E + 1 - has_shared || k > kMaxRows || (k + (long long)has_shared) * T > kMaxRows)
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

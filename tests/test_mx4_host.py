@@ -104,6 +104,20 @@ def test_experts_refusals():
     assert back(T=0, dy=None, dx=None, wk=None, nb=0) == OK
 
 
+def test_experts_sizes_past_every_integer():
+    """Sums and products of the sizes that pass 32 bits are refused, not wrapped."""
+    f, b = moe.lib().moe_mx4_experts_matmul, moe.lib().moe_mx4_experts_matmul_backward
+    top = 2 ** 31 - 1
+    for T, k, E, shared in ((4, top, 8, 1), (top, top, 8, 1), (4, 2, top, 1), (4, 2, top, 0), (0, top, 8, 1), (2, 2 ** 30, 8, 0)):
+        for gather in (0, 1):
+            assert f(FAKE, None, moe.BF16, 64, T, k, E, shared, gather, FAKE, FAKE, FAKE, FAKE, 16, 64, FAKE, moe.BF16,
+                     FAKE, 1 << 40, None) == UNS, (T, k, E, shared)
+            assert b(FAKE, moe.BF16, 64, T, k, E, shared, gather, FAKE, FAKE, FAKE, FAKE, 16, 64, FAKE, moe.BF16, FAKE,
+                     1 << 40, None) == UNS, (T, k, E, shared)
+        assert moe.lib().moe_mx4_experts_matmul_workspace_size(T, k, shared) == 0 or E == top
+        assert moe.lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, shared, 64, 1) == 0 or E == top
+
+
 def test_balance_refusals():
     f, size = moe.lib().moe_balance_loss, moe.lib().moe_balance_loss_workspace_size
     need = size(64, 10, 512)

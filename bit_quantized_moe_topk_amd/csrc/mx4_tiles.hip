@@ -371,8 +371,9 @@ __global__ __launch_bounds__(512, 2) void tiles_stream(Mx4Args a) {
 
 hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s) {
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
-  // streamed: 32-bit offsets within one matrix and within the rows
-  const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && a.K >= 2 * kStep && (long long)a.N * a.K < (1LL << 32) &&
+  // streamed: scales on four bytes, 32-bit offsets within one matrix and within the rows
+  const bool even = a.xdtype == 1 && vec && a.K % kStep == 0 && a.K >= 2 * kStep &&
+                    (reinterpret_cast<uintptr_t>(a.ws) & 3) == 0 && (long long)a.N * a.K < (1LL << 32) &&
                     (a.perm ? a.T : a.A) * a.ldx * 2 < (1LL << 32);
   const bool wide = a.K % 512 == 0 && (reinterpret_cast<uintptr_t>(a.ws) & 15) == 0;
   const long long tiles = mx4_row_tiles(a);

@@ -310,6 +310,33 @@ def test_special_values_of_many_rows(T, N, K, kind):
     assert (np.abs(y[np.ix_(rows, rest)] - ref) <= (3 * K + 3) * 2.0 ** -24 * size + 2.0 ** -148).all()
 
 
+@pytest.mark.parametrize("at", [1, 2, 4])
+@pytest.mark.parametrize("T", [3, 1100, 33000])
+def test_scales_that_start_anywhere(T, at):
+    """Scales need no alignment: those of a matrix and of rows that start 1, 2 or 4 bytes into a buffer."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + at)
+    N, K = 300, 512
+
+    def moved(q):
+        room = torch.empty(q.scales.numel() + 16, dtype=torch.uint8, device="cuda")
+        s = room[at:at + q.scales.numel()].view(q.scales.shape)
+        s.copy_(q.scales)
+        return moe.Mx4(q.codes, s, q.K)
+
+    w, wv = random_matrix(rng, (N,), K)
+    x, xv = random_rows(rng, T, K, "bf16")
+    q, qv = random_matrix(rng, (T,), K)
+    d, dv = random_rows(rng, T, 320, "bf16")
+    v, vv = random_matrix(rng, (320,), K)
+    assert torch.equal(moe.mx4_dequantize(moved(w)), moe.mx4_dequantize(w))
+    for name, y, left, right in (("rows", moe.mx4_matmul(x, moved(w)), xv, wv.T),
+                                 ("four bits", moe.mx4_matmul(moved(q), moved(w)), qv, wv.T),
+                                 ("gradient", moe.mx4_matmul_backward(d, moved(v)), dv, vv)):
+        check(f"{name} T={T} at {at}", y, left @ right, np.abs(left) @ np.abs(right), left.shape[1])
+
+
 def test_results_repeat_and_leave_the_rest_alone():
     torch = torch_cuda()
     import bit_quantized_moe_topk_amd as moe

@@ -14,6 +14,8 @@ inline unsigned size_of(int32_t t) { return t == MOE_BF16 ? 2u : 4u; }
 // Limits of the launches: rows and columns of a matrix, rows of a product.
 constexpr int32_t kMaxDim = 1 << 19;
 constexpr int32_t kMaxRows = 1 << 22;
+// Assignments of a balance loss: row numbers and ids, and a launch's strides past them, fit 32 bits.
+constexpr long long kMaxIds = 1LL << 30;
 
 // Checks that all products share. dtype: of the rows that come in (n_in values
 // each), out: of those that go out.
@@ -165,7 +167,7 @@ int moe_mx4_experts_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, 
 }
 
 size_t moe_balance_loss_workspace_size(int32_t T, int32_t k, int32_t E) {
-  if (T < 0 || k < 1 || E < 1 || E > MOE_MAX_E) return 0;
+  if (T < 0 || k < 1 || E < 1 || E > MOE_MAX_E || (long long)T * k > kMaxIds) return 0;
   return moe::balance_workspace_bytes(T, k, E);
 }
 
@@ -173,7 +175,7 @@ int moe_balance_loss(const void* logits, int32_t dtype, int64_t ld, int32_t T, i
                      const int32_t* idx, const uint8_t* mask, float* losses, int32_t* counts, int32_t* kept, void* ws,
                      size_t ws_bytes, void* stream) {
   if (T < 0 || E < 1 || k < 1 || ld < E || !float_type(dtype)) return MOE_ERR_INVALID_ARG;
-  if (E > MOE_MAX_E || (long long)T * k > 0x7FFFFFFFLL || ld > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  if (E > MOE_MAX_E || (long long)T * k > kMaxIds || ld > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
   if (!losses || !counts || !kept || !aligned(losses, 4) || !aligned(counts, 4) || !aligned(kept, 4))
     return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !idx || !aligned(logits, size_of(dtype)) || !aligned(idx, 4))) return MOE_ERR_INVALID_ARG;
@@ -186,7 +188,7 @@ int moe_balance_loss_backward(const void* logits, int32_t dtype, int64_t ld, int
                               const uint8_t* mask, const int32_t* counts, const int32_t* kept, const float* d_losses,
                               void* dlogits, void* stream) {
   if (T < 0 || E < 1 || k < 1 || ld < E || !float_type(dtype)) return MOE_ERR_INVALID_ARG;
-  if (E > MOE_MAX_E || (long long)T * k > 0x7FFFFFFFLL || ld > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
+  if (E > MOE_MAX_E || (long long)T * k > kMaxIds || ld > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!logits || !counts || !kept || !d_losses || !dlogits || !aligned(logits, size_of(dtype)) ||
       !aligned(dlogits, size_of(dtype)) || !aligned(counts, 4) || !aligned(kept, 4) || !aligned(d_losses, 4))

@@ -445,7 +445,7 @@ size_t moe_balance_loss_workspace_size(int32_t T, int32_t k, int32_t E);
  * logits: [T][E], MOE_F32 or MOE_BF16, ld elements from row to row (>= E); idx:
  * [T][k] int32 (moe_route_topk); counts: [E] int32; kept: [1] int32; losses: [2]
  * float32. Sums are float32 in a fixed order: reproducible run to run.
- * Requires 1 <= E <= MOE_MAX_E, k >= 1; T == 0 writes n = 0 and zeros.
+ * Requires 1 <= E <= MOE_MAX_E, k >= 1, T*k <= 2^30; T == 0 writes n = 0 and zeros.
  * ws: at least moe_balance_loss_workspace_size bytes, any content; calls that
  * overlap in time must not share it. */
 int moe_balance_loss(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E, int32_t k,

@@ -139,6 +139,15 @@ def test_balance_refusals():
     assert b(None, moe.F32, 512, 0, 512, 10, None, None, None, None, None, None) == OK
 
 
+def test_balance_sizes_past_the_launches():
+    f, b, n = moe.lib().moe_balance_loss, moe.lib().moe_balance_loss_backward, moe.lib().moe_balance_loss_workspace_size
+    for T, k in ((2 ** 31 - 1, 1), (2 ** 30 + 1, 1), (2 ** 29, 3), (2, 2 ** 30), (2 ** 31 - 1, 2 ** 31 - 1)):
+        assert n(T, k, 1) == 0
+        assert f(FAKE, moe.BF16, 1, T, 1, k, FAKE, None, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == UNS
+        assert b(FAKE, moe.BF16, 1, T, 1, k, None, FAKE, FAKE, FAKE, FAKE, None) == UNS
+    assert n(2 ** 30, 1, 1) > 0
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 64)
     codes, scales = torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(16, 2, dtype=torch.uint8)

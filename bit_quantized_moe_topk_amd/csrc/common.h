@@ -189,8 +189,8 @@ void launch_mx4_zero(uint32_t* counter, hipStream_t s);
 hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s);
 bool mx4_tiles4_can(const Mx4Args& a);
 hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s);
-hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, int T, int k, int has_shared, int A,
-                                 int K, void* y, int ydtype, hipStream_t s);
+hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, const int32_t* offsets, int E_tot, int T,
+                                 int k, int has_shared, int A, int K, void* y, int ydtype, hipStream_t s);
 // Balance loss and z loss of a router, and their gradient (balance.hip).
 size_t balance_workspace_bytes(int T, int k, int E);
 hipError_t launch_balance(const void* logits, int dtype, long long ld, int T, int E, int k, const int32_t* idx,

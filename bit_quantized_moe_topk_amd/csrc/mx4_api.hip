@@ -162,7 +162,8 @@ int moe_mx4_experts_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, 
   a.offsets = offsets;
   hipError_t e = moe::launch_mx4_gradient(a, s);
   if (e == hipSuccess && gather)
-    e = moe::launch_mx4_sum_tokens(static_cast<const float*>(part), slot_of, T, k, has_shared, A, K, dx, dxdtype, s);
+    e = moe::launch_mx4_sum_tokens(static_cast<const float*>(part), slot_of, offsets, a.E_tot, T, k, has_shared, A, K,
+                                   dx, dxdtype, s);
   return status_of(e);
 }
 

@@ -231,12 +231,14 @@ __global__ __launch_bounds__(256) void rows_gradient(Mx4Args a, bool vec) {
 }
 
 // dx[t] = the sum of a token's rows of part, in the order of its assignments
-// (the shared expert's last); float32 sums, one rounding. A lane adds up four
-// columns (where K is no multiple of four, one), four rows on their way at once.
+// (the shared expert's last); float32 sums, one rounding. Rows of part that are in
+// no group were not written and add nothing. A lane adds up four columns (where K
+// is no multiple of four, one), four rows on their way at once.
 template <bool BF, int V>
 __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part, const int32_t* __restrict__ slot_of,
-                                                  int T, int k, int has_shared, int A, int K, void* __restrict__ y) {
-  const int t = blockIdx.x, n = k + has_shared;
+                                                  const int32_t* __restrict__ offsets, int E_tot, int T, int k,
+                                                  int has_shared, int A, int K, void* __restrict__ y) {
+  const int t = blockIdx.x, n = k + has_shared, lo = max(offsets[0], 0), hi = min(offsets[E_tot], A);
   for (int c = V * (blockIdx.y * 256 + threadIdx.x); c < K; c += V * gridDim.y * 256) {
     float v[V] = {};
     for (int j0 = 0; j0 < n; j0 += 4) {
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part
         const int s = j < n ? slot_of[j < k ? (size_t)t * k + j : (size_t)T * k + t] : -1;
 #pragma unroll
         for (int i = 0; i < V; ++i) p[z][i] = 0.f;
-        if ((unsigned)s < (unsigned)A) {
+        if (s >= lo && s < hi) {
           if constexpr (V == 4) {
             const float4 q = *reinterpret_cast<const float4*>(part + (size_t)s * K + c);
             p[z][0] = q.x; p[z][1] = q.y; p[z][2] = q.z; p[z][3] = q.w;
@@ -330,12 +332,13 @@ hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, int T, int k, int has_shared, int A,
-                                 int K, void* y, int ydtype, hipStream_t s) {
+hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, const int32_t* offsets, int E_tot, int T,
+                                 int k, int has_shared, int A, int K, void* y, int ydtype, hipStream_t s) {
   const bool four = K % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
   const dim3 g(T, four ? (K + 1023) / 1024 : (K + 255) / 256);
 #define SUM_TOKENS(BF, V) \
-  MOE_LAUNCH("mx4_sum_tokens", s, (sum_tokens<BF, V>), g, dim3(256), 0, s, part, slot_of, T, k, has_shared, A, K, y)
+  MOE_LAUNCH("mx4_sum_tokens", s, (sum_tokens<BF, V>), g, dim3(256), 0, s, part, slot_of, offsets, E_tot, T, k, \
+             has_shared, A, K, y)
   if (ydtype == 1) {
     if (four) SUM_TOKENS(true, 4);
     else SUM_TOKENS(true, 1);

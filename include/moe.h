@@ -416,7 +416,8 @@ size_t moe_mx4_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int3
  *   gather == 1: dx [T][K]; the sum over the token's assignments, in the order
  *                j = 0 .. k-1, then the shared expert's, kept in float32 in ws
  *                ([A][K]) and rounded once. slot_of: [A] as moe_group writes it
- *                (else it may be NULL); values outside [0, A) add nothing.
+ *                (else it may be NULL); values outside [0, A), and rows in no
+ *                group, add nothing.
  * ws: at least ..._workspace_size bytes (any content, 16-byte aligned). */
 int moe_mx4_experts_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t T, int32_t k,
                                     int32_t E, int32_t has_shared, int32_t gather,

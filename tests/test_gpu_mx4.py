@@ -442,6 +442,33 @@ def test_rows_of_no_group_stay_and_bad_ids_stay_in_bounds():
     check("a cut offset", moe.mx4_experts_matmul(x, w, g), ref, size, K)
 
 
+@pytest.mark.parametrize("K", [64, 66])
+def test_gradient_of_tokens_whose_rows_are_in_no_group(K):
+    """A grouping that leaves rows out at both ends: they add nothing to their tokens, whatever the workspace holds."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(K)
+    E, N, T, k = 4, 32, 12, 3
+    A = T * k
+    w, wv = random_matrix(rng, (E, N), K)
+    off = np.array([3, 3, 10, 22, 29, 29], np.int32)
+    perm = rng.permutation(A).astype(np.int32)
+    slot = np.empty(A, np.int32)
+    slot[perm] = np.arange(A)
+    g = moe.Grouping(torch.zeros(E, dtype=torch.int32, device="cuda"), *(torch.from_numpy(v).cuda() for v in (off, perm, slot)))
+    d, dv = random_rows(rng, A, N, "bf16")
+    rows, sizes = np.zeros((A, K)), np.zeros((A, K))
+    for e in range(E):
+        rows[off[e]:off[e + 1]] = dv[off[e]:off[e + 1]] @ wv[e]
+        sizes[off[e]:off[e + 1]] = np.abs(dv[off[e]:off[e + 1]]) @ np.abs(wv[e])
+    ref, size = np.zeros((T, K)), np.zeros((T, K))
+    np.add.at(ref, perm // k, rows)
+    np.add.at(size, perm // k, sizes)
+    n = moe.lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, 0, K, 1)
+    room = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN
+    check("rows in no group", moe.mx4_experts_matmul_backward(d, w, g, tokens=T, workspace=room), ref, size, N + k)
+
+
 def test_experts_refusals():
     torch = torch_cuda()
     import bit_quantized_moe_topk_amd as moe

@@ -490,6 +490,7 @@ def layer_static(logits: torch.Tensor, x: torch.Tensor, ex: "Experts", k: int, m
 # ---- microscaled 4-bit operands ---------------------------------------------------
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
+_MOST = 2 ** 31 - 1  # sizes that the library's calls can be told
 
 
 # The handle of a device's current stream (the first form builds no Stream object: small products
@@ -522,6 +523,8 @@ def _rows(name: str, t: torch.Tensor, n: int | None = None):
     if len(shape) != 2 or (n is not None and shape[1] != n):
         raise ValueError(f"{name} must be [rows, {'n' if n is None else n}]: got {tuple(shape)}")
     R, m = shape
+    if R > _MOST or m > _MOST:
+        raise ValueError(f"{name} is too large: {tuple(shape)}")
     ld, inner = t.stride()
     if R <= 1:
         ld = m
@@ -562,6 +565,8 @@ class Mx4:
             raise ValueError(f"codes {tuple(c)} and scales {tuple(s)} do not hold rows of {K}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
+        if K > _MOST or s[:-1].numel() > _MOST:
+            raise ValueError(f"too many rows or values: {tuple(s[:-1])} rows of {K}")
         self.codes, self.scales, self.K = codes, scales, K
 
     @classmethod

@@ -418,7 +418,8 @@ size_t moe_mx4_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int3
  *                ([A][K]) and rounded once. slot_of: [A] as moe_group writes it
  *                (else it may be NULL); values outside [0, A), and rows in no
  *                group, add nothing.
- * ws: at least ..._workspace_size bytes (any content, 16-byte aligned). */
+ * ws: at least ..._workspace_size bytes (any content, 16-byte aligned); calls
+ * that overlap in time must not share it. */
 int moe_mx4_experts_matmul_backward(const void *dy, int32_t dtype, int64_t ldd, int32_t T, int32_t k,
                                     int32_t E, int32_t has_shared, int32_t gather,
                                     const int32_t *offsets, const int32_t *slot_of,

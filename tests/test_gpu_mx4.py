@@ -448,8 +448,8 @@ def test_gradient_of_tokens_whose_rows_are_in_no_group(K):
     torch = torch_cuda()
     import bit_quantized_moe_topk_amd as moe
     rng = np.random.default_rng(K)
-    E, N, T, k = 4, 32, 12, 3
-    A = T * k
+    E, N, T, k = 4, 32, 12, 2  # the last of the four is the shared expert
+    A = T * (k + 1)
     w, wv = random_matrix(rng, (E, N), K)
     off = np.array([3, 3, 10, 22, 29, 29], np.int32)
     perm = rng.permutation(A).astype(np.int32)
@@ -462,11 +462,11 @@ def test_gradient_of_tokens_whose_rows_are_in_no_group(K):
         rows[off[e]:off[e + 1]] = dv[off[e]:off[e + 1]] @ wv[e]
         sizes[off[e]:off[e + 1]] = np.abs(dv[off[e]:off[e + 1]]) @ np.abs(wv[e])
     ref, size = np.zeros((T, K)), np.zeros((T, K))
-    np.add.at(ref, perm // k, rows)
-    np.add.at(size, perm // k, sizes)
-    n = moe.lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, 0, K, 1)
+    np.add.at(ref, mx4_ref.token_rows(perm, T, k), rows)
+    np.add.at(size, mx4_ref.token_rows(perm, T, k), sizes)
+    n = moe.lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, 1, K, 1)
     room = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN
-    check("rows in no group", moe.mx4_experts_matmul_backward(d, w, g, tokens=T, workspace=room), ref, size, N + k)
+    check("rows in no group", moe.mx4_experts_matmul_backward(d, w, g, tokens=T, workspace=room), ref, size, N + k + 1)
 
 
 def test_experts_refusals():
@@ -498,6 +498,19 @@ def test_experts_refusals():
         moe.mx4_experts_matmul_backward(torch.zeros(18, 16, device="cuda"), w, g, tokens=6,
                                         workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == moe.ERR_WORKSPACE
+
+
+def test_sizes_past_the_calls_are_refused():
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    tall = torch.empty((2 ** 31 + 3, 1), dtype=torch.bfloat16, device="cuda")
+    w = moe.Mx4(torch.zeros((4, 16), dtype=torch.uint8, device="cuda"), torch.zeros((4, 1), dtype=torch.uint8, device="cuda"), 1)
+    for f in (lambda: moe.mx4_quantize(tall), lambda: moe.mx4_quantize(tall.view(1, -1)), lambda: moe.mx4_matmul(tall, w),
+              lambda: moe.mx4_quantize(tall.view(2 ** 31 + 3, 1, 1)),
+              lambda: moe.balance_loss(tall, torch.zeros((2 ** 31 + 3, 0), dtype=torch.int32, device="cuda")),
+              lambda: moe.Mx4(tall.view(torch.uint8)[:, :1].contiguous().expand(-1, 16), tall.view(torch.uint8)[:, :1].contiguous(), 32)):
+        with pytest.raises(ValueError):
+            f()
 
 
 def test_offsets_past_32_bits():

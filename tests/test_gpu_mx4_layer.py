@@ -137,6 +137,45 @@ def test_two_graphs_and_a_stream_of_its_own():
             assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_graphs_of_many_rows_take_turns_with_one_workspace():
+    """More tiles than CUs: two graphs and an eager call use one workspace, one after the other, whatever it holds."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    T, k, E, N, K = 1200, 3, 200, 640, 512
+    w = moe.mx4_quantize(torch.randn((E + 1, N, K), generator=gen, device="cuda"))
+    idx, _ = moe.route_topk(torch.randn((T, E), generator=gen, device="cuda"), k)
+    grp = moe.group(idx, E, True)
+    A = T * (k + 1)
+    room = torch.empty(moe.lib().moe_mx4_experts_matmul_backward_workspace_size(T, k, 1, K, 1), dtype=torch.uint8, device="cuda")
+
+    def step(x, dy):
+        y = moe.mx4_experts_matmul(x, w, grp, tokens=T, workspace=room)
+        y4 = moe.mx4_experts_matmul(moe.mx4_quantize(x), w, grp, tokens=T, workspace=room)
+        return y, y4, moe.mx4_experts_matmul_backward(dy, w, grp, tokens=T, workspace=room)
+
+    data = [(torch.randn((T, K), generator=gen, device="cuda").bfloat16(),
+             torch.randn((A, N), generator=gen, device="cuda").bfloat16()) for _ in range(3)]
+    alone = [[t.clone() for t in step(*d)] for d in data]
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for d in data[:2]:
+        side.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+            outs.append(step(*d))
+        graphs.append(g)
+    for rep in range(3):
+        for g, out, want in zip(graphs, outs, alone):
+            room.random_(0, 256)
+            for t in out:
+                t.zero_()
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip(out, want)), rep
+        assert all(torch.equal(a, b) for a, b in zip(step(*data[2]), alone[2]))
+        torch.cuda.synchronize()
+
+
 def test_four_bit_rows_of_a_decode_window():
     """Quantised activations through the grouped product: the same rows as values through it give the same sums."""
     torch = torch_cuda()

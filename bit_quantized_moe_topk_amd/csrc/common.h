@@ -187,6 +187,7 @@ hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s);
 hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);
 void launch_mx4_zero(uint32_t* counter, hipStream_t s);
 hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s);
+hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s);
 bool mx4_tiles4_can(const Mx4Args& a);
 hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s);
 hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, const int32_t* offsets, int E_tot, int T,

@@ -278,20 +278,46 @@ __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part
   }
 }
 
-// Whether the tile kernels take a product. With groups they read each matrix
-// once and need no workgroup for each row: from 32 rows on (4 tokens x 11
-// experts, [1024, 2048]: 14.8 us against 17.7; 16 tokens 31 against 40), float32
-// rows from 96 on (44 rows: 47 against 26; 176: 48 against 60), gradients
-// always (11 rows: 19 against 26). One matrix: once the 16-row units fill the
-// chip a few times over (512 rows, [1024, 2048]: 15 us against 23; float32 rows
-// at 2,048: 89 against 165; gradients: at 2,048 rows 33 against 42, float32
-// not yet: 95 against 66).
-bool tiles_pay(const Mx4Args& a, bool gradient) {
-  const bool f32 = a.xdtype == 0;
-  if (a.offsets) return gradient || a.A >= (f32 ? 96 : 32);
+// Which kernels take a product of these rows.
+//
+// kFewRows (a workgroup for 16 rows and a strip of the matrix, all of them in
+// one launch) is the quickest to begin: up to 32 rows in groups, and for one
+// matrix until the 16-row units fill the chip a few times over (512 rows,
+// [1024, 2048]: tiles 15 us against 23).
+// kFew (the same 16 rows, from one list of all groups' tiles, the matrix read
+// ahead) reads each matrix once where groups hold a handful of rows. Float32
+// rows, whose parts it makes once for all waves: up to 80 rows a group (64
+// tokens x 11, 512 experts, [2048, 512]: 38 us against the tiles' 97; 4,096
+// tokens: 416 against 500; 16 experts, 384 rows a group, [1024, 2048]: 118
+// against 106), and for one matrix from half a tile for every CU up to four
+// (1,024 rows, [1024, 2048]: 24 us against kFewRows' 51; 256 rows: 22 against
+// 16; 8,192 rows: 134 against the tiles' 106). bf16 rows: up to 12 a group (256
+// tokens, [2048, 512]: 62 against 77; 1,024 tokens: 124 against 110), with more
+// than 1,024 columns up to 3 (32 tokens, [1024, 2048]: 54 against 64; 256
+// tokens: 136 against 121), and there only with four strips for every CU, as
+// one wave goes through all columns (4 tokens: 18 against 15).
+// kTiles: the rest.
+enum Kernels { kFewRows, kFew, kTiles };
+
+Kernels forward_kernels(const Mx4Args& a) {
+  const long long cus = device_cus(), units = (a.A + kRows - 1) / kRows, strips = (a.N + 255) / 256;
+  if (!a.offsets) {
+    if (a.xdtype != 0) return units * ((a.N + 31) / 32) > 4 * cus ? kTiles : kFewRows;
+    return 2 * units * strips < cus ? kFewRows : units * strips <= 4 * cus ? kFew : kTiles;
+  }
+  if (a.A < 32) return kFewRows;
+  if (a.xdtype == kMx4) return kTiles;
+  if (a.xdtype == 0) return a.A <= 80LL * a.E_tot ? kFew : kTiles;
+  const bool deep = a.K > 1024;
+  const long long groups = a.A < a.E_tot ? a.A : a.E_tot;
+  return a.A <= (deep ? 3LL : 12LL) * a.E_tot && 2 * groups * strips >= (deep ? 4 : 1) * cus ? kFew : kTiles;
+}
+
+// Gradients: tiles with groups always (11 rows: 19 us against 26), for one matrix at 2,048 rows
+// (33 us against 42), float32 not yet (95 against 66).
+bool gradient_tiles_pay(const Mx4Args& a) {
   const long long units = (a.A + kRows - 1) / kRows;
-  if (gradient) return units * ((a.K + kCols - 1) / kCols) > (f32 ? 2560 : 1280);
-  return units * ((a.N + 31) / 32) > (f32 ? 3072 : 1024);
+  return a.offsets || units * ((a.K + kCols - 1) / kCols) > (a.xdtype == 0 ? 10 : 5) * device_cus();
 }
 
 __global__ __launch_bounds__(256) void zero_counters(uint32_t* p) { p[threadIdx.x] = 0u; }
@@ -303,7 +329,9 @@ void launch_mx4_zero(uint32_t* counter, hipStream_t s) {
 }
 
 hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
-  if (tiles_pay(a, false)) {
+  const Kernels take = forward_kernels(a);
+  if (take == kFew) return launch_mx4_few(a, s);
+  if (take == kTiles) {
     if (a.xdtype != kMx4) return launch_mx4_tiles(a, s);
     if (mx4_tiles4_can(a)) return launch_mx4_tiles4(a, s);
   }
@@ -324,7 +352,7 @@ hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
 }
 
 hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
-  if (tiles_pay(a, true)) return launch_mx4_grad_tiles(a, s);
+  if (gradient_tiles_pay(a)) return launch_mx4_grad_tiles(a, s);
   const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.K + kCols - 1) / kCols);
   const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
   if (a.xdtype == 1) MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<1>, g, dim3(256), 0, s, a, vec);

@@ -356,6 +356,21 @@ def test_results_repeat_and_leave_the_rest_alone():
     assert moe.mx4_matmul(x[:0], w).shape == (0, N) and moe.mx4_matmul_backward(d[:0], w).shape == (0, K)
 
 
+@pytest.mark.parametrize("T,N,K", [(260, 2048, 96), (250, 2047, 260), (1030, 520, 1000), (600, 1030, 33), (2100, 300, 256)])
+def test_matmul_float32_of_some_hundred_rows(T, N, K):
+    """Sixteen rows a tile: columns in no whole block or stage, rows that end inside a tile, odd strides, ends of strips."""
+    torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(T + N + K)
+    w, wv = random_matrix(rng, (N,), K)
+    for strided in (False, True):
+        x, xv = random_rows(rng, T, K, "f32", strided)
+        x = x if not strided else x[:, :K]
+        ref, size = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+        for dt in types().values():
+            check(f"f32 {T}x{N}x{K} strided={strided} -> {dt}", moe.mx4_matmul(x, w, dtype=dt), ref, size, 3 * K)
+
+
 # ---- experts --------------------------------------------------------------------------
 
 GROUPS = [  # T, k, E, shared, N, K, skew, experts that get nothing
@@ -364,7 +379,10 @@ GROUPS = [  # T, k, E, shared, N, K, skew, experts that get nothing
     (300, 4, 16, False, 130, 288, 0.5, 4), (1500, 2, 6, True, 64, 128, 2, 2),
     # more tiles than CUs, taken from the queues; long and short rows; a crowded group among empty ones
     (1200, 3, 400, True, 600, 512, 0.3, 50), (1100, 2, 300, True, 640, 384, 0, 0), (900, 6, 2047, True, 128, 256, 0.5, 900),
-    (700, 3, 300, True, 576, 1024, 3, 0)]
+    (700, 3, 300, True, 576, 1024, 3, 0),
+    # groups of a few rows, in more tiles than run at once; columns and matrix rows in no whole stage or strip
+    (90, 4, 500, True, 1030, 200, 0.5, 100), (64, 8, 120, False, 520, 1100, 0, 0), (40, 10, 512, True, 2048, 72, 1, 0),
+    (300, 2, 64, True, 2050, 129, 2, 10)]
 
 
 @pytest.mark.parametrize("T,k,E,shared,N,K,skew,quiet", GROUPS)

@@ -82,14 +82,16 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
   int ls = 0, lb = 0;
   bool crossed = false;  // it is in the next item
   bool rows = false;  // whether this wave's last load() brought rows of dy
-  // the next stage, of whatever tile it is; false: there is none
+  int held = 0;       // stages loaded and not used yet
+  // the next stage, of whatever tile it is, if there is one
   auto load = [&]() __attribute__((always_inline)) {
     if (ls == S) {
-      if (crossed || next >= items) return false;
+      if (crossed || next >= items) return;
       crossed = true;
       lt = tile_of(tiles, a, next, items, strips, strip);
       ls = 0;
     }
+    ++held;
     const int s = ls++, b0 = lt.n0 / 32;
     const char* wbase = reinterpret_cast<const char*>(a.wc) + (size_t)lt.e * a.N * nb * 16;
     const uint8_t* sbase = a.ws + (size_t)lt.e * a.N * nb;
@@ -142,12 +144,13 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
         B.s[at] = s * kGN + n < a.N ? sbase[blk] : 0;
       }
     }
-    return true;
   };
-  bool more = load();
-  if (STREAM) more = load();
-  auto done = [&]() __attribute__((always_inline)) {  // all but the last load() have landed
-    if (!STREAM || !more) step_done();
+  load();
+  if (STREAM) load();
+  // The next stage has landed; a load() beyond it may be in flight (there is none where a tile is one stage and the
+  // item after the next is not known yet).
+  auto done = [&]() __attribute__((always_inline)) {
+    if (!STREAM || held < 2) step_done();
     else if (rows) step_done<kDL + kWL + 1>();
     else step_done<kWL + 1>();
   };
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
       constexpr int L = decltype(LL)::value;
       constexpr bool kShared = decltype(SH)::value;
       for (int s = 0; s < S; ++s) {
-        more = load();
+        load();
         {
           const GradBuf<P, WK>& B = buf[cb];
 #pragma unroll
@@ -197,6 +200,7 @@ __global__ __launch_bounds__(128 * WK, P == 1 ? 2 : 1) void tiles_gradient(Mx4Ar
               }
           }
         }
+        --held;
         done();
         cb = cb + 1 == kBufs ? 0 : cb + 1;
       }

@@ -189,7 +189,8 @@ def test_matmul_many_rows(T, N, K, kind):
         check(f"{kind} {T}x{N}x{K} -> f32", moe.mx4_matmul(x, w, dtype=torch.float32), ref, size, K)
 
 
-MANY_BACK = [(1300, 192, 2176), (1301, 64, 2176), (1300, 200, 2176), (1300, 192, 2100), (2600, 70, 2100), (33000, 128, 512)]
+MANY_BACK = [(1300, 192, 2176), (1301, 64, 2176), (1300, 200, 2176), (1300, 192, 2100), (2600, 70, 2100), (33000, 128, 512),
+             (40000, 64, 2176), (40100, 64, 1100), (40000, 60, 1000)]
 
 
 @pytest.mark.parametrize("T,N,K", MANY_BACK)

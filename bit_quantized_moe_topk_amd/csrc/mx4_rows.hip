@@ -168,42 +168,72 @@ __global__ __launch_bounds__(256) void rows_forward(Mx4Args a, bool vec) {
 // rows' pairs are then regrouped along n, so that eight conversions' worth of
 // registers give the operands of eight 16x16x32 products, product c covering
 // columns k0 + 8 r + c. No transposed copy of the matrix is needed.
+// The next step's are on their way while one is used: every load is issued in
+// any case, within the matrix and the rows, and what lies past N counts as zeros
+// (a way past the loads would have the products wait for them).
 template <int DT>
-__global__ __launch_bounds__(256) void rows_gradient(Mx4Args a, bool vec) {
+struct GradRegs {
+  uint32_t w[8], s[8];
+  uint4 d[DT == 1 ? 1 : 2];
+};
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void rows_gradient(Mx4Args a) {
   __shared__ float part[4][kRows * kCols];
   const Unit u = unit_of(a);
   if (u.M <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
   const int nb = mx4_blocks(a.K), k0 = blockIdx.y * kCols;
-  const int kc = k0 + 8 * r;
-  const bool inside = kc < 32 * nb;
-  const size_t row0 = (size_t)u.e * a.N;
-  const int xr = r < u.M ? mx4_row(a, u.s0 + r) : -1;
+  const int piece = min(k0 / 8 + r, 4 * nb - 1);  // dword of codes in a matrix row (past it: not stored)
+  const uint32_t* wc = reinterpret_cast<const uint32_t*>(a.wc) + (size_t)u.e * a.N * nb * 4 + piece;
+  const uint8_t* ws = a.ws + (size_t)u.e * a.N * nb + piece / 4;
+  const char* row = static_cast<const char*>(a.x) + (size_t)(u.s0 + min(r, u.M - 1)) * a.ldx * (DT == 1 ? 2 : 4);
+  auto load = [&](int n0, GradRegs<DT>& v) __attribute__((always_inline)) {
+    const int n = n0 + 8 * g;
+    if constexpr (VEC) {
+      const uint4* p = reinterpret_cast<const uint4*>(row + (size_t)min(n, a.N - 8) * (DT == 1 ? 2 : 4));
+      v.d[0] = p[0];
+      if constexpr (DT != 1) v.d[1] = p[1];
+    } else if (n < a.N) {
+      if constexpr (DT == 1) {
+        v.d[0] = load8_bf16(reinterpret_cast<const uint16_t*>(row), n, a.N, false);
+      } else {
+        float f[8];
+        load8_f32(reinterpret_cast<const float*>(row), n, a.N, false, f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          v.d[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                              __float_as_uint(f[4 * i + 3]));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const size_t at = (size_t)min(n + j, a.N - 1) * nb;
+      v.w[j] = wc[4 * at];
+      v.s[j] = ws[at];
+    }
+  };
   floatx4_t acc[8] = {};
-  for (int n0 = 32 * wave; n0 < a.N; n0 += 128) {
+  auto step = [&](int n0, const GradRegs<DT>& v, GradRegs<DT>& next) __attribute__((always_inline)) {
+    load(n0 + 128, next);
+    __builtin_amdgcn_sched_barrier(0);
+    const int n = n0 + 8 * g;
     uint32_t p[8][4];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int n = n0 + 8 * g + j;
-      uint32_t w = 0, sw = 0;
-      if (inside && n < a.N) {
-        w = reinterpret_cast<const uint32_t*>(a.wc)[(row0 + n) * nb * 4 + kc / 8];
-        sw = a.ws[(row0 + n) * nb + kc / 32];
-      }
-      const float sc = mx4_scale(sw);
-      p[j][0] = mx4_pair<0>(w, sc);
-      p[j][1] = mx4_pair<1>(w, sc);
-      p[j][2] = mx4_pair<2>(w, sc);
-      p[j][3] = mx4_pair<3>(w, sc);
+      const float sc = mx4_scale(n + j < a.N ? v.s[j] : 0u);
+      p[j][0] = mx4_pair<0>(v.w[j], sc);
+      p[j][1] = mx4_pair<1>(v.w[j], sc);
+      p[j][2] = mx4_pair<2>(v.w[j], sc);
+      p[j][3] = mx4_pair<3>(v.w[j], sc);
     }
-    const int n = n0 + 8 * g;
-    uint4 d[3];
+    uint4 d[3], x[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = n < a.N ? v.d[DT == 1 ? 0 : i] : make_uint4(0, 0, 0, 0);
     if constexpr (DT == 1) {
-      d[0] = make_uint4(0, 0, 0, 0);
-      if (xr >= 0 && n < a.N) d[0] = load8_bf16(static_cast<const uint16_t*>(a.x) + xr * a.ldx, n, a.N, vec);
+      d[0] = x[0];
     } else {
-      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (xr >= 0 && n < a.N) load8_f32(static_cast<const float*>(a.x) + xr * a.ldx, n, a.N, vec, f);
+      const float f[8] = {__uint_as_float(x[0].x), __uint_as_float(x[0].y), __uint_as_float(x[0].z), __uint_as_float(x[0].w),
+                          __uint_as_float(x[1].x), __uint_as_float(x[1].y), __uint_as_float(x[1].z), __uint_as_float(x[1].w)};
       split3x8(f, d[0], d[1], d[2]);
     }
 #pragma unroll
@@ -216,6 +246,12 @@ __global__ __launch_bounds__(256) void rows_gradient(Mx4Args a, bool vec) {
       for (int q = DT == 1 ? 0 : 2; q >= 0; --q)
         acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, d[q]), wf, acc[c], 0, 0, 0);
     }
+  };
+  GradRegs<DT> even, odd;
+  load(32 * wave, even);
+  for (int n0 = 32 * wave; n0 < a.N; n0 += 256) {
+    step(n0, even, odd);
+    if (n0 + 128 < a.N) step(n0 + 128, odd, even);
   }
   // acc[c][i]: row 4 g + i, column k0 + 8 r + c
 #pragma unroll
@@ -313,11 +349,17 @@ Kernels forward_kernels(const Mx4Args& a) {
   return a.A <= (deep ? 3LL : 12LL) * a.E_tot && 2 * groups * strips >= (deep ? 4 : 1) * cus ? kFew : kTiles;
 }
 
-// Gradients: tiles with groups always (11 rows: 19 us against 26), for one matrix at 2,048 rows
-// (33 us against 42), float32 not yet (95 against 66).
+// Gradients: tiles where groups hold more than a few rows, bf16 rows from 4 a group on (64 tokens x
+// 11, 512 experts, [1000, 2048]: tiles 155 us against 100 in 16-row units; 256 tokens, [2048, 512]: 107
+// against 117; 192 rows of 17 experts: 47 against 29), float32 from 12 (256 tokens x 11, 512 experts,
+// [2048, 512]: 445 against 170; 45 rows a group, [1000, 2048]: 100 against 124). One matrix: from about
+// eight 16-row units for every CU on (bf16 [1024, 2048], 2,048 rows: 35 us against 33, 4,096: 38 against
+// 60; float32 4,096 rows: 96 against 98).
 bool gradient_tiles_pay(const Mx4Args& a) {
+  const bool f32 = a.xdtype == 0;
+  if (a.offsets) return a.A > (f32 ? 12LL : 4LL) * a.E_tot && a.A > 256;
   const long long units = (a.A + kRows - 1) / kRows;
-  return a.offsets || units * ((a.K + kCols - 1) / kCols) > (a.xdtype == 0 ? 10 : 5) * device_cus();
+  return units * ((a.K + kCols - 1) / kCols) > (f32 ? 10 : 8) * device_cus();
 }
 
 __global__ __launch_bounds__(256) void zero_counters(uint32_t* p) { p[threadIdx.x] = 0u; }
@@ -354,9 +396,11 @@ hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
 hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s) {
   if (gradient_tiles_pay(a)) return launch_mx4_grad_tiles(a, s);
   const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.K + kCols - 1) / kCols);
-  const bool vec = rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
-  if (a.xdtype == 1) MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<1>, g, dim3(256), 0, s, a, vec);
-  else MOE_LAUNCH("mx4_rows_grad", s, rows_gradient<0>, g, dim3(256), 0, s, a, vec);
+  const bool vec = a.N % 8 == 0 && rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
+  if (a.xdtype == 1 && vec) MOE_LAUNCH("mx4_rows_grad", s, (rows_gradient<1, true>), g, dim3(256), 0, s, a);
+  else if (a.xdtype == 1) MOE_LAUNCH("mx4_rows_grad", s, (rows_gradient<1, false>), g, dim3(256), 0, s, a);
+  else if (vec) MOE_LAUNCH("mx4_rows_grad", s, (rows_gradient<0, true>), g, dim3(256), 0, s, a);
+  else MOE_LAUNCH("mx4_rows_grad", s, (rows_gradient<0, false>), g, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -777,9 +777,15 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tens
         raise ValueError(f"idx must be [{T}, k]: got {tuple(idx.shape)}")
     k = idx.shape[1]
     keep = _token_mask(token_mask, T, dev)
-    if out is None:  # parts of one tensor
-        losses, kept, counts = torch.empty(E + 3, dtype=torch.int32, device=dev).split_with_sizes((2, 1, E))
+    need = _bytes("moe_balance_loss_workspace_size", T, k, E)
+    inside = None
+    if out is None:  # parts of one tensor, a small workspace (16-byte aligned, as the tensor is) among them
+        n = (need + 15) // 16 * 4 if workspace is None and need <= 1 << 16 else 0
+        room = torch.empty(n + E + 3, dtype=torch.int32, device=dev)
+        scratch, losses, kept, counts = room.split_with_sizes((n, 2, 1, E))
         out = BalanceLoss(losses.view(torch.float32), counts, kept, k)
+        if n:
+            inside = (room.data_ptr(), 4 * n, room)
     else:
         _need_cuda("out.losses", out.losses, torch.float32)
         _int32("out.counts", out.counts, dev)
@@ -787,7 +793,7 @@ def balance_loss(logits: torch.Tensor, idx: torch.Tensor, token_mask: torch.Tens
         if out.losses.numel() != 2 or out.counts.numel() != E or out.kept.numel() != 1 or out.losses.device != dev:
             raise ValueError("out does not match the logits")
         out.k = k
-    wp, wn, keep_ws = _workspace(workspace, _bytes("moe_balance_loss_workspace_size", T, k, E), dev)
+    wp, wn, keep_ws = inside or _workspace(workspace, need, dev)
     _call("moe_balance_loss", dev, logits.data_ptr(), code, ld, T, E, k, idx.data_ptr(), keep, out.losses.data_ptr(),
           out.counts.data_ptr(), out.kept.data_ptr(), wp, wn)
     return out

@@ -461,6 +461,35 @@ def test_rows_of_no_group_stay_and_bad_ids_stay_in_bounds():
     check("a cut offset", moe.mx4_experts_matmul(x, w, g), ref, size, K)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "mx4"])
+@pytest.mark.parametrize("E,N", [(4, 32), (300, 1000)])
+def test_bad_ids_of_few_rows(E, N, kind):
+    """Ids out of range and rows in no group, for each type and in more tiles than CUs: neighbours are right, the rest stays."""
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    rng = np.random.default_rng(E + N)
+    K, A = 96, 700
+    w, wv = random_matrix(rng, (E, N), K)
+    off = np.minimum(np.sort(rng.integers(0, A - 60, E + 2)), A - 61).astype(np.int32)
+    ids = rng.permutation(A).astype(np.int32)
+    wild = rng.permutation(A)[:40]
+    perm = ids.copy()
+    perm[wild] = rng.choice(np.array([-1, A, 2 ** 31 - 1, -2 ** 31], np.int64), 40).astype(np.int32)
+    g = moe.Grouping(torch.zeros(E + 1, dtype=torch.int32, device="cuda"), torch.from_numpy(off).cuda(),
+                     torch.from_numpy(perm).cuda(), torch.from_numpy(perm).cuda())
+    x, xv = random_rows(rng, A, K, kind)
+    room = torch.full((A, N), 7.0, device="cuda")
+    y = moe.mx4_experts_matmul(x, w, g, tokens=A, dtype=torch.float32, out=room)
+    ref, size = mx4_ref.grouped(xv[ids], wv, off[:E + 1])
+    inside = np.zeros(A, bool)
+    inside[off[0]:off[E]] = True
+    tame = inside.copy()
+    tame[wild] = False
+    at = torch.from_numpy(np.flatnonzero(tame)).cuda()
+    check(f"{kind} among bad ids", y[at], ref[tame], size[tame], K * (3 if kind == "f32" else 1))
+    assert (y[torch.from_numpy(np.flatnonzero(~inside)).cuda()] == 7).all()
+
+
 @pytest.mark.parametrize("K", [64, 66])
 def test_gradient_of_tokens_whose_rows_are_in_no_group(K):
     """A grouping that leaves rows out at both ends: they add nothing to their tokens, whatever the workspace holds."""

@@ -197,13 +197,16 @@ def gpu_hold(ms: float) -> None:
     torch.cuda._sleep(int(ms * 1e-3 * 2.4e9))
 
 
-def kernel_source_hash() -> str:
-    """Digest of the HIP sources (a byte-counter summary is valid only for them)."""
+# Sources (by their names' beginnings) of operators that no leg here runs, and that no kernel here includes.
+OTHER_SOURCES = ("mx4", "balance")
+
+
+def kernel_source_hash(d: str = os.path.join(ROOT, "bit_quantized_moe_topk_amd", "csrc")) -> str:
+    """Digest of the HIP sources of the kernels timed here (a byte-counter summary is valid only for them)."""
     import hashlib
-    d = os.path.join(ROOT, "bit_quantized_moe_topk_amd", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):
-        if f.endswith((".hip", ".h")):
+        if f.endswith((".hip", ".h")) and not f.startswith(OTHER_SOURCES):
             h.update(f.encode())
             h.update(open(os.path.join(d, f), "rb").read())
     return h.hexdigest()[:16]

@@ -16,7 +16,7 @@
 //
 // Sums are float32 in a fixed order (per wave over its tokens, then over the
 // waves in order), counts are integers: results do not vary from run to run.
-#include "common.h"
+#include "balance.h"
 #include "gemv.h"
 #include "topk.h"
 

@@ -176,29 +176,4 @@ XsJob xs_job(int q, int H, const void* x, int xdtype, int T, uint16_t* x16, int3
 hipError_t launch_tile_weights(const Experts& ex, hipStream_t s);
 hipError_t launch_combine(const Experts& ex, const FfnArgs& a, hipStream_t s);
 
-// Microscaled 4-bit rows (mx4_quant.hip) and their products (mx4.h, mx4_rows.hip).
-struct Mx4Args;
-hipError_t launch_mx4_quantize(const void* x, int xdtype, long long ld, int rows, int K, uint8_t* codes,
-                               uint8_t* scales, hipStream_t s);
-hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int K, int ydtype,
-                                 void* y, hipStream_t s);
-hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s);
-hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s);
-hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);
-void launch_mx4_zero(uint32_t* counter, hipStream_t s);
-hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s);
-hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s);
-bool mx4_tiles4_can(const Mx4Args& a);
-hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s);
-hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, const int32_t* offsets, int E_tot, int T,
-                                 int k, int has_shared, int A, int K, void* y, int ydtype, hipStream_t s);
-// Balance loss and z loss of a router, and their gradient (balance.hip).
-size_t balance_workspace_bytes(int T, int k, int E);
-hipError_t launch_balance(const void* logits, int dtype, long long ld, int T, int E, int k, const int32_t* idx,
-                          const uint8_t* keep, float* losses, int32_t* counts, int32_t* kept, void* ws,
-                          hipStream_t s);
-hipError_t launch_balance_gradient(const void* logits, int dtype, long long ld, int T, int E, int k,
-                                   const uint8_t* keep, const int32_t* counts, const int32_t* kept, const float* d,
-                                   void* dx, hipStream_t s);
-
 }  // namespace moe

@@ -150,4 +150,20 @@ inline bool rows_vec(const void* p, long long ld, int size) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16 == 0;
 }
 
+// ---- launchers (each returns hipGetLastError() after enqueueing) ----------
+hipError_t launch_mx4_quantize(const void* x, int xdtype, long long ld, int rows, int K, uint8_t* codes,
+                               uint8_t* scales, hipStream_t s);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int rows, int K, int ydtype,
+                                 void* y, hipStream_t s);
+hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_gradient(const Mx4Args& a, hipStream_t s);
+hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s);
+void launch_mx4_zero(uint32_t* counter, hipStream_t s);
+hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s);
+hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s);
+bool mx4_tiles4_can(const Mx4Args& a);
+hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s);
+hipError_t launch_mx4_sum_tokens(const float* part, const int32_t* slot_of, const int32_t* offsets, int E_tot, int T,
+                                 int k, int has_shared, int A, int K, void* y, int ydtype, hipStream_t s);
+
 }  // namespace moe

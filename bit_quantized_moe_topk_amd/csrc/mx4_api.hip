@@ -1,7 +1,7 @@
 // Host implementation of the microscaled 4-bit calls and the balance loss of
 // include/moe.h: argument checks and dispatch. Nothing here allocates.
 #include "../../include/moe.h"
-#include "common.h"
+#include "balance.h"
 #include "mx4.h"
 
 namespace {

@@ -294,7 +294,7 @@ hipError_t launch_mx4_grad_tiles(Mx4Args a, hipStream_t s) {
   const dim3 g((unsigned)(most < cap ? most : cap));
   if (most <= cap || g.x % kXcds) a.counter = nullptr;
   else if (a.counter) launch_mx4_zero(a.counter, s);
-  if (stream) MOE_LAUNCH("mx4_grad_tiles", s, (tiles_gradient<1, 4, true>), g, dim3(512), 0, s, a, vec);
+  if (stream) MOE_LAUNCH("mx4_grad_stream", s, (tiles_gradient<1, 4, true>), g, dim3(512), 0, s, a, vec);
   else if (a.xdtype == 1) MOE_LAUNCH("mx4_grad_tiles", s, (tiles_gradient<1, 2, false>), g, dim3(256), 0, s, a, vec);
   else MOE_LAUNCH("mx4_grad_tiles", s, (tiles_gradient<3, 2, false>), g, dim3(256), 0, s, a, vec);
   return hipGetLastError();

@@ -392,10 +392,10 @@ hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s) {
   else if (a.counter) launch_mx4_zero(a.counter, s);
   if (!even && a.xdtype == 1) MOE_LAUNCH("mx4_tiles", s, tiles_forward<1>, g, dim3(kThreads), 0, s, a, vec);
   else if (!even) MOE_LAUNCH("mx4_tiles", s, tiles_forward<3>, g, dim3(kThreads), 0, s, a, vec);
-  else if (strip == 512 && wide) MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<8, true>), g, dim3(512), 0, s, a);
-  else if (strip == 512) MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<8, false>), g, dim3(512), 0, s, a);
-  else if (strip == 256) MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<4, false>), g, dim3(512), 0, s, a);
-  else MOE_LAUNCH("mx4_tiles_stream", s, (tiles_stream<2, false>), g, dim3(512), 0, s, a);
+  else if (strip == 512 && wide) MOE_LAUNCH("mx4_stream_512_wide", s, (tiles_stream<8, true>), g, dim3(512), 0, s, a);
+  else if (strip == 512) MOE_LAUNCH("mx4_stream_512", s, (tiles_stream<8, false>), g, dim3(512), 0, s, a);
+  else if (strip == 256) MOE_LAUNCH("mx4_stream_256", s, (tiles_stream<4, false>), g, dim3(512), 0, s, a);
+  else MOE_LAUNCH("mx4_stream_128", s, (tiles_stream<2, false>), g, dim3(512), 0, s, a);
   return hipGetLastError();
 }
 

@@ -193,11 +193,11 @@ hipError_t launch_mx4_tiles4(Mx4Args a, hipStream_t s) {
   if (most <= cap || g.x % kXcds) a.counter = nullptr;
   else if (a.counter) launch_mx4_zero(a.counter, s);
   if (nb % 16 == 0 && at % 16 == 0 && a.E_tot <= kWideGroups)
-    MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<kWide>, g, dim3(kThreads4), 0, s, a);
+    MOE_LAUNCH("mx4_tiles4_wide", s, tiles_mx4<kWide>, g, dim3(kThreads4), 0, s, a);
   else if (nb % 4 == 0 && at % 4 == 0)
-    MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<kQuads>, g, dim3(kThreads4), 0, s, a);
+    MOE_LAUNCH("mx4_tiles4_quads", s, tiles_mx4<kQuads>, g, dim3(kThreads4), 0, s, a);
   else
-    MOE_LAUNCH("mx4_tiles4", s, tiles_mx4<kBytes>, g, dim3(kThreads4), 0, s, a);
+    MOE_LAUNCH("mx4_tiles4_bytes", s, tiles_mx4<kBytes>, g, dim3(kThreads4), 0, s, a);
   return hipGetLastError();
 }
 

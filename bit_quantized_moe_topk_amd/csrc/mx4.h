@@ -109,6 +109,10 @@ __device__ inline int mx4_row(const Mx4Args& a, int s) {
   return (unsigned)t < (unsigned)a.T ? t : -1;
 }
 
+// An offset cut to the rows, and so the first row of group e.
+__device__ inline int cut_offset(const Mx4Args& a, int offset) { return min(max(offset, 0), a.A); }
+__device__ inline int first_row(const Mx4Args& a, int e) { return cut_offset(a, a.offsets[e]); }
+
 // The group of row s: how many of offsets[1 .. E_tot] are at most s (one wave,
 // every lane gets it; 512 offsets on their way at once). E_tot: the row is
 // behind the last group.

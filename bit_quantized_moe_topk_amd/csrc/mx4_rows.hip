@@ -31,9 +31,8 @@ __device__ inline Unit unit_of(const Mx4Args& a) {
   u.e = mx4_group_of(a.offsets, a.E_tot, u.s0);
   u.M = 0;
   if (u.e < a.E_tot) {
-    const int first = u.e ? a.offsets[u.e] : max(a.offsets[0], 0);
-    if (u.s0 >= first && (u.s0 - first) % kRows == 0)
-      u.M = min(kRows, min(a.offsets[u.e + 1], a.A) - u.s0);
+    const int first = first_row(a, u.e);
+    if (u.s0 >= first && (u.s0 - first) % kRows == 0) u.M = min(kRows, first_row(a, u.e + 1) - u.s0);
   }
   return u;
 }

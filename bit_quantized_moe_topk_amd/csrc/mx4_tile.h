@@ -38,8 +38,6 @@ struct TilesScratch {
   int wsum[16];
 };
 
-__device__ inline int first_row(const Mx4Args& a, int e) { return min(max(a.offsets[e], 0), a.A); }
-
 template <int TM = kTM, int CAP>
 __device__ inline int tiles_init(TilesOf<CAP>& t, TilesScratch& w, const Mx4Args& a) {
   if (!a.offsets) return (a.A + TM - 1) / TM;
@@ -51,7 +49,7 @@ __device__ inline int tiles_init(TilesOf<CAP>& t, TilesScratch& w, const Mx4Args
     for (int z = 0; z < kAtOnce; ++z) v[z] = a.offsets[min(e0 + z * nt, a.E_tot)];
 #pragma unroll
     for (int z = 0; z < kAtOnce; ++z)
-      if (e0 + z * nt <= a.E_tot) w.first[e0 + z * nt] = min(max(v[z], 0), a.A);
+      if (e0 + z * nt <= a.E_tot) w.first[e0 + z * nt] = cut_offset(a, v[z]);
   }
   __syncthreads();
   // this thread's groups are neighbours: their tiles, the sum of all before, and the places

@@ -396,10 +396,11 @@ size_t moe_mx4_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_s
  * E_tot is at most MOE_MAX_E + 1, A at most 2^22, N and K at most 2^19.
  * offsets: [E_tot + 1] (moe_group writes one more), perm: [A]; perm may be NULL
  * when gather == 0. Values of perm outside [0, A) are not detected; the kernels
- * stay in bounds and the results of those rows are unspecified; offsets are cut
- * to [0, A]. Types and rounding as moe_mx4_matmul. ws: at least ..._workspace_size
- * bytes (any content, 16-byte aligned); calls that overlap in time must not
- * share it. Results do not depend on which workgroup takes which rows. */
+ * stay in bounds and the results of those rows are unspecified. offsets must not
+ * decrease; each counts as cut to [0, A]. Types and rounding as
+ * moe_mx4_matmul. ws: at least ..._workspace_size bytes (any content, 16-byte
+ * aligned); calls that overlap in time must not share it. Results do not depend
+ * on which workgroup takes which rows. */
 int moe_mx4_experts_matmul(const void *x, const uint8_t *x_scales, int32_t xdtype, int64_t ldx,
                            int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t gather,
                            const int32_t *offsets, const int32_t *perm, const uint8_t *w_codes,

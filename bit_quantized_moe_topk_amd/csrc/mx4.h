@@ -102,12 +102,14 @@ inline long long mx4_row_tiles(const Mx4Args& a) {
   return full > groups ? full : groups;
 }
 
-// x's row that row s of the groups reads; -1: none (an id out of range).
-__device__ inline int mx4_row(const Mx4Args& a, int s) {
-  if (!a.perm) return s;
-  const int t = token_of(a.perm[s], a.T, a.k);
-  return (unsigned)t < (unsigned)a.T ? t : -1;
+// The token of an assignment id, -1 of one outside [0, A) (asked of the id: those from -(k - 1) to -1 divided by k
+// are 0).
+__device__ inline int mx4_token(const Mx4Args& a, int id) {
+  return (unsigned)id < (unsigned)a.A ? token_of(id, a.T, a.k) : -1;
 }
+
+// x's row that row s of the groups reads; -1: none (an id out of range).
+__device__ inline int mx4_row(const Mx4Args& a, int s) { return a.perm ? mx4_token(a, a.perm[s]) : s; }
 
 // An offset cut to the rows, and so the first row of group e.
 __device__ inline int cut_offset(const Mx4Args& a, int offset) { return min(max(offset, 0), a.A); }

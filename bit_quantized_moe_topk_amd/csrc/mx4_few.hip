@@ -83,8 +83,8 @@ __global__ __launch_bounds__(64 * W, 4) void tiles_few(Mx4Args a) {
         wc[j] = reinterpret_cast<const uint4*>(a.wc) + row * nb;
         ws[j] = a.ws + row * nb;
       }
-      const int row = a.perm ? token_of(id, a.T, a.k) : t.s0 + min(m, t.M - 1);
-      none = m >= t.M || (a.perm && (unsigned)row >= (unsigned)a.T);  // past the tile, or an id out of range
+      const int row = a.perm ? mx4_token(a, id) : t.s0 + min(m, t.M - 1);
+      none = m >= t.M || row < 0;  // past the tile, or an id out of range
       xrow = static_cast<const char*>(a.x) + (size_t)(none ? 0 : row) * a.ldx * (P == 1 ? 2 : 4);
       ls = 0;
       ahead += gridDim.x;

@@ -22,6 +22,7 @@ typedef float floatx16_t __attribute__((ext_vector_type(16)));
 typedef int int8v_t __attribute__((ext_vector_type(8)));
 
 constexpr int kMx4 = 4;  // x type code of microscaled rows (MOE_MX4)
+constexpr int kMx4MaxRows = 1 << 22;  // rows of a product
 
 __host__ __device__ inline int mx4_blocks(int K) { return (K + 31) / 32; }
 

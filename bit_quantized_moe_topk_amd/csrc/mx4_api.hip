@@ -13,7 +13,7 @@ inline unsigned size_of(int32_t t) { return t == MOE_BF16 ? 2u : 4u; }
 
 // Limits of the launches: rows and columns of a matrix, rows of a product.
 constexpr int32_t kMaxDim = 1 << 19;
-constexpr int32_t kMaxRows = 1 << 22;
+constexpr int32_t kMaxRows = moe::kMx4MaxRows;
 // Assignments of a balance loss: row numbers and ids, and a launch's strides past them, fit 32 bits.
 constexpr long long kMaxIds = 1LL << 30;
 

@@ -6,7 +6,7 @@
 // become bf16 exactly; float32 rows enter as three exact bf16 parts, so that
 // every product is exact and only the float32 sums round. Bound by the
 // matrix's bytes: each is read once per 16 rows.
-#include "mx4.h"
+#include "mx4_tile.h"
 
 namespace moe {
 namespace {
@@ -342,7 +342,7 @@ Kernels forward_kernels(const Mx4Args& a) {
   }
   if (a.A < 32) return kFewRows;
   if (a.xdtype == kMx4) return kTiles;
-  if (a.xdtype == 0) return a.A <= 80LL * a.E_tot ? kFew : kTiles;
+  if (a.xdtype == 0) return a.A <= (long long)kFewRowsF32 * a.E_tot ? kFew : kTiles;
   const bool deep = a.K > 1024;
   const long long groups = a.A < a.E_tot ? a.A : a.E_tot;
   return a.A <= (deep ? 3LL : 12LL) * a.E_tot && 2 * groups * strips >= (deep ? 4 : 1) * cus ? kFew : kTiles;

@@ -24,12 +24,16 @@ struct TileInfo {
 };
 
 // Tiles of a launch: base[e] = the tiles before group e (of one strip of matrix
-// rows). 16 bits do for 2^22 rows in tiles of up to 128, and one more a group
-// (tiles of 32 are for few rows).
+// rows). 16 bits hold them: 2^22 rows in tiles of 128 make 32,768, and one more
+// a group. Tiles of 16 rows are for groups of up to kFewRowsF32 rows on average.
 template <int CAP>
 struct TilesOf {
   uint16_t base[CAP];
 };
+constexpr int kMaxTiles = 65535;
+constexpr int kFewRowsF32 = 80;  // (what was measured: mx4_rows.hip)
+static_assert(kMx4MaxRows / kTM + MOE_MAX_E_DEV + 1 <= kMaxTiles, "tiles of 128 rows");
+static_assert((MOE_MAX_E_DEV + 1) * (kFewRowsF32 / 16 + 1) <= kMaxTiles, "tiles of 16 rows");
 typedef TilesOf<MOE_MAX_E_DEV + 4> Tiles;
 
 // Memory that tiles_init needs besides, free afterwards (past a barrier).
@@ -65,11 +69,11 @@ __device__ inline int tiles_init(TilesOf<CAP>& t, TilesScratch& w, const Mx4Args
     all += w.wsum[i];
   }
   for (int e = lo; e < hi; ++e) {
-    t.base[e] = (uint16_t)min(at, 65535);
+    t.base[e] = (uint16_t)min(at, kMaxTiles);
     at += max(0, w.first[e + 1] - w.first[e] + TM - 1) / TM;
   }
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(min(all, 65535));  // more only where groups overlap, as they must not
+  return __builtin_amdgcn_readfirstlane(min(all, kMaxTiles));  // more only where groups overlap, as they must not
 }
 
 // The last group whose first tile is at most ti.

@@ -8,8 +8,8 @@
 // scale as the exponent field of a float: byte 0 as 2^-127 and byte 255 as NaN
 // (checked on the card for all 4,096 pairs of byte and code), so a scale byte
 // shifted into place needs no further care. A value has at most two
-// significant bits, so it is exact in bf16 as in float32 (from 2^128 on it is
-// infinite in both).
+// significant bits, so it is exact in bf16 as in float32 (from 2^128 on, scale
+// bytes 253 and 254, it is infinite in both).
 #pragma once
 
 #include "common.h"
@@ -42,9 +42,15 @@ __device__ inline bf16x8_t mx4_frag(uint32_t w, float scale) {
 }
 
 // A float32 value as the sum of three bf16 values: the top 16 bits, the top 16
-// bits of what is left, and the rest (8 significant bits each, all exact), so
-// that three bf16 products give the float32 product with exact weights. What
-// is not finite keeps its class in the first part alone.
+// bits of what is left, and the rest (8 significant bits each), so that three
+// bf16 products give the float32 product with exact weights. From 2^-110 on the
+// sum is the value; smaller ones lose the bits below 2^-133, the least that bf16
+// holds. What is not finite keeps its class in the first part alone. An infinite
+// weight (from 2^128 on) makes NaN with lower parts that are zero. Cutting it to
+// a finite one for them took 3 to 14 % of a float32 product's time (64 tokens x
+// 11, 512 experts, [2048, 512]: 58 us against 53, its gradient 106 against 93),
+// a path of its own past a branch up to 25 %: left out, as quantisation never
+// writes such scale bytes (253, 254).
 struct Split3 {
   uint32_t h, m, l;  // bf16 bits in the high half
 };

@@ -367,8 +367,12 @@ int moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int32_t rows
  *        x_scales is NULL for the other types.
  *   y  : [T][N], MOE_F32 or MOE_BF16.
  * Every product is exact (float32 x enters the matrix cores as three bf16
- * parts); sums are float32 in a fixed order, with one rounding to y's type. So
- * results are reproducible run to run. T == 0: no launch. */
+ * parts; |x| below 2^-110 loses its bits below 2^-133); sums are float32 in a
+ * fixed order, with one rounding to y's type. So results are reproducible run to
+ * run. Weights of 2^128 and more (scale bytes 253 and 254, which moe_mx4_quantize
+ * never writes) are infinite: results that they reach are infinite or NaN with
+ * MOE_BF16 rows, as the arithmetic of infinities has it, and one of the two with
+ * MOE_F32 rows. With MOE_MX4 rows they are what they are. T == 0: no launch. */
 int moe_mx4_matmul(const void *x, const uint8_t *x_scales, int32_t xdtype, int64_t ldx, int32_t T,
                    const uint8_t *w_codes, const uint8_t *w_scales, int32_t N, int32_t K, void *y,
                    int32_t ydtype, void *stream);

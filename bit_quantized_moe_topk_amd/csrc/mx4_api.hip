@@ -17,6 +17,40 @@ constexpr int32_t kMaxRows = moe::kMx4MaxRows;
 // Assignments of a balance loss: row numbers and ids, and a launch's strides past them, fit 32 bits.
 constexpr long long kMaxIds = 1LL << 30;
 
+// Rows of `bytes` bytes, `step` bytes from one to the next, in memory.
+struct Rows {
+  const void* p;
+  long long rows;
+  unsigned long long bytes, step;
+};
+inline Rows flat(const void* p, unsigned long long bytes) { return {p, 1, bytes, bytes}; }
+inline Rows float_rows(const void* p, int32_t type, int64_t ld, int64_t rows, int64_t n) {
+  return {p, rows, (unsigned long long)n * size_of(type), (unsigned long long)ld * size_of(type)};
+}
+
+// Whether [y, y + n) holds a byte of one of those rows (128 bits: rows may reach past any address).
+bool overlaps(const void* y, unsigned long long n, const Rows& r) {
+  typedef unsigned __int128 wide;
+  if (!y || !r.p || n == 0 || r.rows < 1 || r.bytes == 0) return false;
+  const wide lo = reinterpret_cast<uintptr_t>(y), hi = lo + n, first = reinterpret_cast<uintptr_t>(r.p);
+  if (hi <= first || lo >= first + (wide)(r.rows - 1) * r.step + r.bytes) return false;
+  // the last row that starts at or before y, and the one after it
+  const wide at = lo > first ? (lo - first) / r.step : 0;
+  for (wide i = at; i < at + 2 && i < (wide)r.rows; ++i)
+    if (lo < first + i * r.step + r.bytes && first + i * r.step < hi) return true;
+  return false;
+}
+
+// The same of a product's results or workspace and its operands: rows x, codes wc and scales ws of `mats` matrices.
+bool overlaps_operands(const void* y, unsigned long long n, const void* x, const uint8_t* xs, int32_t type, int64_t ld,
+                       int64_t rows, int32_t n_in, const uint8_t* wc, const uint8_t* ws, int64_t mats, int32_t N, int32_t K) {
+  const unsigned long long blocks = (unsigned long long)mats * N * moe::mx4_blocks(K);
+  const unsigned long long xb = (unsigned long long)rows * moe::mx4_blocks(n_in);
+  return overlaps(y, n, flat(wc, 16 * blocks)) || overlaps(y, n, flat(ws, blocks)) ||
+         (type == MOE_MX4 ? overlaps(y, n, flat(x, 16 * xb)) || overlaps(y, n, flat(xs, xb))
+                          : overlaps(y, n, float_rows(x, type, ld, rows, n_in)));
+}
+
 // Checks that all products share. dtype: of the rows that come in (n_in values
 // each), out: of those that go out.
 int check_product(const void* x, const uint8_t* xs, int32_t dtype, int64_t ld, int64_t rows, int32_t n_in,
@@ -76,6 +110,10 @@ int moe_mx4_quantize(const void* x, int32_t xdtype, int64_t ld, int32_t rows, in
   if (K > kMaxDim || ld > (1LL << 40)) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales || !aligned(x, size_of(xdtype)) || !aligned(codes, 16)) return MOE_ERR_INVALID_ARG;
+  const unsigned long long blocks = (unsigned long long)rows * moe::mx4_blocks(K);
+  const Rows in = float_rows(x, xdtype, ld, rows, K);
+  if (overlaps(codes, 16 * blocks, in) || overlaps(scales, blocks, in) || overlaps(codes, 16 * blocks, flat(scales, blocks)))
+    return MOE_ERR_INVALID_ARG;
   return status_of(moe::launch_mx4_quantize(x, xdtype, ld, rows, K, codes, scales, static_cast<hipStream_t>(stream)));
 }
 
@@ -85,6 +123,9 @@ int moe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows
   if (K > kMaxDim) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!codes || !scales || !y || !aligned(codes, 16) || !aligned(y, size_of(ydtype))) return MOE_ERR_INVALID_ARG;
+  const unsigned long long blocks = (unsigned long long)rows * moe::mx4_blocks(K);
+  const unsigned long long out = (unsigned long long)rows * K * size_of(ydtype);
+  if (overlaps(y, out, flat(codes, 16 * blocks)) || overlaps(y, out, flat(scales, blocks))) return MOE_ERR_INVALID_ARG;
   return status_of(moe::launch_mx4_dequantize(codes, scales, rows, K, ydtype, y, static_cast<hipStream_t>(stream)));
 }
 
@@ -93,6 +134,9 @@ int moe_mx4_matmul(const void* x, const uint8_t* x_scales, int32_t xdtype, int64
                    void* stream) {
   const int st = check_product(x, x_scales, xdtype, ldx, T, K, w_codes, w_scales, N, K, y, ydtype);
   if (st != MOE_OK || T == 0) return st;
+  if (overlaps_operands(y, (unsigned long long)T * N * size_of(ydtype), x, x_scales, xdtype, ldx, T, K, w_codes, w_scales,
+                        1, N, K))
+    return MOE_ERR_INVALID_ARG;
   const moe::Mx4Args a = product(x, x_scales, xdtype, ldx, T, w_codes, w_scales, N, K, y, ydtype);
   return status_of(moe::launch_mx4_forward(a, static_cast<hipStream_t>(stream)));
 }
@@ -102,6 +146,9 @@ int moe_mx4_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, int32_t 
   if (!float_type(dtype)) return MOE_ERR_INVALID_ARG;
   const int st = check_product(dy, nullptr, dtype, ldd, T, N, w_codes, w_scales, N, K, dx, dxdtype);
   if (st != MOE_OK || T == 0) return st;
+  if (overlaps_operands(dx, (unsigned long long)T * K * size_of(dxdtype), dy, nullptr, dtype, ldd, T, N, w_codes, w_scales,
+                        1, N, K))
+    return MOE_ERR_INVALID_ARG;
   const moe::Mx4Args a = product(dy, nullptr, dtype, ldd, T, w_codes, w_scales, N, K, dx, dxdtype);
   return status_of(moe::launch_mx4_gradient(a, static_cast<hipStream_t>(stream)));
 }
@@ -123,6 +170,12 @@ int moe_mx4_experts_matmul(const void* x, const uint8_t* x_scales, int32_t xdtyp
   if (!offsets || (gather && !perm)) return MOE_ERR_INVALID_ARG;
   const size_t need = counter_bytes(A);
   if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  const unsigned long long out = (unsigned long long)A * N * size_of(ydtype);
+  const int32_t rows = gather ? T : A;
+  if (overlaps_operands(y, out, x, x_scales, xdtype, ldx, rows, K, w_codes, w_scales, E + has_shared, N, K) ||
+      (need && (overlaps(y, out, flat(ws, need)) ||
+                overlaps_operands(ws, need, x, x_scales, xdtype, ldx, rows, K, w_codes, w_scales, E + has_shared, N, K))))
+    return MOE_ERR_INVALID_ARG;
   moe::Mx4Args a = product(x, x_scales, xdtype, ldx, A, w_codes, w_scales, N, K, y, ydtype);
   a.T = T;
   a.k = k;
@@ -153,6 +206,11 @@ int moe_mx4_experts_matmul_backward(const void* dy, int32_t dtype, int64_t ldd, 
   if (!offsets || (gather && !slot_of)) return MOE_ERR_INVALID_ARG;
   const size_t need = moe_mx4_experts_matmul_backward_workspace_size(T, k, has_shared, K, gather);
   if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  const unsigned long long out = (unsigned long long)(gather ? T : A) * K * size_of(dxdtype);
+  if (overlaps_operands(dx, out, dy, nullptr, dtype, ldd, A, N, w_codes, w_scales, E + has_shared, N, K) ||
+      (need && (overlaps(dx, out, flat(ws, need)) ||
+                overlaps_operands(ws, need, dy, nullptr, dtype, ldd, A, N, w_codes, w_scales, E + has_shared, N, K))))
+    return MOE_ERR_INVALID_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   void* part = gather ? static_cast<char*>(ws) + counter_bytes(A) : nullptr;
   moe::Mx4Args a = product(dy, nullptr, dtype, ldd, A, w_codes, w_scales, N, K, gather ? part : dx,
@@ -193,6 +251,10 @@ int moe_balance_loss_backward(const void* logits, int32_t dtype, int64_t ld, int
   if (T == 0) return MOE_OK;
   if (!logits || !counts || !kept || !d_losses || !dlogits || !aligned(logits, size_of(dtype)) ||
       !aligned(dlogits, size_of(dtype)) || !aligned(counts, 4) || !aligned(kept, 4) || !aligned(d_losses, 4))
+    return MOE_ERR_INVALID_ARG;
+  // in the logits' own place every row is read by the wave that then writes it
+  if (!(dlogits == logits && ld == E) &&
+      overlaps(dlogits, (unsigned long long)T * E * size_of(dtype), float_rows(logits, dtype, ld, T, E)))
     return MOE_ERR_INVALID_ARG;
   return status_of(moe::launch_balance_gradient(logits, dtype, ld, T, E, k, mask, counts, kept, d_losses, dlogits,
                                                 static_cast<hipStream_t>(stream)));

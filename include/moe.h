@@ -344,7 +344,11 @@ int moe_expert_gateup_fp8(const void *x, int32_t T, const moe_experts *ex, int32
  *           0, 0.5, 1, 1.5, 2, 3, 4, 6.
  *   scales: [R][B] bytes. Byte s stands for 2^(s - 127); the value is the signed
  *           magnitude times that. s = 255: every value of the block is NaN.
- * Codes past K in a row's last block are zero. codes is 16-byte aligned. */
+ * Codes past K in a row's last block are zero. codes is 16-byte aligned.
+ * In every moe_mx4_* call results and workspace share no memory with one another
+ * or with the operands (MOE_ERR_INVALID_ARG). N and K are at most 2^19, the rows
+ * of a product at most 2^22, and row distances at most 2^40 elements
+ * (MOE_ERR_UNSUPPORTED). */
 
 /* Quantises x ([rows][K], MOE_F32 or MOE_BF16, ld elements from row to row,
  * ld >= K). The scale of a block is the power of two that brings its largest
@@ -397,7 +401,7 @@ size_t moe_mx4_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_s
  *                the token of assignment perm[s].
  *   y     : [A][N] in the groups' order. Rows that are in no group (from
  *           offsets[E_tot] on) are left as they were.
- * E_tot is at most MOE_MAX_E + 1, A at most 2^22, N and K at most 2^19.
+ * E_tot is at most MOE_MAX_E + 1.
  * offsets: [E_tot + 1] (moe_group writes one more), perm: [A]; perm may be NULL
  * when gather == 0. Values of perm outside [0, A) are not detected; the kernels
  * stay in bounds and the results of those rows are unspecified. offsets must not
@@ -465,7 +469,8 @@ int moe_balance_loss(const void *logits, int32_t dtype, int64_t ld, int32_t T, i
  *   dlogits[t][e] = p[t][e] * (d_losses[0] * E / n * (f[e] - sum_j f[j] p[t][j])
  *                              + d_losses[1] * 2 * lse[t] / n),
  * f[e] = counts[e] / (n k) (counts depend on idx alone and pass no gradient).
- * Rows of tokens that mask leaves out are 0. T == 0: no launch. */
+ * Rows of tokens that mask leaves out are 0. dlogits may be the logits themselves
+ * (where ld == E), and shares no memory with them otherwise. T == 0: no launch. */
 int moe_balance_loss_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
                               int32_t k, const uint8_t *mask, const int32_t *counts,
                               const int32_t *kept, const float *d_losses, void *dlogits,

@@ -25,11 +25,19 @@ namespace {
 
 constexpr int kWaves = 4;         // tokens in flight per workgroup
 constexpr int kSmallWaves = 16;   // the same of the one-launch form
-constexpr int kSmallT = 128;      // its most tokens
-constexpr int kSmallIds = 4096;   // and ids
-constexpr int kCountIds = 4096;   // ids per counting workgroup
+// The one-launch form's most tokens, ids and logits: all pass through one CU, which soon takes longer than two launches
+// on the GPU (k = 10; one launch against two: 16 x 512 5.6 us against 8.8, 64 x 512 10.7 against 9.1, 128 x 512 17.7
+// against 9.1, 128 x 2,048 45 against 15; 64 x 512 with k = 128 11.1 against 10.3), but a launch less is 3 us of the
+// host's time, which bounds a small call.
+constexpr int kSmallT = 128, kSmallIds = 4096, kSmallLogits = 1 << 15;
+// Ids per counting workgroup: every workgroup of the pass adds up all their counts, so few of them (forward, 8,192
+// tokens x 10: 18.6 us, with 512 ids 20.5, with 8,192 18.2), and not too few (1,000 x 8: 9.3 us, with 1,024 ids 8.5,
+// with 8,192 10.2).
+constexpr int kCountIds = 4096;
 constexpr int kCountGroups = 64;  // most counting workgroups
-constexpr int kRowGroups = 1024;  // most workgroups of the pass over the logits
+// Most workgroups of the pass over the logits (65,536 x 512: 53 us, with 512 63, with 256 91; 8,192 x 512: 18.8, 18.3 and
+// 20.5).
+constexpr int kRowGroups = 1024;
 constexpr int kLines = 16;        // counters of finished workgroups, a line each, before the last one
 
 struct BalanceArgs {
@@ -366,7 +374,7 @@ int row_groups(int T) {
 
 template <int P, bool VEC>
 void launch_rows(const BalanceArgs& a, hipStream_t s) {
-  if (a.T <= kSmallT && (long long)a.T * a.k <= kSmallIds) {
+  if (a.T <= kSmallT && (long long)a.T * a.k <= kSmallIds && (long long)a.T * a.E <= kSmallLogits) {
     MOE_LAUNCH("balance_small", s, (balance_small<P, VEC>), dim3(1), dim3(64 * kSmallWaves), 0, s, a);
     return;
   }
@@ -397,7 +405,9 @@ void launch_grad(const BalanceArgs& a, hipStream_t s) {
     else CALL(32, false);                         \
   } while (0)
 
-// E > 128: fewer experts fill the wave better one at a time.
+// E > 128: fewer experts fill the wave better one at a time (8,192 x 128 float32, fours against ones: 12.0 us against 11.1,
+// the gradient 6.9 against 5.5; 8,192 x 512: 16.0 against 16.3, 14.2 against 13.2; 65,536 x 512: 53 against 55 and 53
+// against 56, bf16 52 against 72 and 47 against 56; 8,192 x 2,048: 41 against 44, 46 against 71).
 bool in_fours(const void* p, long long ld, const void* q, int E, int bf16) {
   const unsigned size = bf16 ? 8 : 16;
   return E > 128 && E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % size == 0 &&

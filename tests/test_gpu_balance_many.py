@@ -76,3 +76,17 @@ def test_gradient_over_the_logits():
         want = moe.balance_loss_backward(x, loss, d)
         y = x.clone()
         assert torch.equal(moe.balance_loss_backward(y, loss, d, out=y), want)
+
+
+@pytest.mark.parametrize("T,E,k,one", [(64, 512, 10, True), (65, 512, 10, False), (128, 256, 8, True), (128, 257, 8, False),
+                                       (16, 2048, 16, True), (17, 2048, 3, False), (15, 2047, 4, True), (128, 100, 32, True),
+                                       (128, 100, 33, False), (1, 2048, 2048, True)])
+def test_either_side_of_the_one_launch_form(T, E, k, one):
+    torch = torch_cuda()
+    import bit_quantized_moe_topk_amd as moe
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    x = torch.randn((T, E), generator=g, device="cuda") * 2
+    idx = torch.topk(x, k).indices.int()
+    assert names_of(lambda: moe.balance_loss(x, idx)) == ({"balance_small"} if one else {"balance_count", "balance_rows"})
+    check_case(x, idx, None)
+    check_case(x.bfloat16(), idx, torch.arange(T, device="cuda") % 3 < 2)

@@ -6,9 +6,10 @@
 // over all of K, so no sums meet. A workgroup takes up to 16 rows of one group,
 // staged in LDS (float32 rows as three exact bf16 parts, split once for all
 // waves) while the last stage's products run, and goes on across tiles. 64
-// tokens x 11 float32 rows, 512 experts, [2048, 512]: 20 us, what reading the
-// matrices takes (44 us in 128-row tiles). Few tiles are bound by one wave's way
-// through all columns, 1.5 us a stage of 256 for bf16 rows.
+// tokens x 11 float32 rows, 512 experts, a few of them popular, [2048, 512]: 19
+// us, what reading the matrices takes (37 us in 128-row tiles). Few tiles are
+// bound by one wave's way through all columns, 1.5 us a stage of 256 for bf16
+// rows.
 #include "mx4_tile.h"
 
 namespace moe {

@@ -313,25 +313,32 @@ __global__ __launch_bounds__(256) void sum_tokens(const float* __restrict__ part
   }
 }
 
-// Which kernels take a product of these rows.
+// Which kernels take a product of these rows. Times: us a call in a chain of
+// calls; experts: 512 and a shared one, 10 a token, evenly loaded, or with a few
+// popular ones (a load that falls with the rank as 1 / rank^1.1).
 //
 // kFewRows (a workgroup for 16 rows and a strip of the matrix, all of them in
-// one launch) is the quickest to begin: up to 32 rows in groups, and for one
-// matrix until the 16-row units fill the chip a few times over (512 rows,
-// [1024, 2048]: tiles 15 us against 23).
+// one launch) is the quickest to begin: up to 32 rows in groups (2 tokens x 11
+// bf16, [1024, 2048]: 12 against kFew's 14 and the tiles' 15), and for one matrix
+// until the 16-row units fill the chip a few times over (bf16, [1024, 2048]: 256
+// rows 10 against the tiles' 17, 512 rows 18 against 17, 1,024 rows 32 against
+// 17; 4-bit rows: 14 against 15 for 512, 25 against 16 for 1,024).
 // kFew (the same 16 rows, from one list of all groups' tiles, the matrix read
 // ahead) reads each matrix once where groups hold a handful of rows. Float32
-// rows, whose parts it makes once for all waves: up to 80 rows a group (64
-// tokens x 11, 512 experts, [2048, 512]: 38 us against the tiles' 97; 4,096
-// tokens: 416 against 500; 16 experts, 384 rows a group, [1024, 2048]: 118
-// against 106), and for one matrix from half a tile for every CU up to four
-// (1,024 rows, [1024, 2048]: 24 us against kFewRows' 51; 256 rows: 22 against
-// 16; 8,192 rows: 134 against the tiles' 106). bf16 rows: up to 12 a group (256
-// tokens, [2048, 512]: 62 against 77; 1,024 tokens: 124 against 110), with more
-// than 1,024 columns up to 3 (32 tokens, [1024, 2048]: 54 against 64; 256
-// tokens: 136 against 121), and there only with four strips for every CU, as
-// one wave goes through all columns (4 tokens: 18 against 15).
-// kTiles: the rest.
+// rows, whose parts it makes once for all waves: up to 80 rows a group ([2048,
+// 512], against the tiles: 64 tokens 55 / 163, with popular experts 19 / 37;
+// 2,000 tokens 240 / 319; 3,500: 388 / 398; 5,000: 542 / 518; 16 experts,
+// [1024, 2048]: 100 rows a group 41 / 91, 384 rows 119 / 98), and for one matrix
+// from half a tile for every CU up to four ([1024, 2048], kFewRows, kFew, tiles:
+// 256 rows 17, 23, 89; 1,024 rows 51, 26, 89; 8,192 rows 410, 142, 105). bf16
+// rows: up to 12 a group ([2048, 512]: 256 tokens 68 / 90, 1,024 tokens 121 /
+// 110), with more than 1,024 columns up to 3 ([1024, 2048], popular experts: 32
+// tokens 23 / 31, evenly loaded 74 / 64; 256 tokens 71 / 57, evenly 164 / 147),
+// and there only with four strips for every CU, as one wave goes through all
+// columns (4 tokens 14.6 / 15.0).
+// kTiles: the rest. Grouped 4-bit rows from 32 on (against kFewRows; [1024,
+// 2048]: 4 tokens 15 / 18, 16 tokens 38 / 52, 64 tokens 84 / 167, where reading
+// the matrices takes 80; [2048, 512]: 13 / 11, 29 / 34, 58 / 109).
 enum Kernels { kFewRows, kFew, kTiles };
 
 Kernels forward_kernels(const Mx4Args& a) {
@@ -348,12 +355,13 @@ Kernels forward_kernels(const Mx4Args& a) {
   return a.A <= (deep ? 3LL : 12LL) * a.E_tot && 2 * groups * strips >= (deep ? 4 : 1) * cus ? kFew : kTiles;
 }
 
-// Gradients: tiles where groups hold more than a few rows, bf16 rows from 4 a group on (64 tokens x
-// 11, 512 experts, [1000, 2048]: tiles 155 us against 100 in 16-row units; 256 tokens, [2048, 512]: 107
-// against 117; 192 rows of 17 experts: 47 against 29), float32 from 12 (256 tokens x 11, 512 experts,
-// [2048, 512]: 445 against 170; 45 rows a group, [1000, 2048]: 100 against 124). One matrix: from about
-// eight 16-row units for every CU on (bf16 [1024, 2048], 2,048 rows: 35 us against 33, 4,096: 38 against
-// 60; float32 4,096 rows: 96 against 98).
+// Gradients: tiles where groups hold more than a few rows and there are more than 256 (tiles against 16-row units, as
+// above). bf16 rows from 4 a group on ([2048, 512]: 64 tokens 72 / 67, 256 tokens 99 / 119, 400 tokens 95 / 139; [1000,
+// 2048], which is not streamed: 64 tokens 243 / 166, 256 tokens 347 / 277, with popular experts 103 / 210; 17 experts,
+// [1024, 2048]: 192 rows 21 / 22, 500 rows 25 / 28). Float32 rows from 12 ([2048, 512]: 256 tokens 501 / 168, 1,000 tokens
+// 555 / 406, 2,000 tokens 746 / 790; 17 experts, [1000, 2048]: 16 rows a group 45 / 57, 45 rows 66 / 49, 64 rows 80 / 156: by
+// how the rows fall on tiles, either leads from 12 to 45 a group). One matrix, [1024, 2048]: from about eight 16-row units
+// for every CU on (bf16: 2,048 rows 35 / 32, 4,096 rows 36 / 57; float32: 4,096 rows 99 / 93).
 bool gradient_tiles_pay(const Mx4Args& a) {
   const bool f32 = a.xdtype == 0;
   if (a.offsets) return a.A > (f32 ? 12LL : 4LL) * a.E_tot && a.A > 256;
@@ -377,8 +385,8 @@ hipError_t launch_mx4_forward(const Mx4Args& a, hipStream_t s) {
     if (mx4_tiles4_can(a)) return launch_mx4_tiles4(a, s);
   }
   const bool vec = a.xdtype != kMx4 && rows_vec(a.x, a.ldx, a.xdtype == 1 ? 2 : 4);
-  // 32 matrix rows a workgroup, or 16 where that leaves half of the CUs without one (one row,
-  // [1024, 2048]: 3.7 us against 5.4)
+  // 32 matrix rows a workgroup, or 16 where that leaves half of the CUs without one (one row, [1024, 2048]: bf16 4.1 us
+  // against 5.8, float32 7.3 against 8.9, 4 bits 3.7 against 4.7)
   const int units = a.offsets ? a.A : (a.A + kRows - 1) / kRows;
   const bool narrow = (long long)units * ((a.N + 31) / 32) * 2 <= device_cus();
   const dim3 g(units, narrow ? (a.N + 15) / 16 : (a.N + 31) / 32);

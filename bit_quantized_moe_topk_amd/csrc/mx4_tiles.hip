@@ -380,8 +380,9 @@ hipError_t launch_mx4_tiles(Mx4Args a, hipStream_t s) {
   const int cap = device_cus();
   // The widest strip that still gives every CU a tile: rows are read once a strip. Of groups some
   // stay empty, so with long rows, where a CU without a tile costs more than a tile too many, half
-  // as many more are asked for ([1024, 2048], 8 tokens x 11: 16.3 us against 20.9 in strips of 256;
-  // 16 tokens 21 against 30 in strips of 512; [2048, 512], 4 tokens: 10.4 against 13.9 the other way).
+  // as many more are asked for (us in strips of 128, 256, 512, bf16, 512 experts and a shared one, 10 a token, a few
+  // popular: [1024, 2048], 8 tokens 15, 20, 30, 16 tokens 26, 21, 31; [2048, 512], 4 tokens 12, 9, 14; evenly loaded,
+  // [1024, 2048], 64 tokens 154, 117, 104, 8,192 tokens 607, 453, 415).
   int strip = even ? 512 : kTN;
   const int want = a.offsets && a.K >= 1024 ? cap + cap / 2 : cap;
   if (even && (tiles * ((a.N + 511) / 512) < want || a.N <= 256)) strip = 256;

@@ -10,8 +10,7 @@ import torch
 moe = pytest.importorskip("bit_quantized_moe_topk_amd")
 if not os.path.exists(moe.LIB_PATH):
     pytest.skip("libmoe.so not built (run __graft_entry__.build())", allow_module_level=True)
-if torch.cuda.is_available():
-    pytest.skip("made-up addresses: not where a call that is taken would launch", allow_module_level=True)
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: not where a call that is taken would launch")
 
 INV = moe.ERR_INVALID_ARG
 MB = 1 << 20

@@ -198,7 +198,7 @@ def gpu_hold(ms: float) -> None:
 
 
 # Sources (by their names' beginnings) of operators that no leg here runs, and that no kernel here includes.
-OTHER_SOURCES = ("mx4", "balance")
+OTHER_SOURCES = ("mx4", "balance", "f8", "norm", "scores", "checks")
 
 
 def kernel_source_hash(d: str = os.path.join(ROOT, "bit_quantized_moe_topk_amd", "csrc")) -> str:

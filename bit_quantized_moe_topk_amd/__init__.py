@@ -17,6 +17,14 @@ Experts in microscaled 4-bit blocks, and a router in training:
     y  = mx4_experts_matmul(x, w, grp, tokens=T)            # [A, N], in the groups' order
     dx = mx4_experts_matmul_backward(dy, w, grp, tokens=T)
     bl = balance_loss(logits, idx);  dlogits = balance_loss_backward(logits, bl, d_losses)
+
+The same in 8 bits (E4M3 with a float32 scale for each block of 128), from the residual stream on:
+    n  = rms_norm(x, weight, residual, fp8=True)            # n.total, n.y for the router, n.fp8 for the experts
+    idx, gates = route_scores(router_logits(n.y, w_router), k, bias, groups=8, keep_groups=4)
+    w  = fp8_quantize(weights, 128)                         # [E (+ 1), N, K] -> Fp8
+    y  = fp8_experts_matmul(n.fp8, w, grp, tokens=T)
+    dx = fp8_experts_matmul_backward(fp8_quantize(dy), w, grp, tokens=T)
+    dlogits = route_scores_backward(logits, idx, d_gates);  dx, dw = rms_norm_backward(dy, n.total, weight, d_total)
 The *_backward calls are explicit: no call here records a graph for autograd.
 """
 from __future__ import annotations
@@ -107,6 +115,16 @@ def lib() -> C.CDLL:
                                                 i32, P, i32, P, sz, P],
             "moe_balance_loss": [P, i32, i64, i32, i32, i32, P, P, P, P, P, P, sz, P],
             "moe_balance_loss_backward": [P, i32, i64, i32, i32, i32, P, P, P, P, P, P],
+            "moe_route_scores": [P, i32, i64, i32, i32, P, i32, i32, i32, i32, i32, i32, C.c_float, P, P, P],
+            "moe_route_scores_backward": [P, i32, i64, i32, i32, i32, i32, i32, C.c_float, P, P, P, P],
+            "moe_fp8_quantize": [P, i32, i64, i32, i32, i32, i32, P, P, P],
+            "moe_fp8_dequantize": [P, P, i32, i32, i32, i32, i32, P, P],
+            "moe_fp8_matmul": [P, P, i32, P, P, i32, i32, P, i32, P],
+            "moe_fp8_matmul_backward": [P, P, i32, P, P, i32, i32, P, i32, P],
+            "moe_fp8_experts_matmul": [P, P, i32, i32, i32, i32, i32, P, P, P, P, i32, i32, P, i32, P, sz, P],
+            "moe_fp8_experts_matmul_backward": [P, P, i32, i32, i32, i32, i32, P, P, P, P, i32, i32, P, i32, P, sz, P],
+            "moe_rms_norm": [P, i32, i64, P, i64, P, i32, C.c_float, i32, i32, P, P, P, P, P],
+            "moe_rms_norm_backward": [P, i64, P, i64, i32, P, i32, P, i64, C.c_float, i32, i32, P, P, P, sz, P],
         }
         for name, args in sigs.items():
             getattr(L, name).argtypes = args
@@ -117,6 +135,9 @@ def lib() -> C.CDLL:
         L.moe_mx4_experts_matmul_backward_workspace_size.restype = sz
         L.moe_balance_loss_workspace_size.argtypes = [i32] * 3
         L.moe_balance_loss_workspace_size.restype = sz
+        for name, n in (("moe_fp8_experts_matmul", 3), ("moe_fp8_experts_matmul_backward", 5), ("moe_rms_norm_backward", 2)):
+            f = getattr(L, name + "_workspace_size")
+            f.argtypes, f.restype = [i32] * n, sz
         L.moe_profile_begin.argtypes = [i32]
         L.moe_profile_begin.restype = C.c_int
         L.moe_profile_end.argtypes = []
@@ -820,8 +841,315 @@ def balance_loss_backward(logits: torch.Tensor, loss: BalanceLoss, d_losses: tor
     return d
 
 
+# ---- routing by scores ----------------------------------------------------------------
+
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _score(name: str) -> int:
+    if name not in _SCORES:
+        raise ValueError(f"score is 'sigmoid' or 'softmax', not {name!r}")
+    return _SCORES[name]
+
+
+def route_scores(logits: torch.Tensor, k: int, bias: torch.Tensor | None = None, score: str = "sigmoid", groups: int = 1,
+                 keep_groups: int = 1, group_top: int = 2, renormalize: bool = True, scale: float = 1.0, out=None):
+    """Top-k experts per token by scores, and their gates (moe_route_scores): (idx int32 [T, k], gates
+    float32 [T, k]). logits: [T, E], float32 or bfloat16; bias: float32 [E], for the selection alone. With
+    `groups` > 1 the experts lie in that many groups, of which the `keep_groups` stay whose `group_top`
+    largest biased scores add up to most. `out` = (idx, gates) writes into existing tensors."""
+    code, ld, T = _rows("logits", logits)
+    E, dev = logits.shape[1], logits.device
+    if bias is not None:
+        _need_cuda("bias", bias, torch.float32)
+        if bias.numel() != E or bias.device != dev:
+            raise ValueError(f"bias must hold {E} values on {dev}")
+    if not 1 <= k <= _MOST or not all(0 <= v <= _MOST for v in (groups, keep_groups, group_top)):
+        raise ValueError("k, groups, keep_groups and group_top must be counts")
+    if out is None:
+        idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        gates = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        idx, gates = out
+        _int32("idx", idx, dev)
+        _need_cuda("gates", gates, torch.float32)
+        if tuple(idx.shape) != (T, k) or tuple(gates.shape) != (T, k) or gates.device != dev:
+            raise ValueError(f"out tensors must be [{T}, {k}] on {dev}")
+    _call("moe_route_scores", dev, logits.data_ptr(), code, ld, T, E, None if bias is None else bias.data_ptr(),
+          _score(score), groups, keep_groups, group_top, k, int(bool(renormalize)), scale, idx.data_ptr(), gates.data_ptr())
+    return idx, gates
+
+
+def route_scores_backward(logits: torch.Tensor, idx: torch.Tensor, d_gates: torch.Tensor, score: str = "sigmoid",
+                          renormalize: bool = True, scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of route_scores' gates for the logits, [T, E] in their type, from idx as it gave them and
+    the gates' gradient (float32 [T, k]); `score`, `renormalize` and `scale` as there (moe_route_scores_backward)."""
+    code, ld, T = _rows("logits", logits)
+    E, dev = logits.shape[1], logits.device
+    _int32("idx", idx, dev)
+    _need_cuda("d_gates", d_gates, torch.float32)
+    if idx.dim() != 2 or idx.shape[0] != T or d_gates.shape != idx.shape or d_gates.device != dev:
+        raise ValueError(f"idx and d_gates must be [{T}, k] on {dev}: got {tuple(idx.shape)} and {tuple(d_gates.shape)}")
+    d = _result(out, (T, E), logits.dtype, dev)
+    _call("moe_route_scores_backward", dev, logits.data_ptr(), code, ld, T, E, idx.shape[1], _score(score),
+          int(bool(renormalize)), scale, idx.data_ptr(), d_gates.data_ptr(), d.data_ptr())
+    return d
+
+
+# ---- 8-bit operands ---------------------------------------------------------------------
+
+
+class Fp8:
+    """Rows of K values in 8 bits: codes float8_e4m3fn [..., R, 128 B], B = ceil(K / 128) (codes past K are zero), with
+    float32 scales, one for 128 values of a row ([..., R, B], block_rows 1) or for 128 x 128 values of a matrix
+    ([..., ceil(R / 128), B], block_rows 128). The layout is in include/moe.h."""
+
+    __slots__ = ("codes", "scales", "K", "block_rows")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, K: int, block_rows: int = 1):
+        if isinstance(codes, torch.Tensor) and codes.dtype is torch.uint8:
+            codes = codes.view(torch.float8_e4m3fn)
+        _need_cuda("codes", codes, torch.float8_e4m3fn)
+        _need_cuda("scales", scales, torch.float32)
+        if block_rows not in (1, 128):
+            raise ValueError(f"block_rows is 1 (rows) or 128 (matrices), not {block_rows}")
+        c, B = codes.shape, (K + 127) // 128
+        if K < 1 or len(c) < 2 or c[-1] != 128 * B or tuple(scales.shape) != (*c[:-2], -(-c[-2] // block_rows), B):
+            raise ValueError(f"codes {tuple(c)} and scales {tuple(scales.shape)} do not hold rows of {K}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        if K > _MOST or c[:-1].numel() > _MOST:
+            raise ValueError(f"too many rows or values: {tuple(c[:-1])} rows of {K}")
+        self.codes, self.scales, self.K, self.block_rows = codes, scales, K, block_rows
+
+    @classmethod
+    def _new(cls, shape, K: int, block_rows: int, dev: torch.device) -> "Fp8":
+        """Room for rows [*shape, K]."""
+        self, B = object.__new__(cls), (K + 127) // 128
+        self.codes = torch.empty((*shape, 128 * B), dtype=torch.float8_e4m3fn, device=dev)
+        self.scales = torch.empty((*shape[:-1], -(-shape[-1] // block_rows), B), dtype=torch.float32, device=dev)
+        self.K, self.block_rows = K, block_rows
+        return self
+
+    @property
+    def shape(self) -> tuple:
+        return (*self.codes.shape[:-1], self.K)
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+
+def _mats(shape, block_rows: int):
+    """(matrices, rows of each) of rows [..., R]: rows with a scale of their own are all one matrix's."""
+    R = shape[-1]
+    n = shape[:-1].numel()
+    return (1, n * R) if block_rows == 1 else (n, R)
+
+
+def fp8_quantize(x: torch.Tensor, block_rows: int = 1, out: Fp8 | None = None) -> Fp8:
+    """Rows x ([..., K], float32 or bfloat16) in 8 bits, a scale for 128 values of a row (block_rows 1) or for
+    128 x 128 values of a matrix (block_rows 128) (moe_fp8_quantize). More than two dimensions must be
+    contiguous; of two, rows may lie further apart."""
+    if isinstance(x, torch.Tensor) and x.dim() > 2 and not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if not isinstance(x, torch.Tensor) or x.dim() < 2 or x.shape[-1] < 1:
+        raise ValueError("x must be a tensor [..., K] of two dimensions or more")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows is 1 (rows) or 128 (matrices), not {block_rows}")
+    K = x.shape[-1]
+    code, ld, _ = _rows("x", x if x.dim() == 2 else x.reshape(-1, K))
+    mats, rows = _mats(x.shape[:-1], block_rows)
+    if out is None:
+        out = Fp8._new(x.shape[:-1], K, block_rows, x.device)
+    elif out.shape != tuple(x.shape) or out.device != x.device or out.block_rows != block_rows:
+        raise ValueError(f"out must be an Fp8 of {tuple(x.shape)} with block_rows {block_rows} on {x.device}")
+    _call("moe_fp8_quantize", x.device, x.data_ptr(), code, ld, mats, rows, K, block_rows, out.codes.data_ptr(),
+          out.scales.data_ptr())
+    return out
+
+
+def fp8_dequantize(q: Fp8, dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of q, [..., K], rounded once to float32 or bfloat16."""
+    y = _result(out, q.shape, dtype, q.device)
+    mats, rows = _mats(q.codes.shape[:-1], q.block_rows)
+    _call("moe_fp8_dequantize", q.device, q.codes.data_ptr(), q.scales.data_ptr(), mats, rows, q.K, q.block_rows,
+          _FLOATS[dtype], y.data_ptr())
+    return y
+
+
+def _fp8_rows(name: str, x: Fp8, n: int) -> int:
+    """Checks rows of n values; how many there are."""
+    if not isinstance(x, Fp8) or x.block_rows != 1 or x.codes.dim() != 2 or x.K != n:
+        raise ValueError(f"{name} must be an Fp8 of rows of {n} values, with block_rows 1"
+                         + (f": got {x.shape}, {x.block_rows}" if isinstance(x, Fp8) else ""))
+    return x.codes.shape[0]
+
+
+def _fp8_matrix(w: Fp8, dims: int, dev: torch.device | None) -> int:
+    """Checks a matrix (dims 2) or the experts' (dims 3); its rows."""
+    if not isinstance(w, Fp8) or w.codes.dim() != dims or w.block_rows != 128 or w.codes.shape[-2] < 1:
+        raise ValueError(f"w must be an Fp8 of {dims} dimensions with block_rows 128, with a row at least")
+    if dev is not None and w.codes.device != dev:
+        raise ValueError(f"w must be on {dev}")
+    return w.codes.shape[-2]
+
+
+def fp8_matmul(x: Fp8, w: Fp8, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """x W^T: [T, N] for 8-bit rows x ([T, K]) and a matrix w ([N, K]) (moe_fp8_matmul), in bfloat16 (on the 8-bit
+    matrix cores) or float32 (products exact)."""
+    N = _fp8_matrix(w, 2, None)
+    T, dev = _fp8_rows("x", x, w.K), x.device
+    _same("w", w, dev)
+    y = _result(out, (T, N), dtype, dev)
+    _call("moe_fp8_matmul", dev, x.codes.data_ptr(), x.scales.data_ptr(), T, w.codes.data_ptr(), w.scales.data_ptr(), N, w.K,
+          y.data_ptr(), _FLOATS[dtype])
+    return y
+
+
+def fp8_matmul_backward(dy: Fp8, w: Fp8, dtype: torch.dtype = torch.bfloat16,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of fp8_matmul for its rows: dy W, [T, K], for 8-bit rows dy ([T, N]: fp8_quantize of the
+    result's gradient). w is not trained in 8 bits."""
+    N = _fp8_matrix(w, 2, None)
+    T, dev = _fp8_rows("dy", dy, N), dy.device
+    _same("w", w, dev)
+    dx = _result(out, (T, w.K), dtype, dev)
+    _call("moe_fp8_matmul_backward", dev, dy.codes.data_ptr(), dy.scales.data_ptr(), T, w.codes.data_ptr(),
+          w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dtype])
+    return dx
+
+
+def fp8_experts_matmul(x: Fp8, w: Fp8, grouping: Grouping, tokens: int | None = None, dtype: torch.dtype = torch.bfloat16,
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """8-bit rows grouped by expert, each times its expert's matrix (moe_fp8_experts_matmul): [A, N] in the
+    groups' order. w: [E, N, K], or [E + 1, N, K] with the shared expert last. x holds the A rows in the groups'
+    order, or, where `tokens` gives their number, one row a token. Rows of `out` that are in no group are left as
+    they were."""
+    N = _fp8_matrix(w, 3, None)
+    R, dev = _fp8_rows("x", x, w.K), x.device
+    _same("w", w, dev)
+    T, k, E, shared, A = _groups(grouping, w, tokens, dev)
+    if R != T:
+        raise ValueError(f"x has {R} rows, expected {T}")
+    gather = tokens is not None
+    if gather:
+        _int32("grouping.perm", grouping.perm, dev, A)
+    y = _result(out, (A, N), dtype, dev)
+    wp, wn, keep = _workspace(workspace, _bytes("moe_fp8_experts_matmul_workspace_size", T, k, shared), dev)
+    _call("moe_fp8_experts_matmul", dev, x.codes.data_ptr(), x.scales.data_ptr(), T, k, E, shared, int(gather),
+          grouping.offsets.data_ptr(), grouping.perm.data_ptr() if gather else None, w.codes.data_ptr(),
+          w.scales.data_ptr(), N, w.K, y.data_ptr(), _FLOATS[dtype], wp, wn)
+    return y
+
+
+def fp8_experts_matmul_backward(dy: Fp8, w: Fp8, grouping: Grouping, tokens: int | None = None,
+                                dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of fp8_experts_matmul for its rows: 8-bit rows dy [A, N] in the groups' order -> [A, K], or, where
+    `tokens` gives their number, [tokens, K], the sum over each token's assignments. w is not trained in 8 bits."""
+    N = _fp8_matrix(w, 3, None)
+    R, dev = _fp8_rows("dy", dy, N), dy.device
+    _same("w", w, dev)
+    T, k, E, shared, A = _groups(grouping, w, tokens, dev)
+    if R != A:
+        raise ValueError(f"dy has {R} rows, expected {A}")
+    gather = tokens is not None
+    if gather:
+        _int32("grouping.slot_of", grouping.slot_of, dev, A)
+    dx = _result(out, (T, w.K), dtype, dev)
+    wp, wn, keep = _workspace(
+        workspace, _bytes("moe_fp8_experts_matmul_backward_workspace_size", T, k, shared, w.K, int(gather)), dev)
+    _call("moe_fp8_experts_matmul_backward", dev, dy.codes.data_ptr(), dy.scales.data_ptr(), T, k, E, shared, int(gather),
+          grouping.offsets.data_ptr(), grouping.slot_of.data_ptr() if gather else None, w.codes.data_ptr(),
+          w.scales.data_ptr(), N, w.K, dx.data_ptr(), _FLOATS[dtype], wp, wn)
+    return dx
+
+
+# ---- RMS norm ---------------------------------------------------------------------------
+
+
+@dataclass
+class Norm:
+    total: torch.Tensor | None  # [T, H]: x + residual (None without a residual)
+    y: torch.Tensor | None      # [T, H]: the normed rows
+    fp8: Fp8 | None             # the same as 8-bit rows
+
+
+def _norm_weight(weight: torch.Tensor, H: int, dev: torch.device) -> int:
+    _need_cuda("weight", weight, (torch.float32, torch.bfloat16))
+    if weight.numel() != H or weight.device != dev:
+        raise ValueError(f"weight must hold {H} values on {dev}")
+    return _FLOATS[weight.dtype]
+
+
+def _like_rows(name: str, t: torch.Tensor, like: torch.Tensor):
+    """(pointer, row distance) of rows that go with `like`; (None, 0) of none."""
+    if t is None:
+        return None, 0
+    _, ld, R = _rows(name, t, like.shape[1])
+    if t.dtype != like.dtype or R != like.shape[0] or t.device != like.device:
+        raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype} on {like.device}")
+    return t.data_ptr(), ld
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+             rows: bool = True, fp8: bool = False, out: Norm | None = None) -> Norm:
+    """RMS norm of x + residual ([T, H], float32 or bfloat16; moe_rms_norm): the sum in x's type, the normed rows in
+    x's type (`rows`), and as 8-bit rows (`fp8`). weight: [H], float32 or bfloat16. `out` writes into a Norm's
+    tensors (its total may be x or residual)."""
+    code, ld, T = _rows("x", x)
+    H, dev = x.shape[1], x.device
+    wcode = _norm_weight(weight, H, dev)
+    rp, rld = _like_rows("residual", residual, x)
+    if not rows and not fp8:
+        raise ValueError("rms_norm gives rows, 8-bit rows, or both")
+    if out is None:
+        out = Norm(torch.empty((T, H), dtype=x.dtype, device=dev) if residual is not None else None,
+                   torch.empty((T, H), dtype=x.dtype, device=dev) if rows else None,
+                   Fp8._new(torch.Size((T,)), H, 1, dev) if fp8 else None)
+    else:
+        if (out.y is not None) != rows or (out.fp8 is not None) != fp8 or (out.total is not None) != (residual is not None):
+            raise ValueError("out does not hold what is asked for")
+        for t in (out.total, out.y):
+            if t is not None:
+                _result(t, (T, H), x.dtype, dev)
+        if fp8 and (out.fp8.shape != (T, H) or out.fp8.block_rows != 1 or out.fp8.device != dev):
+            raise ValueError(f"out.fp8 must be an Fp8 of {(T, H)} with block_rows 1 on {dev}")
+    _call("moe_rms_norm", dev, x.data_ptr(), code, ld, rp, rld, weight.data_ptr(), wcode, eps, T, H,
+          None if out.total is None else out.total.data_ptr(), None if out.y is None else out.y.data_ptr(),
+          out.fp8.codes.data_ptr() if fp8 else None, out.fp8.scales.data_ptr() if fp8 else None)
+    return out
+
+
+def rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, d_total: torch.Tensor | None = None,
+                      eps: float = 1e-6, workspace: torch.Tensor | None = None, out=None):
+    """The gradients of rms_norm (moe_rms_norm_backward): (dh [T, H] in h's type, dweight float32 [H]). h: the rows that
+    were normed (rms_norm's total, or its x where there was no residual); dy: the normed rows' gradient; d_total: what
+    reaches total besides. dh is the gradient of x and of residual alike. `out` = (dh, dweight) writes into
+    existing tensors; a dweight of None there is left out."""
+    code, ld, T = _rows("h", h)
+    H, dev = h.shape[1], h.device
+    wcode = _norm_weight(weight, H, dev)
+    dp, ldd = _like_rows("dy", dy, h)
+    tp, ldt = _like_rows("d_total", d_total, h)
+    if dp is None:
+        raise ValueError("dy must be a tensor")
+    dh, dw = out if out is not None else (None, torch.empty(H, dtype=torch.float32, device=dev))
+    dh = _result(dh, (T, H), h.dtype, dev)
+    if dw is not None and out is not None:
+        _result(dw, (H,), torch.float32, dev)
+    need = _bytes("moe_rms_norm_backward_workspace_size", T, H) if dw is not None else 0
+    wp, wn, keep = _workspace(workspace, need, dev)
+    _call("moe_rms_norm_backward", dev, dp, ldd, h.data_ptr(), ld, code, weight.data_ptr(), wcode, tp, ldt, eps, T, H,
+          dh.data_ptr(), None if dw is None else dw.data_ptr(), wp, wn)
+    return dh, dw
+
+
 __all__ = ["layer", "layer_static", "profile_begin", "profile_end", "router_logits", "route_topk", "route_group", "group", "Grouping", "Experts", "ffn_q", "lib", "status_string",
            "MoeError", "Q2", "Q3", "F32", "BF16", "FAST", "CHECK_F32", "MAX_E", "LIB_PATH",
            "MX4", "Mx4", "mx4_quantize", "mx4_dequantize", "mx4_matmul", "mx4_matmul_backward",
            "mx4_experts_matmul", "mx4_experts_matmul_backward", "BalanceLoss", "balance_loss",
-           "balance_loss_backward"]
+           "balance_loss_backward", "route_scores", "route_scores_backward", "Fp8", "fp8_quantize", "fp8_dequantize",
+           "fp8_matmul", "fp8_matmul_backward", "fp8_experts_matmul", "fp8_experts_matmul_backward", "Norm", "rms_norm",
+           "rms_norm_backward"]

@@ -1,0 +1,173 @@
+// 8-bit operands: the block format and the device helpers that the quantiser,
+// the norm and the products share (header-only; not part of the ABI).
+//
+// A row's values are E4M3 codes, 128 of them to a block with one float32 scale
+// (a row), or 128 x 128 (a matrix); rows of codes are filled up to whole blocks
+// with zeros, so that every row starts on 128 bytes and no kernel looks at the end
+// of a contraction.
+//
+// scale = max(largest magnitude, 2^-116) / 448, which is a normal number, and
+// code = the exact quotient rounded once. A quotient rounded to float32 first may
+// come to lie on the border between two codes (one in 1,000 values of a bf16
+// row does, whose magnitudes and largest magnitude are short), so the sign of
+// the exact remainder decides there (f8_quotient).
+//
+// The 8-bit matrix cores add up the 128 products of a 16x16x128 instruction with
+// about 13 bits under the binade of the largest (65536 + 8 is kept, 65536 + 4 is
+// not: measured, the same for every 8-bit form). Against bf16's own half step, 2^-9, that is
+// nothing, so results in bf16 take them. Results in float32 take the bf16 matrix
+// cores: a code has four significant bits, so it is exact in bf16, products are
+// exact, and sums keep float32's bits. Block sums are scaled and added up in
+// float32 either way.
+#pragma once
+
+#include "mx4_tile.h"
+#include "topk.h"
+
+namespace moe {
+
+constexpr int kF8Block = 128;
+constexpr float kF8Least = 0x1p-116f;  // least magnitude that a scale goes by
+
+__host__ __device__ inline int f8_blocks(int K) { return (K + kF8Block - 1) / kF8Block; }
+
+// One product launch: y[s][n] = sum over c of x[row(s)][c] M[e(s)][n][c], N results a row and
+// K columns c. Mx4Args' x and wc are codes; forward: the stored matrix is M ([N][wb 128]);
+// back: it is M turned ([K][wb 128]).
+struct F8Args : Mx4Args {
+  const float* xf;  // [rows][xb]
+  const float* wf;  // [E_tot][..][wb]
+  int xb, wb;       // blocks of a row of x (along K) and of a stored row of the matrix
+  bool back;
+  bool exact;       // products on the bf16 matrix cores (results that stay in float32)
+};
+
+// The scale for x of a block, and the float32 quotient of v by it, exact but for its last bit, which
+// is set where the quotient is not exact: so rounding it to a code rounds the exact quotient. (Two
+// steps bring v * inv to within one unit of it; the remainder's sign says on which side it lies.)
+__device__ inline float f8_scale_of(float top) { return fmaxf(top, kF8Least) / 448.f; }
+
+__device__ inline float f8_quotient(float v, float s, float inv) {
+  float q = v * inv;
+  q = fmaf(fmaf(-q, s, v), inv, q);
+  const float r = fmaf(-q, s, v);
+  uint32_t u = __float_as_uint(q);
+  if (r != 0.f && fabsf(q) >= 0x1p-11f) {  // (below, the code is 0)
+    if ((r < 0.f) != (q < 0.f)) --u;
+    u |= 1u;
+  }
+  return __builtin_copysignf(__uint_as_float(u), v);  // (a zero keeps its sign)
+}
+
+// The codes of eight values of a block whose largest magnitude is `top` (bits, ordered as
+// integers): two dwords. *scale is the block's. Blocks below 2^-40 are brought up first, so that no
+// remainder is lost below float32's range.
+__device__ inline uint2 f8_codes(const float (&f)[8], uint32_t top, float* scale) {
+  if (top >= 0x7F800000u) {
+    *scale = __uint_as_float(0x7FC00000u);
+    return make_uint2(0u, 0u);
+  }
+  float s = f8_scale_of(__uint_as_float(top));
+  *scale = s;
+  const float up = top < 0x2B800000u ? 0x1p80f : 1.f;
+  s *= up;
+  const float inv = 1.f / s;
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(f[i] * up, s, inv);
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+__device__ inline uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The largest of eight magnitudes over the 16 lanes of a row of lanes, which hold one block.
+__device__ inline uint32_t f8_top16(const float (&f)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, magnitude(f[i]));
+  top = max(top, dpp(top, 0xB1));
+  top = max(top, dpp(top, 0x4E));
+  top = max(top, dpp(top, 0x141));
+  return max(top, dpp(top, 0x140));
+}
+
+// Eight values from column c of a row of n in either type (zeros past n). vec: 16-byte loads.
+template <bool BF>
+__device__ inline void load8(const void* __restrict__ row, int c, int n, bool vec, float (&f)[8]) {
+  if constexpr (BF) {
+    const uint4 u = load8_bf16(static_cast<const uint16_t*>(row), c, n, vec);
+    f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+    f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+  } else {
+    load8_f32(static_cast<const float*>(row), c, n, vec, f);
+  }
+}
+
+template <bool BF>
+__device__ inline void store8(void* __restrict__ row, int c, int n, bool vec, const float (&f)[8]) {
+  if constexpr (BF) {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+    uint16_t* y = static_cast<uint16_t*>(row) + c;
+    if (vec && c + 8 <= n) {
+      *reinterpret_cast<uint4*>(y) = make_uint4(p[0], p[1], p[2], p[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < n) y[i] = (uint16_t)(p[i / 2] >> (16 * (i & 1)));
+    }
+  } else {
+    float* y = static_cast<float*>(row) + c;
+    if (vec && c + 8 <= n) {
+      *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(y + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < n) y[i] = f[i];
+    }
+  }
+}
+
+// Eight codes as bf16 values, exactly.
+__device__ inline bf16x8_t f8_bf16(int lo, int hi) {
+  typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+  const uint4 v = make_uint4(__builtin_bit_cast(uint32_t, (pair_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false)),
+                             __builtin_bit_cast(uint32_t, (pair_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true)),
+                             __builtin_bit_cast(uint32_t, (pair_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false)),
+                             __builtin_bit_cast(uint32_t, (pair_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true)));
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// The 128 products of a block, 16 matrix rows (a) by 16 rows (b): lane l has 32 codes of row l % 16 of
+// each; result i is matrix row 4 (l / 16) + i, row l % 16.
+template <bool EXACT>
+__device__ inline floatx4_t f8_products(const int8v_t& a, const int8v_t& b) {
+  if constexpr (EXACT) {
+    floatx4_t c = {};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_bf16(a[i], a[i + 1]), f8_bf16(b[i], b[i + 1]), c, 0, 0, 0);
+    return c;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, floatx4_t{}, 0, 0, 0, 0, 0, 0);
+  }
+}
+
+__device__ inline int8v_t f8_pair(uint4 a, uint4 b) {
+  return int8v_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// ---- launchers (each returns hipGetLastError() after enqueueing) ----------
+hipError_t launch_f8_quantize(const void* x, int xdtype, long long ld, int mats, int rows, int K, int block_rows,
+                              uint8_t* codes, float* scales, hipStream_t s);
+hipError_t launch_f8_dequantize(const uint8_t* codes, const float* scales, int mats, int rows, int K, int block_rows,
+                                int ydtype, void* y, hipStream_t s);
+hipError_t launch_f8_product(const F8Args& a, hipStream_t s);
+
+}  // namespace moe

@@ -476,6 +476,164 @@ int moe_balance_loss_backward(const void *logits, int32_t dtype, int64_t ld, int
                               const int32_t *kept, const float *d_losses, void *dlogits,
                               void *stream);
 
+/* ---- routing by scores -------------------------------------------------------- */
+
+#define MOE_SIGMOID 0 /* score of an expert: 1 / (1 + exp(-logit))          */
+#define MOE_SOFTMAX 1 /* exp(logit) / sum of exp(logit) over all E experts  */
+
+/* Top-k selection and gates from scores, with a bias that takes part in the
+ * selection alone and with groups of experts. Per token:
+ *   s[e] = the score of logits[t][e];  c[e] = s[e] + bias[e] (bias NULL: 0)
+ *   The E experts lie in `groups` groups of E / groups neighbours. A group's value
+ *   is the sum of its group_top (1 or 2) largest c; the `keep` groups of the
+ *   largest values stay, equal values in favour of the lower group.
+ *   idx[t][0..k-1]  = the k experts of the kept groups with the largest c, in
+ *                     descending rank, equal c in favour of the lower index.
+ *   gates[t][j]     = scale * s[idx_j], with renorm != 0 over the sum of the k
+ *                     selected scores (0 where that sum is 0).
+ * Groups and experts are ranked by values in 64 bits, so that the order does not
+ * depend on how scores are rounded to 32 (without a bias by the logits themselves,
+ * which have the same order). An expert whose logit or bias is -inf is switched off:
+ * it comes behind every other (in a group's sum it is left out; a group that has no other
+ * comes behind every other group), with its score, 0 where the logit is -inf. A
+ * c that is NaN ranks below -inf. Of a token whose logits are all -inf every score
+ * is 0. Softmax scores of a token with a NaN or +inf logit are NaN: its gates
+ * are NaN, its indices distinct and in range.
+ * logits: [T][E], MOE_F32 or MOE_BF16, ld elements from row to row (>= E); bias:
+ * [E] float32 or NULL; idx: [T][k] int32; gates: [T][k] float32.
+ * Requires E % groups == 0, 1 <= keep <= groups <= 64, group_top 1 or 2,
+ * 1 <= k <= keep * E / groups, E <= MOE_MAX_E, T <= 2^22, scale finite. Results share no
+ * memory with one another or with the operands (MOE_ERR_INVALID_ARG), here and in every
+ * call down to moe_fp8_experts_matmul_backward, where nothing else is said. T == 0: no launch. */
+int moe_route_scores(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
+                     const float *bias, int32_t score, int32_t groups, int32_t keep,
+                     int32_t group_top, int32_t k, int32_t renorm, float scale, int32_t *idx,
+                     float *gates, void *stream);
+
+/* The gradient of moe_route_scores' gates for the logits, from idx as it wrote
+ * them and the gates' gradient d_gates [T][k] (float32). The selection itself, and so
+ * the bias, passes none. With S the sum of the selected scores, d = scale * d_gates, and for
+ * renorm d := (d_j - sum_i d_i s_i / S) / S (0 where S is 0):
+ *   sigmoid: dlogits[t][idx_j] = d_j s_j (1 - s_j), 0 elsewhere
+ *   softmax: dlogits[t][e]     = s_e ((sum of d_j over idx_j = e) - sum_i d_i s_i)
+ * An index that appears twice in a row counts twice; one outside [0, E) is not
+ * there. dlogits: [T][E] in the logits' type, rows E elements apart. A token's
+ * NaN logits make its gradient NaN where they enter. k <= MOE_MAX_E. */
+int moe_route_scores_backward(const void *logits, int32_t dtype, int64_t ld, int32_t T, int32_t E,
+                              int32_t k, int32_t score, int32_t renorm, float scale,
+                              const int32_t *idx, const float *d_gates, void *dlogits, void *stream);
+
+/* ---- 8-bit rows and matrices ---------------------------------------------------- */
+
+/* Values in 8 bits: E4M3 codes (sign, 4 exponent bits with bias 7, 3 bits of
+ * mantissa; largest 448, 0x7F and 0xFF are NaN, no infinities) and a float32
+ * scale for each block; a value is its code's times the scale. B = ceil(K / 128).
+ *   codes : rows of 128 B bytes, one a value; codes past K are zero. 16-byte aligned.
+ *   scales: of rows (activations) [R][B], one for 128 consecutive values of a row;
+ *           of a matrix [ceil(N / 128)][B], one for 128 rows by 128 columns.
+ * Several matrices ([E_tot][N][K]) have codes [E_tot][N][128 B] and scales
+ * [E_tot][ceil(N / 128)][B]. N and K are at most 2^19, the rows of a product at most
+ * 2^22, and row distances at most 2^40 elements (MOE_ERR_UNSUPPORTED). */
+
+/* Quantises x (`mats` matrices of [rows][K], MOE_F32 or MOE_BF16, ld elements from row
+ * to row, rows * ld from matrix to matrix). block_rows is 1 (rows) or 128
+ * (matrices). scale = max(largest magnitude of the block, 2^-116) / 448 in float32;
+ * code = x / scale, the exact quotient rounded once to the nearest code, ties to
+ * the even one; zeros keep their sign. A block that holds a NaN or an infinity becomes
+ * NaN (scale NaN, codes 0). mats == 0 or rows == 0: no launch. */
+int moe_fp8_quantize(const void *x, int32_t xdtype, int64_t ld, int32_t mats, int32_t rows, int32_t K,
+                     int32_t block_rows, uint8_t *codes, float *scales, void *stream);
+
+/* The values that codes and scales stand for, rounded once to ydtype: y [mats][rows][K],
+ * MOE_F32 or MOE_BF16. */
+int moe_fp8_dequantize(const uint8_t *codes, const float *scales, int32_t mats, int32_t rows, int32_t K,
+                       int32_t block_rows, int32_t ydtype, void *y, void *stream);
+
+/* y[t][n] = sum_k x[t][k] W[n][k] for T 8-bit rows and one 8-bit matrix of N rows of
+ * K values. y: [T][N], MOE_F32 or MOE_BF16. Blocks of 128 columns are added up in
+ * float32, each scaled by its two scales, in a fixed order (reproducible run to
+ * run). For MOE_F32 results every product of two codes is exact and their sum is float32; for
+ * MOE_BF16 the 8-bit matrix cores add up a block's 128 products, which drop what
+ * lies under 2^-13 of the binade of the block's largest product (far below bf16's own step
+ * for values of like size). T == 0: no launch. */
+int moe_fp8_matmul(const uint8_t *x_codes, const float *x_scales, int32_t T, const uint8_t *w_codes,
+                   const float *w_scales, int32_t N, int32_t K, void *y, int32_t ydtype, void *stream);
+
+/* The gradient of moe_fp8_matmul for its rows: dx[t][k] = sum_n dy[t][n] W[n][k].
+ * dy: 8-bit rows of N values (a scale for 128 of them), dx: [T][K], MOE_F32 or MOE_BF16.
+ * Codes of dy past N are zero. Products and sums as in moe_fp8_matmul. The matrix is not
+ * trained in 8 bits: it has no gradient here. */
+int moe_fp8_matmul_backward(const uint8_t *dy_codes, const float *dy_scales, int32_t T,
+                            const uint8_t *w_codes, const float *w_scales, int32_t N, int32_t K,
+                            void *dx, int32_t dxdtype, void *stream);
+
+/* Workspace bytes moe_fp8_experts_matmul needs (0 for a few rows). */
+size_t moe_fp8_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_shared);
+
+/* The same products for rows grouped by expert: arguments, groups, `gather`, rows in no
+ * group and bad ids as in moe_mx4_experts_matmul. x: [A] 8-bit rows in the groups'
+ * order (gather == 0), or [T], one a token (gather == 1). */
+int moe_fp8_experts_matmul(const uint8_t *x_codes, const float *x_scales, int32_t T, int32_t k,
+                           int32_t E, int32_t has_shared, int32_t gather, const int32_t *offsets,
+                           const int32_t *perm, const uint8_t *w_codes, const float *w_scales,
+                           int32_t N, int32_t K, void *y, int32_t ydtype, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/* Workspace bytes moe_fp8_experts_matmul_backward needs. */
+size_t moe_fp8_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int32_t has_shared,
+                                                      int32_t K, int32_t gather);
+
+/* The gradient of moe_fp8_experts_matmul for its rows, as moe_mx4_experts_matmul_backward:
+ * dy: [A] 8-bit rows of N values in the groups' order; gather == 0: dx [A][K]; gather == 1:
+ * dx [T][K], the sum over the token's assignments in the order j = 0 .. k-1, then the
+ * shared expert's, kept in float32 in ws and rounded once. */
+int moe_fp8_experts_matmul_backward(const uint8_t *dy_codes, const float *dy_scales, int32_t T, int32_t k,
+                                    int32_t E, int32_t has_shared, int32_t gather,
+                                    const int32_t *offsets, const int32_t *slot_of,
+                                    const uint8_t *w_codes, const float *w_scales, int32_t N,
+                                    int32_t K, void *dx, int32_t dxdtype, void *ws, size_t ws_bytes,
+                                    void *stream);
+
+/* ---- RMS norm --------------------------------------------------------------------- */
+
+#define MOE_MAX_NORM_H 32768 /* values of a row of moe_rms_norm */
+
+/* The residual's addition and the root-mean-square norm in front of a router and its
+ * experts. Per row t of T:
+ *   r = x[t] + residual[t] (residual NULL: x[t]), in float32
+ *   total[t] = r, rounded once to dtype (total NULL: not written)
+ *   v = weight * r / sqrt(mean(r^2) + eps), from r before its rounding
+ *   y[t] = v rounded once to dtype (y NULL: not written)
+ *   codes[t], scales[t] = v as an 8-bit row, as moe_fp8_quantize writes it (both NULL: not)
+ * x, residual: [T][H], MOE_F32 or MOE_BF16, ldx and ldr elements from row to row; weight:
+ * [H], MOE_F32 or MOE_BF16 (wdtype); total, y: [T][H], rows H elements apart. One of total,
+ * y and codes at least is written. total may be x or residual themselves where their
+ * rows are H apart. Sums are float32 in a fixed order. A row whose squares
+ * pass float32's range has mean infinity and gives 0 (and NaN where r is infinite);
+ * a NaN makes its whole row NaN. H <= MOE_MAX_NORM_H, T <= 2^22 (else
+ * MOE_ERR_UNSUPPORTED), eps >= 0 and finite. T == 0: no launch. */
+int moe_rms_norm(const void *x, int32_t dtype, int64_t ldx, const void *residual, int64_t ldr,
+                 const void *weight, int32_t wdtype, float eps, int32_t T, int32_t H, void *total,
+                 void *y, uint8_t *codes, float *scales, void *stream);
+
+/* Workspace bytes moe_rms_norm_backward needs. */
+size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H);
+
+/* The gradients of the norm at the rows h (moe_rms_norm's total, or its x where there was no
+ * residual). With q = 1 / sqrt(mean(h^2) + eps) and dy the gradient of v (an 8-bit row passes
+ * its values' gradient straight through):
+ *   dh[t]   = d_total[t] + q (weight dy - h q^2 mean(weight dy h))   (d_total NULL: 0)
+ *   dweight = sum over t of dy h q
+ * dh is the gradient of x and of the residual alike. dy, h, d_total: [T][H] of `dtype`, ldd, ldh
+ * and ldt elements from row to row; dh: [T][H] of `dtype`; dweight: [H] float32. dweight NULL: only
+ * dh, no workspace. T == 0 writes dweight = 0. Sums are float32 in a fixed order. ws: at least
+ * moe_rms_norm_backward_workspace_size bytes (any content, 16-byte aligned); calls that
+ * overlap in time must not share it. */
+int moe_rms_norm_backward(const void *dy, int64_t ldd, const void *h, int64_t ldh, int32_t dtype,
+                          const void *weight, int32_t wdtype, const void *d_total, int64_t ldt,
+                          float eps, int32_t T, int32_t H, void *dh, float *dweight, void *ws,
+                          size_t ws_bytes, void *stream);
+
 /* ---- whole layer without allocation --------------------------------------- */
 
 /* Bytes of the library's own scratch array per GPU (moe_layer_static). */

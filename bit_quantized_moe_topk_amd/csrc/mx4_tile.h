@@ -88,8 +88,8 @@ __device__ inline int tile_group(const TilesOf<CAP>& t, int E_tot, int ti) {
   return lo;
 }
 
-// Item `id` of `items` (counted from the last group's end), strips of `strip` matrix rows.
-template <int TM = kTM, int CAP>
+// Item `id` of `items` (counted from the last group's end), strips of `strip` matrix rows; rows dealt in runs of RUN.
+template <int TM = kTM, int RUN = 32, int CAP>
 __device__ inline TileInfo tile_of(const TilesOf<CAP>& t, const Mx4Args& a, int id, int items, int strips, int strip) {
   TileInfo i;
   const int item = items - 1 - id, ti = item / strips;
@@ -102,8 +102,8 @@ __device__ inline TileInfo tile_of(const TilesOf<CAP>& t, const Mx4Args& a, int 
     j = ti - __builtin_amdgcn_readfirstlane((int)t.base[i.e]);
     of = (rows + TM - 1) / TM;
   }
-  const int runs = (rows + 31) / 32;
-  const int a0 = (int)((long long)j * runs / of) * 32, a1 = (int)((long long)(j + 1) * runs / of) * 32;
+  const int runs = (rows + RUN - 1) / RUN;
+  const int a0 = (int)((long long)j * runs / of) * RUN, a1 = (int)((long long)(j + 1) * runs / of) * RUN;
   i.s0 = r0 + a0;
   i.M = min(a1, rows) - a0;
   i.n0 = (item - ti * strips) * strip;

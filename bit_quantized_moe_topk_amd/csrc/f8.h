@@ -169,6 +169,7 @@ hipError_t launch_f8_quantize(const void* x, int xdtype, long long ld, int mats,
 hipError_t launch_f8_dequantize(const uint8_t* codes, const float* scales, int mats, int rows, int K, int block_rows,
                                 int ydtype, void* y, hipStream_t s);
 hipError_t launch_f8_product(const F8Args& a, hipStream_t s);
+bool f8_tiles_can(const F8Args& a);
 hipError_t launch_f8_tiles(F8Args a, hipStream_t s);
 
 }  // namespace moe

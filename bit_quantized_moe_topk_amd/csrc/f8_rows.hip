@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void rows_product(F8Args a) {
 }  // namespace
 
 hipError_t launch_f8_product(const F8Args& a, hipStream_t s) {
-  if (a.A >= (a.offsets ? 64 : 32)) return launch_f8_tiles(a, s);
+  if (a.A >= (a.offsets ? 64 : 32) && f8_tiles_can(a)) return launch_f8_tiles(a, s);
   const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.N + 15) / 16);
   if (a.back && a.exact) MOE_LAUNCH("f8_rows_back", s, (rows_product<true, true>), g, dim3(256), 0, s, a);
   else if (a.back) MOE_LAUNCH("f8_rows_back", s, (rows_product<true, false>), g, dim3(256), 0, s, a);

@@ -77,26 +77,18 @@ __device__ inline void f8_store_f32(const F8Args& a, const floatx4_t (&acc)[4], 
   }
 }
 
-template <bool EXACT>
-struct Frag {  // 32 codes of a lane, as its products take them
-  int8v_t v;
-  __device__ void set(const int8v_t& c) { v = c; }
-  __device__ static floatx4_t product(const Frag& a, const Frag& b) { return f8_products<false>(a.v, b.v); }
+// What a wave's products of a step read: 32 codes a lane of four runs of 16 matrix rows and of L runs of rows, and the
+// rows' scales.
+template <int L>
+struct Operands {
+  int8v_t w[4], x[L > 0 ? L : 1];
+  float s[L > 0 ? L : 1];
 };
-template <>
-struct Frag<true> {
-  bf16x8_t v[4];
-  __device__ void set(const int8v_t& c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f8_bf16(c[2 * i], c[2 * i + 1]);
-  }
-  __device__ static floatx4_t product(const Frag& a, const Frag& b) {
-    floatx4_t c = {};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
-    return c;
-  }
-};
+
+// A uniform value that no kernel of this launch writes, by a scalar load.
+__device__ inline float uniform_load(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
+}
 
 template <bool BACK, bool EXACT, int WN>
 __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
@@ -112,7 +104,7 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(buf), a) * strips;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, wn = wave % WN, wm = wave / WN;
-  const int P = max(a.xb, 2);  // (a contraction of one block has an empty second step)
+  const int P = max(a.xb, 3);  // (a short contraction has empty steps: loads run three ahead, into the next tile at most)
   const int stored = BACK ? a.K : a.N;
   Deal deal{items, (int)gridDim.x, a.counter, &slot, 0u};
   int item = deal.first();
@@ -120,29 +112,31 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   deal.ask();
   int next = deal.answer(item);
 
-  // load cursor: rows 16 wave + 8 u + l / 8 of the tile, the chunk that belongs at position l % 8; row 16 wave + l of the scales
-  const uint8_t *xp[2], *wp[kWL];
-  const float* sp;
+  // load cursor: rows 16 wave + 8 u + l / 8 of the tile, the chunk that belongs at position l % 8; row 16 wave + l % 16 of
+  // the scales; matrix rows 8 (WN wave + u) + l / 8, or the columns of a contraction row (offsets of a lane, bases of all)
+  uint32_t xoff[2], woff[kWL], soff;
+  const uint8_t* wbase;
   int lp = 0, row_next[3];
   auto row_of = [&](int u) { return u < 2 ? 16 * wave + 8 * u + (lane >> 3) : 16 * wave + r; };
   auto fetch_rows = [&](const TileInfo& t) {  // the row numbers of a tile, to be used later
 #pragma unroll
     for (int u = 0; u < 3; ++u) row_next[u] = max(mx4_row(a, t.s0 + min(row_of(u), t.M - 1)), 0);
   };
+  const uint32_t xrow = (uint32_t)a.xb * kF8Block, wrow = (uint32_t)a.wb * kF8Block;
+  auto turned_row = [&](int u) { return 16 * wave + 16 / kWL * u + lane / (4 * WN); };
   auto aim = [&](const TileInfo& t) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      xp[u] = static_cast<const uint8_t*>(a.x) + (size_t)row_next[u] * a.xb * kF8Block + 16 * ((lane & 7) ^ ((row_of(u) >> 1) & 7));
-    sp = a.xf + (size_t)row_next[2] * a.xb;
-    const uint8_t* w = a.wc + (size_t)t.e * stored * a.wb * kF8Block;
+    for (int u = 0; u < 2; ++u) xoff[u] = (uint32_t)row_next[u] * xrow + 16 * ((lane & 7) ^ ((row_of(u) >> 1) & 7));
+    soff = (uint32_t)row_next[2] * (uint32_t)a.xb * 4u;
+    wbase = a.wc + (size_t)t.e * stored * wrow;
 #pragma unroll
     for (int u = 0; u < kWL; ++u) {
       if constexpr (BACK) {  // (the row is added a step at a time: past the last, the last again, against codes of 0)
-        const int c = (16 * wave + 16 / kWL * u) + lane / (4 * WN), q = (lane % (4 * WN)) ^ (turned_at<WN>(c, 0) - c * 4 * WN);
-        wp[u] = w + 16 * (size_t)min(t.n0 / 16 + q, 8 * a.wb - 1);
+        const int c = turned_row(u), q = (lane % (4 * WN)) ^ (turned_at<WN>(c, 0) - c * 4 * WN);
+        woff[u] = 16u * (uint32_t)min(t.n0 / 16 + q, 8 * a.wb - 1);
       } else {
         const int n = 8 * (WN * wave + u) + (lane >> 3);
-        wp[u] = w + (size_t)min(t.n0 + n, a.N - 1) * a.wb * kF8Block + 16 * ((lane & 7) ^ ((n >> 1) & 7));
+        woff[u] = (uint32_t)min(t.n0 + n, a.N - 1) * wrow + 16 * ((lane & 7) ^ ((n >> 1) & 7));
       }
     }
     lp = 0;
@@ -151,15 +145,16 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
     Buf8<WN>& B = buf[b];
     const int p = min(lp, a.xb - 1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) stream16(xp[u] + (size_t)p * kF8Block, lds_offset(B.x) + 1024 * (2 * wave + u));
+    for (int u = 0; u < 2; ++u)
+      stream16(static_cast<const uint8_t*>(a.x) + p * kF8Block, xoff[u], lds_offset(B.x) + 1024 * (2 * wave + u));
 #pragma unroll
     for (int u = 0; u < kWL; ++u) {
-      size_t at = (size_t)p * kF8Block;
       if constexpr (BACK)
-        at = (size_t)min(p * kF8Block + 16 * wave + 16 / kWL * u + lane / (4 * WN), a.K - 1) * a.wb * kF8Block;
-      stream16(wp[u] + at, lds_offset(B.w) + 1024 * (kWL * wave + u));
+        stream16(wbase, woff[u] + (uint32_t)min(p * kF8Block + turned_row(u), a.K - 1) * wrow, lds_offset(B.w) + 1024 * (kWL * wave + u));
+      else
+        stream16(wbase + p * kF8Block, woff[u], lds_offset(B.w) + 1024 * (kWL * wave + u));
     }
-    if (lane < 16) stream4(sp + p, lds_offset(scale[b]) + 64 * wave);
+    if (lane < 16) stream4(a.xf + p, soff, lds_offset(scale[b]) + 64 * wave);
     ++lp;
   };
 
@@ -169,7 +164,10 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   aim(t);
   load(0);
   load(1);
-  step_done<kLoads>();
+  load(2);
+  // (what has landed where a tile begins: steps 0 and 1, or with EXACT step 0)
+  if (EXACT) step_done<2 * kLoads>();
+  else step_done<kLoads>();
   for (;;) {
     const bool more = next < items;
     if (more) {
@@ -188,58 +186,125 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
     for (int i = 0; i < kRuns; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = floatx4_t{};
+    // one loop for each number of live runs (a switch inside the loop makes the compiler move accumulators)
     auto run = [&](auto LL) __attribute__((always_inline)) {
       constexpr int L = decltype(LL)::value;
-      for (int p = 0; p < P; ++p) {
-        const int b2 = b == 0 ? 2 : b - 1;  // the buffer of the step before, which every wave has left
-        const bool loads = p + 2 < P || more;
-        if (p + 2 == P && more) aim(tn);
-        if (loads) load(b2);
-        if (L > 0 && p < a.xb) {
-          const Buf8<WN>& B = buf[b];
-          const float sw = ws[(size_t)p * wstep];
-          Frag<EXACT> w[4];
-          float s[L > 0 ? L : 1];
+      auto read_scales = [&](Operands<L>& o, int at) __attribute__((always_inline)) {
 #pragma unroll
-          for (int i = 0; i < L; ++i) s[i] = scale[b][kRun * (run0 + i) + r];
+        for (int i = 0; i < L; ++i) o.s[i] = scale[at][kRun * (run0 + i) + r];
+      };
+      auto read_w = [&](Operands<L>& o, int at, int j) __attribute__((always_inline)) {
+        const Buf8<WN>& B = buf[at];
+        if constexpr (BACK) {
+          typedef int v2i __attribute__((ext_vector_type(2)));
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int c = 32 * g + 8 * z + (r >> 1);
+            const char* from = reinterpret_cast<const char*>(B.w + turned_at<WN>(c, 4 * wn + j)) + 8 * (r & 1);
+            const v2i u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (__attribute__((address_space(3))) v2i*)(__attribute__((address_space(3))) char*)const_cast<char*>(from));
+            o.w[j][2 * z] = u[0];
+            o.w[j][2 * z + 1] = u[1];
+          }
+        } else {
+          const int n = 64 * wn + 16 * j + r;
+          o.w[j] = f8_pair(B.w[chunk_at(n, 2 * g)], B.w[chunk_at(n, 2 * g + 1)]);
+        }
+      };
+      auto read_x = [&](Operands<L>& o, int at, int i) __attribute__((always_inline)) {
+        const int m = kRun * (run0 + i) + r;
+        o.x[i] = f8_pair(buf[at].x[chunk_at(m, 2 * g)], buf[at].x[chunk_at(m, 2 * g + 1)]);
+      };
+      float sw = 0.f;
+      const float* wp = ws;
+      // Step p, while the next step's operands take the places of those that are used up and the load three steps on is
+      // on its way. A block's sum is brought into its accumulator two products later, when it is there.
+      Operands<L> o;
+      auto step = [&](int p, bool loads) __attribute__((always_inline)) {
+        const int b1 = b == 2 ? 0 : b + 1;
+        float f[L > 0 ? L : 1];
+#pragma unroll
+        for (int i = 0; i < L; ++i) f[i] = p < a.xb ? o.s[i] * sw : 0.f;
+        if (loads) load(b);
+        if constexpr (L > 0) {
+          if (p + 1 < a.xb) wp += wstep;
+          sw = uniform_load(wp);
+          read_scales(o, b1);
+          __builtin_amdgcn_sched_barrier(0);
+          floatx4_t c[3];
+#pragma unroll
+          for (int k = 0; k < 4 * L + 2; ++k) {
+            if (k < 4 * L) c[k % 3] = f8_products<false>(o.w[k % 4], o.x[k / 4]);
+            if (k < 4 * L && k >= 4 * L - 4) read_w(o, b1, k % 4);
+            if (k < 4 * L && k % 4 == 3) read_x(o, b1, k / 4);
+            if (k >= 2) {
+              const int i = (k - 2) / 4, j = (k - 2) % 4;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) acc[i][j][z] = fmaf(c[(k - 2) % 3][z], f[i], acc[i][j][z]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        // the loads of the step after next have landed; this step's may be in flight
+        if (loads) step_done<kLoads>();
+        else step_done();
+        b = b1;
+      };
+      // The same with bf16 products: codes become bf16 as they are read, which leaves no registers for a second set; the
+      // step's buffer is loaded again when every wave has read it.
+      auto step_exact = [&](int p) __attribute__((always_inline)) {
+        if (L > 0 && p < a.xb) {
+          read_scales(o, b);
+          const float swp = uniform_load(wp);
+          wp += wstep;
+          bf16x8_t w[4][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if constexpr (BACK) {
-              typedef int v2i __attribute__((ext_vector_type(2)));
-              int8v_t v;
+            read_w(o, b, j);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const int c = 32 * g + 8 * z + (r >> 1);
-                const char* from = reinterpret_cast<const char*>(B.w + turned_at<WN>(c, 4 * wn + j)) + 8 * (r & 1);
-                const v2i u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (__attribute__((address_space(3))) v2i*)(__attribute__((address_space(3))) char*)const_cast<char*>(from));
-                v[2 * z] = u[0];
-                v[2 * z + 1] = u[1];
-              }
-              w[j].set(v);
-            } else {
-              const int n = 64 * wn + 16 * j + r;
-              w[j].set(f8_pair(B.w[chunk_at(n, 2 * g)], B.w[chunk_at(n, 2 * g + 1)]));
-            }
+            for (int z = 0; z < 4; ++z) w[j][z] = f8_bf16(o.w[j][2 * z], o.w[j][2 * z + 1]);
           }
 #pragma unroll
           for (int i = 0; i < L; ++i) {
-            Frag<EXACT> x;
-            const int m = kRun * (run0 + i) + r;
-            x.set(f8_pair(B.x[chunk_at(m, 2 * g)], B.x[chunk_at(m, 2 * g + 1)]));
-            const float f = s[i] * sw;
+            read_x(o, b, i);
+            bf16x8_t x[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) x[z] = f8_bf16(o.x[i][2 * z], o.x[i][2 * z + 1]);
+            const float f = o.s[i] * swp;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const floatx4_t c = Frag<EXACT>::product(w[j], x);
+              floatx4_t c = {};
+#pragma unroll
+              for (int z = 0; z < 4; ++z) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][z], x[z], c, 0, 0, 0);
 #pragma unroll
               for (int z = 0; z < 4; ++z) acc[i][j][z] = fmaf(c[z], f, acc[i][j][z]);
             }
           }
         }
-        // the next step's loads have landed; this iteration's may be in flight
-        if (loads) step_done<kLoads>();
+        if (p + 2 < P || more) step_done<kLoads>();
         else step_done();
+        if (p + 3 == P && more) aim(tn);
+        if (p + 3 < P || more) load(b);
         b = b == 2 ? 0 : b + 1;
+      };
+      if constexpr (EXACT) {
+        for (int p = 0; p < P; ++p) step_exact(p);
+      } else {
+        if constexpr (L > 0) {
+          sw = uniform_load(wp);
+          read_scales(o, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) read_w(o, b, j);
+#pragma unroll
+          for (int i = 0; i < L; ++i) read_x(o, b, i);
+        }
+        // every wave has read its first operands before their buffer is loaded again
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma nounroll
+        for (int p = 0; p < P - 3; ++p) step(p, true);
+        if (more) aim(tn);
+#pragma nounroll
+        for (int p = P - 3; p < P; ++p) step(p, more);
       }
     };
     if (live == 4) run(std::integral_constant<int, kRuns < 4 ? 0 : 4>{});
@@ -262,6 +327,12 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
 }
 
 }  // namespace
+
+// Offsets within the rows and within one matrix are 32 bits wide.
+bool f8_tiles_can(const F8Args& a) {
+  const long long rows = a.perm ? a.T : a.A, stored = a.back ? a.K : a.N;
+  return rows * a.xb * kF8Block < (1LL << 32) && stored * a.wb * kF8Block < (1LL << 32);
+}
 
 hipError_t launch_f8_tiles(F8Args a, hipStream_t s) {
   constexpr int strip = 256;

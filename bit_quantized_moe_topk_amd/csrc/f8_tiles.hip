@@ -27,11 +27,14 @@ struct Buf8 {
   uint4 w[64 * WN * 8];    // matrix row n likewise; turned: contraction row c, its 4 WN chunks of 16 columns (turned_at)
 };
 
+// A lane's 32 codes of a row of 128 are chunks g and g + 4, g = l / 16. (A 16-byte read serves lanes 0-3, 12-15 and 20-27 at
+// once, and so on: with chunks g and g + 1 beside one another those hit all banks once, with 2 g and 2 g + 2 twice, which
+// took 8 cycles a read instead of 4.)
 // Place of chunk q of contraction row c: the eight rows that 16 lanes read take different banks, and so do
-// the rows 32 further on that the next 16 lanes read.
+// the rows 16 further on that the next 16 lanes read.
 template <int WN>
 __device__ inline int turned_at(int c, int q) {
-  return c * (4 * WN) + (q ^ (WN >= 4 ? (c & 7) | ((c >> 2) & 8) : (c & 7)));
+  return c * (4 * WN) + (q ^ (WN >= 4 ? (c & 7) | (((c >> 4) ^ (c >> 5)) & 1) << 3 : (c & 7)));
 }
 
 __device__ inline void f8_store_bf16(const F8Args& a, const floatx4_t (&acc)[4], int row, bool there, int n0, bool wide) {
@@ -199,7 +202,7 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
           typedef int v2i __attribute__((ext_vector_type(2)));
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
-            const int c = 32 * g + 8 * z + (r >> 1);
+            const int c = 16 * g + 8 * (z & 1) + 64 * (z >> 1) + (r >> 1);
             const char* from = reinterpret_cast<const char*>(B.w + turned_at<WN>(c, 4 * wn + j)) + 8 * (r & 1);
             const v2i u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
                 (__attribute__((address_space(3))) v2i*)(__attribute__((address_space(3))) char*)const_cast<char*>(from));
@@ -208,12 +211,12 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
           }
         } else {
           const int n = 64 * wn + 16 * j + r;
-          o.w[j] = f8_pair(B.w[chunk_at(n, 2 * g)], B.w[chunk_at(n, 2 * g + 1)]);
+          o.w[j] = f8_pair(B.w[chunk_at(n, g)], B.w[chunk_at(n, g + 4)]);
         }
       };
       auto read_x = [&](Operands<L>& o, int at, int i) __attribute__((always_inline)) {
         const int m = kRun * (run0 + i) + r;
-        o.x[i] = f8_pair(buf[at].x[chunk_at(m, 2 * g)], buf[at].x[chunk_at(m, 2 * g + 1)]);
+        o.x[i] = f8_pair(buf[at].x[chunk_at(m, g)], buf[at].x[chunk_at(m, g + 4)]);
       };
       float sw = 0.f;
       const float* wp = ws;

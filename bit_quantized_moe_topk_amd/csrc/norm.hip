@@ -27,15 +27,20 @@ struct NormArgs {
   bool vin, vout, vw;  // 16 bytes at a time: rows that come in, rows that go out, the weight
 };
 
+__device__ inline double wave_sum(double v) {
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
 // Sums of N values over the W waves of a row, the same in each.
-template <int W, int N>
-__device__ inline void row_sums(float (&v)[N], float (*mem)[N], int& turn) {
+template <int W, int N, typename F>
+__device__ inline void row_sums(F (&v)[N], F (*mem)[N], int& turn) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (W > 1) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, first = wave / W * W;
     constexpr int kWaves = W < 4 ? 4 : W;
-    float(*m)[N] = mem + (turn & 1) * kWaves;
+    F(*m)[N] = mem + (turn & 1) * kWaves;
     turn ^= 1;  // (the next row's sums go elsewhere: one barrier a row)
     if (lane == 0)
 #pragma unroll
@@ -43,12 +48,19 @@ __device__ inline void row_sums(float (&v)[N], float (*mem)[N], int& turn) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float s = m[first][i];
+      F s = m[first][i];
 #pragma unroll
       for (int w = 1; w < W; ++w) s += m[first + w][i];
       v[i] = s;
     }
   }
+}
+
+// 1 / sqrt(m) in 64 bits: one step from the 32-bit instruction's, where that holds.
+__device__ inline double inverse_root(double m) {
+  if (!(m > 0x1p-100 && m < 0x1p100)) return 1.0 / sqrt(m);
+  const double y = __builtin_amdgcn_rsqf((float)m);
+  return y * (1.5 - 0.5 * m * y * y);
 }
 
 constexpr int threads_of(int W) { return W < 4 ? 256 : 64 * W; }
@@ -75,7 +87,7 @@ __device__ inline void load_weight(const NormArgs& a, float (&w)[C][8]) {
 template <bool BF, int C, int W>
 __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
   typedef Place<C, W> P;
-  __shared__ float mem[2 * (W < 4 ? 4 : W)][1];
+  __shared__ double mem[2 * (W < 4 ? 4 : W)][1];
   constexpr int kSize = BF ? 2 : 4;
   const int nb = f8_blocks(a.H);
   float w[C][8];
@@ -84,7 +96,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
   for (int t0 = blockIdx.x * P::kRowsAtOnce; t0 < a.T; t0 += gridDim.x * P::kRowsAtOnce) {
     const int t = t0 + P::row();
     const bool there = t < a.T;
-    float f[C][8], sum[1] = {0.f};
+    float f[C][8], part = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -101,17 +113,24 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
         if (a.total) store8<BF>(static_cast<char*>(a.total) + (size_t)t * a.H * kSize, col, a.H, a.vout, f[c]);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[0] = fmaf(f[c][i], f[c][i], sum[0]);
+      for (int i = 0; i < 8; ++i) part = fmaf(f[c][i], f[c][i], part);
     }
+    // From a lane's sum on in 64 bits, and the factor as two 32-bit parts: a value is off by its last rounding, and a
+    // block's scale hardly ever, which leaves a few codes in a million on the other side of a border.
+    double sum[1] = {part};
     row_sums<W, 1>(sum, mem, turn);
-    const float q = 1.f / sqrtf(sum[0] / (float)a.H + a.eps);
+    const double root = inverse_root(sum[0] / a.H + (double)a.eps);
+    const float q = (float)root, ql = fabsf(q) < INFINITY ? (float)(root - (double)q) : 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int col = P::col(c);
       if (!there || col >= nb * kF8Block) continue;
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = f[c][i] * q * w[c][i];
+      for (int i = 0; i < 8; ++i) {
+        const float u = f[c][i] * q;
+        v[i] = fmaf(u, w[c][i], fmaf(f[c][i], ql, fmaf(f[c][i], q, -u)) * w[c][i]);
+      }
       if (a.y) store8<BF>(static_cast<char*>(a.y) + (size_t)t * a.H * kSize, col, a.H, a.vout, v);
       if (a.codes) {
         // past the row's end there is nothing, whatever q is
@@ -173,7 +192,22 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
     }
   }
   if (!a.part) return;
-  float* part = a.part + (size_t)(blockIdx.x * P::kRowsAtOnce + P::row()) * a.H;
+  // the workgroup's rows in flight, then its part
+  if constexpr (P::kRowsAtOnce > 1) {
+    __shared__ __attribute__((aligned(16))) float rows[P::kRowsAtOnce - 1][8 * 64 * W * C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (P::row() > 0) store8<false>(rows[P::row() - 1], P::col(c), 1 << 30, true, dw[c]);
+    __syncthreads();
+    if (P::row() > 0) return;
+#pragma unroll
+    for (int z = 0; z + 1 < P::kRowsAtOnce; ++z)
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[c][i] += rows[z][P::col(c) + i];
+  }
+  float* part = a.part + (size_t)blockIdx.x * a.H;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = P::col(c);
@@ -181,19 +215,24 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
   }
 }
 
-// dweight[h] = the sum of n parts, 64 columns a workgroup, 16 runs of parts side by side.
+// dweight[h] = the sum of n parts, 32 columns a workgroup, 32 runs of parts side by side, eight loads at once.
 __global__ __launch_bounds__(1024) void norm_parts(const float* __restrict__ part, int n, int H, float* __restrict__ dw) {
-  __shared__ float sums[16][64];
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
+  __shared__ float sums[32][33];
+  const int c = threadIdx.x & 31, run = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+  const int per = (n + 31) / 32, end = min(n, (run + 1) * per);
   float s = 0.f;
-  const int per = (n + 15) / 16;
-  if (col < H)
-    for (int i = run * per; i < min(n, (run + 1) * per); ++i) s += part[(size_t)i * H + col];
-  sums[run][lane] = s;
+  for (int i = run * per; i < end && col < H; i += 8) {
+    float v[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) v[z] = part[(size_t)min(i + z, end - 1) * H + col];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) s += i + z < end ? v[z] : 0.f;
+  }
+  sums[run][c] = s;
   __syncthreads();
   if (run || col >= H) return;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) s += sums[i][lane];
+  for (int i = 1; i < 32; ++i) s += sums[i][c];
   dw[col] = s;
 }
 
@@ -211,7 +250,7 @@ Shape shape_of(int T, int H) {
   return s;
 }
 
-constexpr int kParts = 1024;
+constexpr int kParts = 512;  // most workgroups of the gradient: each leaves a row of parts
 int rows_at_once(const Shape& s) { return s.W < 4 ? 4 / s.W : 1; }
 int grid_of(int T, const Shape& s, int most) {
   const int n = (T + rows_at_once(s) - 1) / rows_at_once(s);
@@ -227,7 +266,7 @@ bool all_vec(const void* p, long long ld, int size) { return !p || rows_vec(p, l
 
 size_t norm_workspace_bytes(int T, int H) {
   const Shape s = shape_of(T, H);
-  return sizeof(float) * (size_t)H * grid_of(T, s, kParts / rows_at_once(s)) * rows_at_once(s);
+  return sizeof(float) * (size_t)H * grid_of(T, s, kParts);
 }
 
 hipError_t launch_norm(const void* x, int dtype, long long ldx, const void* residual, long long ldr, const void* weight,
@@ -262,7 +301,7 @@ hipError_t launch_norm_backward(const void* dy, long long ldd, const void* h, lo
   a.vout = all_vec(dh, H, size);
   a.vw = rows_vec(weight, 0, 2);
   const Shape f = shape_of(T, H);
-  const dim3 g(grid_of(T, f, kParts / rows_at_once(f)));
+  const dim3 g(grid_of(T, f, kParts));
   if (T > 0) {
 #define BACKWARD(BF, CC, WW) \
   if ((dtype == 1) == BF && f.C == CC && f.W == WW) \
@@ -272,8 +311,7 @@ hipError_t launch_norm_backward(const void* dy, long long ldd, const void* h, lo
 #undef BACKWARD
   }
   if (dweight)
-    MOE_LAUNCH("norm_parts", s, norm_parts, dim3((H + 63) / 64), dim3(1024), 0, s, a.part,
-               T > 0 ? (int)g.x * rows_at_once(f) : 0, H, dweight);
+    MOE_LAUNCH("norm_parts", s, norm_parts, dim3((H + 31) / 32), dim3(1024), 0, s, a.part, T > 0 ? (int)g.x : 0, H, dweight);
   return hipGetLastError();
 }
 

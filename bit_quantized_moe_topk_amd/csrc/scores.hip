@@ -2,8 +2,18 @@
 // selection alone, groups of experts, top-k and gates, and the gates' gradient
 // for the logits.
 //
-// One wave a token. What is ranked (score + bias) is held in 64 bits: in 32,
-// two experts a last place apart would come in the order of their roundings.
+// One wave a token, expert lane + 64 i in slot i. The order is that of values in
+// 64 bits (score + bias): in 32, two experts a last place apart would come in the
+// order of their roundings. But 64 bits for all 512 experts of 8,192 tokens took 55 us.
+// So scores are computed in 32 first, which with a bias are off by less than a
+// margin; what is not within it of a border is settled:
+//   groups  : their values in 32 bits, unless the last that stays and the first that
+//             goes are near each other; then those of each group's best two in 64.
+//   experts : all within the margin of a lower bound of the k-th (topk.h's threshold)
+//             are candidates, one a lane, whose values are computed in 64 bits at
+//             once and ranked by counting. Without a bias the logits are the order.
+// What remains (over 64 candidates or ranks; a third expert of a group near its
+// second where groups are near) goes through 64 bits for all experts and k rounds.
 #include "gemv.h"
 #include "norm.h"
 #include "topk.h"
@@ -18,60 +28,91 @@ __device__ inline uint64_t orderable64(double v) {
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 constexpr uint64_t kOff = 0x000FFFFFFFFFFFFFull;  // -inf's code
+constexpr uint32_t kOff32 = 0x007FFFFFu;          // and the one of orderable()
 __device__ inline double from_orderable64(uint64_t o) {
   return __longlong_as_double((o >> 63) ? (o & 0x7FFFFFFFFFFFFFFFull) : ~o);
 }
 
-__device__ inline double wave_max64(double v) {
-  for (int o = 32; o > 0; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
-  return v;
-}
 __device__ inline double wave_sum64(double v) {
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
+__device__ inline float wave_maxf(float v) { return from_orderable(wave_reduce<true>(orderable(v))); }
 
 __device__ inline float logit_at(const ScoreArgs& a, int t, int e) {
   const size_t at = (size_t)t * a.ld + e;
   return a.bf16 ? bf16_lo(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
 }
 
+// What a softmax needs of its row: the largest logit (NaN of a row with a NaN, -inf of one that is all off) and
+// the sum of exponentials (1 where only their ratios matter).
+struct Base {
+  float top;
+  double total;
+};
+__device__ inline double score64(const ScoreArgs& a, const Base& b, float l) {
+  if (!a.softmax) return 1.0 / (1.0 + exp(-(double)l));
+  return b.top == -INFINITY ? 0.0 : exp((double)l - (double)b.top) / b.total;
+}
+// The same in 32 bits, within 2^-21 (and of a sigmoid relative to its value, down to 2^-126).
+__device__ inline float score32(const ScoreArgs& a, const Base& b, float l) {
+  if (!a.softmax) return __builtin_amdgcn_rcpf(1.f + expf(-l));
+  return b.top == -INFINITY ? 0.f : expf(l - b.top) * __builtin_amdgcn_rcpf((float)b.total);
+}
+
+// The sum of a row's exponentials in 64 bits.
+template <int P>
+__device__ inline double total64(const float (&l)[P], int E, float top) {
+  double v = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < P; ++i) {
+    float x = l[0];
+#pragma unroll
+    for (int z = 1; z < P; ++z) x = i == z ? l[z] : x;
+    if ((int)(threadIdx.x & 63) + 64 * i < E) v += top == -INFINITY ? 0.0 : exp((double)x - (double)top);
+  }
+  return wave_sum64(v);
+}
+
 constexpr int kWaves = 4;  // tokens per workgroup
 
 template <int P>
-__global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
-  __shared__ double values[kWaves][64 * P];
-  __shared__ uint64_t keys[kWaves][64 * P];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x * kWaves + wave;
-  if (t >= a.T) return;
-  double s[P];
-  uint64_t key[P];
-  float l[P];
-#pragma unroll
-  for (int i = 0; i < P; ++i) l[i] = logit_at(a, t, min(lane + 64 * i, a.E - 1));
-  double top = -INFINITY, total = 0.0;
-  if (a.softmax) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) top = fmax(top, (double)l[i]);
-    top = wave_max64(top);
-    bool nan = false;  // (a maximum leaves it out)
-#pragma unroll
-    for (int i = 0; i < P; ++i) nan |= l[i] != l[i];
-    if (__any(nan)) top = NAN;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (lane + 64 * i < a.E) total += top == -INFINITY ? 0.0 : exp((double)l[i] - top);
-    total = wave_sum64(total);
+struct Scratch {
+  union {
+    uint64_t key[64 * P];  // 64 bits for all experts
+    float row[64 * P];     // what ranks an expert within its group
+  };
+  uint32_t head[64];
+  uint64_t cand[64];
+  float l[64], b[64];
+  int e[64];
+};
+
+// The groups whose value (order code v of group lane) is among the `keep` largest, a bit each.
+template <typename V>
+__device__ inline uint64_t kept_groups(const ScoreArgs& a, V v, bool* stays) {
+  const int lane = threadIdx.x & 63;
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const V o = __shfl(v, g, 64);
+    rank += o > v || (o == v && g < lane);
   }
+  *stays = lane < a.groups && rank < a.keep;
+  return __ballot(*stays);
+}
+
+// 64 bits for all experts: groups by scanning them, then k rounds.
+template <int P>
+__device__ inline void select64(const ScoreArgs& a, int t, const float (&l)[P], const float (&bias)[P], Base base,
+                                Scratch<P>& sc) {
+  const int lane = threadIdx.x & 63;
+  if (a.softmax) base.total = total64<P>(l, a.E, base.top);
+  uint64_t key[P];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = lane + 64 * i;
-    s[i] = !a.softmax ? 1.0 / (1.0 + exp(-(double)l[i])) : top == -INFINITY ? 0.0 : exp((double)l[i] - top) / total;
-    double c = !a.bias ? (double)l[i] : s[i] + (double)a.bias[min(e, a.E - 1)];
-    if (l[i] == -INFINITY) c = -INFINITY;
-    key[i] = e < a.E ? orderable64(c) : 0ull;
-    values[wave][e] = s[i];
-    keys[wave][e] = key[i];
+    const double c = l[i] == -INFINITY ? -INFINITY : a.bias ? score64(a, base, l[i]) + (double)bias[i] : (double)l[i];
+    key[i] = lane + 64 * i < a.E ? orderable64(c) : 0ull;
+    sc.key[lane + 64 * i] = key[i];
   }
   __builtin_amdgcn_wave_barrier();
   if (a.groups > 1) {
@@ -79,107 +120,308 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     uint64_t mine = 0;
     if (lane < a.groups) {
       uint64_t k1 = kOff, k2 = kOff;  // what is not above -inf is left out
-      int e1 = 0, e2 = 0;
       for (int e = lane * size; e < (lane + 1) * size; ++e) {
-        const uint64_t k = keys[wave][e];
-        if (k > k1) {
-          k2 = k1;
-          e2 = e1;
-          k1 = k;
-          e1 = e;
-        } else if (k > k2) {
-          k2 = k;
-          e2 = e;
-        }
+        const uint64_t k = sc.key[e];
+        k2 = k > k1 ? k1 : k > k2 ? k : k2;
+        k1 = k > k1 ? k : k1;
       }
       mine = k1;
       if (a.group_top == 2 && k1 > kOff) {
-        const double v1 = a.bias ? from_orderable64(k1) : values[wave][e1];
-        const double v2 = k2 == kOff ? 0.0 : a.bias ? from_orderable64(k2) : values[wave][e2];
+        double v1 = from_orderable64(k1), v2 = k2 == kOff ? 0.0 : from_orderable64(k2);
+        if (!a.bias) {
+          v1 = score64(a, base, (float)v1);
+          if (k2 != kOff) v2 = score64(a, base, (float)v2);
+        }
         mine = orderable64(v1 + v2);
       }
     }
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t o = __shfl(mine, g, 64);
-      rank += o > mine || (o == mine && g < lane);
-    }
-    const uint64_t kept = __ballot(lane < a.groups && rank < a.keep);
+    bool stays;
+    const uint64_t kept = kept_groups(a, mine, &stays);
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane + 64 * i < a.E && !(kept >> ((lane + 64 * i) / size) & 1)) key[i] = 0ull;
   }
   double sum = 0.0;
+  int mine = 0;
+  float logit = 0.f;  // of rank `lane`
   for (int j = 0; j < a.k; ++j) {
     uint64_t best = key[0];
     int e = lane;
+    float x = l[0];
 #pragma unroll
     for (int i = 1; i < P; ++i)
       if (key[i] > best) {
         best = key[i];
         e = lane + 64 * i;
+        x = l[i];
       }
     for (int o = 32; o > 0; o >>= 1) {
       const uint64_t ob = __shfl_xor(best, o, 64);
       const int oe = __shfl_xor(e, o, 64);
+      const float ox = __shfl_xor(x, o, 64);
       if (ob > best || (ob == best && oe < e)) {
         best = ob;
         e = oe;
+        x = ox;
       }
     }
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane + 64 * i == e) key[i] = 0ull;
-    if (lane == 0) a.idx[(size_t)t * a.k + j] = e;
-    sum += values[wave][e];
+    if (lane == (j & 63)) mine = e;
+    if (lane == j) logit = x;
+    sum += score64(a, base, x);
+    if ((j & 63) == 63 || j + 1 == a.k) {
+      const int r = (j & ~63) + lane;
+      if (r <= j) a.idx[(size_t)t * a.k + r] = mine;
+    }
+    if (j >= 64 && lane == 0) a.gates[(size_t)t * a.k + j] = x;  // its logit, until the sum is known
   }
-  __threadfence_block();
-  for (int j = lane; j < a.k; j += 64) {
-    const double v = values[wave][a.idx[(size_t)t * a.k + j]];
-    a.gates[(size_t)t * a.k + j] = (float)((double)a.scale * (!a.renorm ? v : sum == 0.0 ? 0.0 : v / sum));
-  }
+  auto gate = [&](float x) {
+    const double v = score64(a, base, x);
+    return (float)((double)a.scale * (!a.renorm ? v : sum == 0.0 ? 0.0 : v / sum));
+  };
+  if (lane < a.k) a.gates[(size_t)t * a.k + lane] = gate(logit);
+  for (int j = 64; j < a.k; ++j)  // (lane 0 reads what it wrote)
+    if (lane == 0) a.gates[(size_t)t * a.k + j] = gate(a.gates[(size_t)t * a.k + j]);
 }
 
+// The three largest of a group's ranking values, the first two with their places.
+struct Top3 {
+  float v1, v2, v3;
+  int e1, e2;
+  __device__ void add(float v, int e) {
+    const bool g1 = v > v1, g2 = v > v2;
+    v3 = g2 ? v2 : fmaxf(v3, v);
+    v2 = g1 ? v1 : g2 ? v : v2;
+    e2 = g1 ? e1 : g2 ? e : e2;
+    v1 = g1 ? v : v1;
+    e1 = g1 ? e : e1;
+  }
+};
+
 template <int P>
-__global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a) {
-  __shared__ float row[kWaves][64 * P];
+__global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
+  __shared__ Scratch<P> scratch[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x * kWaves + wave;
   if (t >= a.T) return;
-  const int32_t* idx = a.idx + (size_t)t * a.k;
-  const float* dg = a.d_gates + (size_t)t * a.k;
+  Scratch<P>& sc = scratch[wave];
+  float l[P], bias[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) row[wave][lane + 64 * i] = 0.f;
-  // the scores' base: over the row, or with renorm over what was selected
-  float top = -INFINITY, total = 0.f, l[P];
-  bool nan = false;  // (a maximum leaves it out)
-  if (a.softmax && !a.renorm) {
+  for (int i = 0; i < P; ++i) l[i] = logit_at(a, t, min(lane + 64 * i, a.E - 1));
+#pragma unroll
+  for (int i = 0; i < P; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, a.E - 1)] : 0.f;
+  Base base{0.f, 1.0};
+  if (a.softmax) {
+    float top = -INFINITY;
+    bool nan = false;  // (a maximum leaves it out)
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      l[i] = lane + 64 * i < a.E ? logit_at(a, t, lane + 64 * i) : -INFINITY;
       top = fmaxf(top, l[i]);
       nan |= l[i] != l[i];
     }
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    if (__any(nan)) top = NAN;
+    top = wave_maxf(top);
+    base.top = __any(nan) || top == INFINITY ? NAN : top;  // (such a row has no scores)
+    if (a.bias || !a.renorm || base.top != base.top) {
+      float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) total += top == -INFINITY ? 0.f : expf(l[i] - top);
-    total = wave_sum(total);
-  } else if (a.softmax) {
-    for (int j = lane; j < a.k; j += 64)
-      if ((unsigned)idx[j] < (unsigned)a.E) {
-        const float v = logit_at(a, t, idx[j]);
-        top = fmaxf(top, v);
-        nan |= v != v;
+      for (int i = 0; i < P; ++i)
+        if (lane + 64 * i < a.E) v += base.top == -INFINITY ? 0.f : expf(l[i] - base.top);
+      base.total = wave_sum(v);
+    }
+  }
+  // what ranks an expert: its logit, or score + bias in 32 bits
+  float c[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) c[i] = l[i] == -INFINITY || !a.bias ? l[i] : score32(a, base, l[i]) + bias[i];
+  const int size = a.E / a.groups;
+  uint64_t kept = ~0ull;
+  bool hard = a.k > 64;
+  if (a.groups > 1 && a.keep < a.groups && !hard) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (lane + 64 * i < a.E) sc.row[lane + 64 * i] = c[i];
+    __builtin_amdgcn_wave_barrier();
+    int per = 64;  // lanes a group, which share its experts
+    while (per * a.groups > 64) per >>= 1;
+    const int g = lane / per;
+    Top3 top{-INFINITY, -INFINITY, -INFINITY, 0, 0};  // (what is not above -inf is left out, NaN too)
+    if (g < a.groups)
+      for (int e = g * size + lane % per; e < (g + 1) * size; e += per) top.add(sc.row[e], e);
+    for (int o = 1; o < per; o <<= 1) {
+      const Top3 u{__shfl_xor(top.v1, o, 64), __shfl_xor(top.v2, o, 64), __shfl_xor(top.v3, o, 64), __shfl_xor(top.e1, o, 64),
+                   __shfl_xor(top.e2, o, 64)};
+      top.add(u.v1, u.e1);
+      top.add(u.v2, u.e2);
+      top.v3 = fmaxf(top.v3, fminf(u.v3, top.v2));
+    }
+    // group `lane`'s
+    const int from = lane < a.groups ? lane * per : 0;
+    top = Top3{__shfl(top.v1, from, 64), __shfl(top.v2, from, 64), __shfl(top.v3, from, 64), __shfl(top.e1, from, 64),
+               __shfl(top.e2, from, 64)};
+    const bool live = top.v1 > -INFINITY, two = a.group_top == 2 && top.v2 > -INFINITY;
+    float v = top.v1, margin = 0.f;
+    if (a.bias || a.group_top == 2) {
+      if (!a.bias) v = live ? score32(a, base, top.v1) : v;
+      if (two) v += a.bias ? top.v2 : score32(a, base, top.v2);
+      margin = a.bias ? 0x1p-18f + 0x1p-21f * fabsf(v) : fmaxf(0x1p-19f * v, 0x1p-126f);
+    }
+    bool stays;
+    kept = kept_groups(a, orderable(v), &stays);
+    // the least that stays and the most that goes
+    const float lo = from_orderable(wave_reduce<false>(stays ? orderable(v) : 0xFFFFFFFFu));
+    const float hi = wave_maxf(lane < a.groups && !stays ? v : -INFINITY);
+    const float most = wave_maxf(lane < a.groups && live ? margin : 0.f);
+    if (most > 0.f && hi > -INFINITY && !(lo - hi >= 2.f * most)) {
+      const float apart = a.bias ? 0x1p-18f + 0x1p-21f * fabsf(top.v2) : 0.f;
+      hard = __any(lane < a.groups && two && a.bias && top.v3 > -INFINITY && !(top.v2 - top.v3 >= apart)) || !(hi < INFINITY);
+      if (!hard) {
+        Base exact = base;
+        if (a.softmax && a.bias) exact.total = total64<P>(l, a.E, base.top);
+        double w = -INFINITY;
+        if (lane < a.groups && live) {
+          w = a.bias ? score64(a, exact, logit_at(a, t, top.e1)) + (double)a.bias[top.e1] : score64(a, exact, top.v1);
+          if (two) w += a.bias ? score64(a, exact, logit_at(a, t, top.e2)) + (double)a.bias[top.e2] : score64(a, exact, top.v2);
+        }
+        kept = kept_groups(a, lane < a.groups ? orderable64(w) : 0ull, &stays);
+        // the best of a group in 32 bits need not be so in 64, where two of them alone are near
+        if (a.group_top == 1) hard = __any(lane < a.groups && a.bias && top.v2 > -INFINITY && !(top.v1 - top.v2 >= apart + margin));
       }
-    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    if (__any(nan)) top = NAN;
-    total = 1.f;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  uint32_t key[P], head = 0u;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = e < a.E && (a.groups == 1 || (kept >> (e / size) & 1)) ? orderable(c[i]) : 0u;
+    head = max(head, key[i]);
+  }
+  int n = 0;
+  uint32_t least = 1u;  // candidates' least code: all that may be selected, where they are few
+  if (!hard && a.keep * size > 64) {
+    sc.head[lane] = head;
+    __builtin_amdgcn_wave_barrier();
+    int gt = 0;
+    const uint4* h4 = reinterpret_cast<const uint4*>(sc.head);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const uint4 h = h4[j];
+      gt += (h.x > head) + (h.y > head) + (h.z > head) + (h.w > head);
+    }
+    least = max(wave_reduce<false>(gt < a.k ? head : 0xFFFFFFFFu), 1u);
+    if (a.bias && least > kOff32) {
+      const float tau = from_orderable(least);
+      least = orderable(tau - (0x1p-18f + 0x1p-21f * fabsf(tau)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) n += __popcll(__ballot(key[i] >= least));
+  if (hard || n > 64) {
+    select64<P>(a, t, l, bias, base, sc);
+    return;
+  }
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const bool in = key[i] >= least;
+    const uint64_t m = __ballot(in);
+    if (in) {
+      const int z = at + __popcll(m & lanemask_lt());
+      sc.l[z] = l[i];
+      sc.b[z] = bias[i];
+      sc.e[z] = lane + 64 * i;
+    }
+    at += __popcll(m);
+  }
+  __builtin_amdgcn_wave_barrier();
+  const bool in = lane < n;
+  const float x = in ? sc.l[lane] : 0.f, b = in ? sc.b[lane] : 0.f;
+  const int e = in ? sc.e[lane] : a.E;
+  int rank = 0;
+  double s = 0.0;
+  for (int pass = 0; pass < 2; ++pass) {
+    s = in ? score64(a, base, x) : 0.0;
+    const double v = s + (double)b;
+    const uint64_t mine = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(v) : orderable64((double)x);
+    sc.cand[lane] = mine;
+    __builtin_amdgcn_wave_barrier();
+    rank = 0;
+    bool near = false;
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o = sc.cand[j];
+      const int oe = sc.e[j];
+      rank += o > mine || (o == mine && oe < e);
+      if (a.softmax && a.bias) near |= in && oe != e && fabs(from_orderable64(o) - v) < 0x1p-20;
+    }
+    __builtin_amdgcn_wave_barrier();
+    // a softmax's sum is in 32 bits so far: what that leaves open is settled with one in 64
+    if (pass || !a.softmax || !a.bias || !__any(near)) break;
+    base.total = total64<P>(l, a.E, base.top);
+  }
+  const bool sel = in && rank < a.k;
+  const double sum = a.renorm ? wave_sum64(sel ? s : 0.0) : 1.0;
+  if (sel) {
+    a.idx[(size_t)t * a.k + rank] = e;
+    a.gates[(size_t)t * a.k + rank] = (float)((double)a.scale * (sum == 0.0 ? 0.0 : s / sum));
+  }
+}
+
+// The gradient. A row's entries are gathered in LDS, zero where nothing was selected, and stored side by side. Bound by the
+// bytes of the rows that it writes; logits are read where one was selected, or with softmax and without
+// renormalisation all of them.
+template <int P>
+__global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool vec) {
+  __shared__ __attribute__((aligned(16))) float rows[kWaves][64 * P];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = blockIdx.x * kWaves + wave;
+  if (t >= a.T) return;
+  float* row = rows[wave];
+  const int32_t* idx = a.idx + (size_t)t * a.k;
+  const float* dg = a.d_gates + (size_t)t * a.k;
+  const bool full = a.softmax && !a.renorm;
+  // assignment `lane`, and its logit
+  int e = lane < a.k ? idx[lane] : -1;
+  if ((unsigned)e >= (unsigned)a.E) e = -1;
+  const float d0 = e >= 0 ? a.scale * dg[lane] : 0.f, l0 = e >= 0 ? logit_at(a, t, e) : -INFINITY;
+  float l[P];
+  if (full) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) l[i] = lane + 64 * i < a.E ? logit_at(a, t, lane + 64 * i) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) row[lane + 64 * i] = 0.f;
+  Base base{0.f, 1.0};
+  if (a.softmax) {  // over the row, or with renorm over what was selected
+    float top = -INFINITY;
+    bool nan = false;  // (a maximum leaves it out)
+    auto look = [&](float v) {
+      top = fmaxf(top, v);
+      nan |= v != v;
+    };
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) look(l[i]);
+    } else {
+      look(l0);
+      for (int j = 64 + lane; j < a.k; j += 64)
+        if ((unsigned)idx[j] < (unsigned)a.E) look(logit_at(a, t, idx[j]));
+    }
+    top = wave_maxf(top);
+    base.top = __any(nan) || top == INFINITY ? NAN : top;  // (such a row has no scores)
+    if (full) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) v += base.top == -INFINITY ? 0.f : expf(l[i] - base.top);
+      base.total = wave_sum(v);
+    }
   }
   auto score = [&](float v) {
-    return !a.softmax ? 1.f / (1.f + expf(-v)) : top == -INFINITY ? 0.f : expf(v - top) / total;
+    if (!a.softmax) return 1.f / (1.f + expf(-v));
+    return base.top == -INFINITY ? 0.f : expf(v - base.top) / (float)base.total;
   };
-  float S = 0.f, D = 0.f;  // sums of the selected scores and of d times them
-  for (int j = lane; j < a.k; j += 64)
+  const float s0 = e >= 0 ? score(l0) : 0.f;
+  float S = s0, D = d0 * s0;  // sums of the selected scores, and of d times them
+  for (int j = 64 + lane; j < a.k; j += 64)
     if ((unsigned)idx[j] < (unsigned)a.E) {
       const float s = score(logit_at(a, t, idx[j]));
       S += s;
@@ -189,26 +431,59 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a) {
   D = wave_sum(D);
   const float mean = a.renorm ? (S == 0.f ? 0.f : D / S) : 0.f, inv = a.renorm ? (S == 0.f ? 0.f : 1.f / S) : 1.f;
   __builtin_amdgcn_wave_barrier();
-  for (int j = 0; j < a.k; ++j) {  // (in order: an index may come twice)
-    const int e = idx[j];
-    if ((unsigned)e < (unsigned)a.E && lane == 0) row[wave][e] += (a.scale * dg[j] - mean) * inv;
+  // An entry's value from the sum of its d: the first of an expert's assignments adds them up, in order.
+  auto entry = [&](float d, float s) { return full ? d : a.softmax ? s * d : d * s * (1.f - s); };
+  if (a.k <= 64) {
+    const float mine = (d0 - mean) * inv;
+    float sum = 0.f;
+    bool first = e >= 0;
+    for (int j = 0; j < a.k; ++j) {
+      const int oe = __builtin_amdgcn_readlane(e, j);
+      const float od = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine), j));
+      if (oe == e) {
+        sum += od;
+        first &= j >= lane;
+      }
+    }
+    if (first) row[e] = entry(sum, s0);
+  } else {
+    for (int j = 0; j < a.k; ++j) {
+      const int o = idx[j];
+      if ((unsigned)o < (unsigned)a.E && lane == 0) row[o] += (a.scale * dg[j] - mean) * inv;
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int c = lane; !full && c < a.E; c += 64)
+      if (row[c] != 0.f) row[c] = entry(row[c], score(logit_at(a, t, c)));
   }
   __builtin_amdgcn_wave_barrier();
+  if (full) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int e = lane + 64 * i;
-    if (e >= a.E) continue;
-    const float d = row[wave][e];
-    float v = 0.f;
-    if (a.softmax && !a.renorm) {
-      v = score(l[i]) * (d - D);
-    } else if (d != 0.f) {
-      const float s = score(logit_at(a, t, e));
-      v = a.softmax ? s * d : d * s * (1.f - s);
+    for (int i = 0; i < P; ++i)
+      if (lane + 64 * i < a.E) row[lane + 64 * i] = score(l[i]) * (row[lane + 64 * i] - D);
+    __builtin_amdgcn_wave_barrier();
+  }
+  const size_t at = (size_t)t * a.E;
+#pragma unroll
+  for (int i = 0; i < P; i += 4) {
+    if (vec) {  // four neighbours a lane
+      const int c = 4 * lane + 64 * i;
+      if (c >= a.E) continue;
+      const float4 v = *reinterpret_cast<const float4*>(row + c);
+      if (a.bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.dlogits) + at + c) =
+            make_uint2(f32_to_bf16_bits(v.x) | f32_to_bf16_bits(v.y) << 16, f32_to_bf16_bits(v.z) | f32_to_bf16_bits(v.w) << 16);
+      else
+        *reinterpret_cast<float4*>(static_cast<float*>(a.dlogits) + at + c) = v;
+    } else {
+#pragma unroll
+      for (int z = 0; z < 4 && i + z < P; ++z) {
+        const int c = lane + 64 * (i + z);
+        if (c >= a.E) continue;
+        if (a.bf16) static_cast<uint16_t*>(a.dlogits)[at + c] = (uint16_t)f32_to_bf16_bits(row[c]);
+        else static_cast<float*>(a.dlogits)[at + c] = row[c];
+      }
     }
-    const size_t at = (size_t)t * a.E + e;
-    if (a.bf16) static_cast<uint16_t*>(a.dlogits)[at] = (uint16_t)f32_to_bf16_bits(v);
-    else static_cast<float*>(a.dlogits)[at] = v;
   }
 }
 
@@ -233,7 +508,8 @@ hipError_t launch_scores(const ScoreArgs& a, hipStream_t s) {
 
 hipError_t launch_scores_backward(const ScoreArgs& a, hipStream_t s) {
   const dim3 g((a.T + kWaves - 1) / kWaves);
-#define BACKWARD(P) MOE_LAUNCH("scores_backward", s, scores_backward<P>, g, dim3(64 * kWaves), 0, s, a)
+  const bool vec = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.dlogits) & 15) == 0;
+#define BACKWARD(P) MOE_LAUNCH("scores_backward", s, scores_backward<P>, g, dim3(64 * kWaves), 0, s, a, vec)
   BY_LANES(BACKWARD)
 #undef BACKWARD
   return hipGetLastError();

@@ -83,23 +83,40 @@ struct Scratch {
     float row[64 * P];     // what ranks an expert within its group
   };
   uint32_t head[64];
-  uint64_t cand[64];
   float l[64], b[64];
   int e[64];
 };
 
-// The groups whose value (order code v of group lane) is among the `keep` largest, a bit each.
+__device__ inline uint32_t from_lane(uint32_t v, int j) { return __builtin_amdgcn_readlane(v, j); }
+__device__ inline uint64_t from_lane(uint64_t v, int j) {
+  return (uint64_t)from_lane((uint32_t)(v >> 32), j) << 32 | from_lane((uint32_t)v, j);
+}
+
+// Group g's value (an order code) lies in lanes g * per and on: whether this lane's is among the `keep` largest, equal ones
+// in favour of the lower group; the bits of all lanes.
 template <typename V>
-__device__ inline uint64_t kept_groups(const ScoreArgs& a, V v, bool* stays) {
+__device__ inline uint64_t kept_groups(const ScoreArgs& a, V v, int per, bool* stays) {
   const int lane = threadIdx.x & 63;
   int rank = 0;
   for (int g = 0; g < a.groups; ++g) {
-    const V o = __shfl(v, g, 64);
-    rank += o > v || (o == v && g < lane);
+    const V o = from_lane(v, g * per);
+    rank += o > v || (o == v && g * per < lane - lane % per);
   }
-  *stays = lane < a.groups && rank < a.keep;
+  *stays = lane / per < a.groups && rank < a.keep;
   return __ballot(*stays);
 }
+
+// The partner of a lane in the step o of a reduction over 2 o lanes that alone are equal within o.
+__device__ inline uint32_t partner(uint32_t v, int o) {
+  switch (o) {
+    case 1: return dpp(v, 0xB1);
+    case 2: return dpp(v, 0x4E);
+    case 4: return dpp(v, 0x141);
+    case 8: return dpp(v, 0x140);
+    default: return __shfl_xor(v, o, 64);
+  }
+}
+__device__ inline float partner(float v, int o) { return __uint_as_float(partner(__float_as_uint(v), o)); }
 
 // 64 bits for all experts: groups by scanning them, then k rounds.
 template <int P>
@@ -136,7 +153,7 @@ __device__ inline void select64(const ScoreArgs& a, int t, const float (&l)[P], 
       }
     }
     bool stays;
-    const uint64_t kept = kept_groups(a, mine, &stays);
+    const uint64_t kept = kept_groups(a, mine, 1, &stays);
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane + 64 * i < a.E && !(kept >> ((lane + 64 * i) / size) & 1)) key[i] = 0ull;
@@ -235,31 +252,30 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
 #pragma unroll
   for (int i = 0; i < P; ++i) c[i] = l[i] == -INFINITY || !a.bias ? l[i] : score32(a, base, l[i]) + bias[i];
   const int size = a.E / a.groups;
-  uint64_t kept = ~0ull;
+  uint64_t out = 0;  // bit i: slot i's group does not stay
   bool hard = a.k > 64;
   if (a.groups > 1 && a.keep < a.groups && !hard) {
 #pragma unroll
     for (int i = 0; i < P; ++i)
       if (lane + 64 * i < a.E) sc.row[lane + 64 * i] = c[i];
     __builtin_amdgcn_wave_barrier();
+    uint64_t kept;
     int per = 64;  // lanes a group, which share its experts
     while (per * a.groups > 64) per >>= 1;
     const int g = lane / per;
     Top3 top{-INFINITY, -INFINITY, -INFINITY, 0, 0};  // (what is not above -inf is left out, NaN too)
     if (g < a.groups)
       for (int e = g * size + lane % per; e < (g + 1) * size; e += per) top.add(sc.row[e], e);
-    for (int o = 1; o < per; o <<= 1) {
-      const Top3 u{__shfl_xor(top.v1, o, 64), __shfl_xor(top.v2, o, 64), __shfl_xor(top.v3, o, 64), __shfl_xor(top.e1, o, 64),
-                   __shfl_xor(top.e2, o, 64)};
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      if (o >= per) continue;
+      const Top3 u{partner(top.v1, o), partner(top.v2, o), partner(top.v3, o), (int)partner((uint32_t)top.e1, o),
+                   (int)partner((uint32_t)top.e2, o)};
       top.add(u.v1, u.e1);
       top.add(u.v2, u.e2);
-      top.v3 = fmaxf(top.v3, fminf(u.v3, top.v2));
+      top.v3 = fmaxf(top.v3, u.v3);
     }
-    // group `lane`'s
-    const int from = lane < a.groups ? lane * per : 0;
-    top = Top3{__shfl(top.v1, from, 64), __shfl(top.v2, from, 64), __shfl(top.v3, from, 64), __shfl(top.e1, from, 64),
-               __shfl(top.e2, from, 64)};
-    const bool live = top.v1 > -INFINITY, two = a.group_top == 2 && top.v2 > -INFINITY;
+    const bool ours = g < a.groups, live = top.v1 > -INFINITY, two = a.group_top == 2 && top.v2 > -INFINITY;
     float v = top.v1, margin = 0.f;
     if (a.bias || a.group_top == 2) {
       if (!a.bias) v = live ? score32(a, base, top.v1) : v;
@@ -267,34 +283,41 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
       margin = a.bias ? 0x1p-18f + 0x1p-21f * fabsf(v) : fmaxf(0x1p-19f * v, 0x1p-126f);
     }
     bool stays;
-    kept = kept_groups(a, orderable(v), &stays);
+    kept = kept_groups(a, orderable(v), per, &stays);
     // the least that stays and the most that goes
     const float lo = from_orderable(wave_reduce<false>(stays ? orderable(v) : 0xFFFFFFFFu));
-    const float hi = wave_maxf(lane < a.groups && !stays ? v : -INFINITY);
-    const float most = wave_maxf(lane < a.groups && live ? margin : 0.f);
+    const float hi = wave_maxf(ours && !stays ? v : -INFINITY);
+    const float most = wave_maxf(ours && live ? margin : 0.f);
     if (most > 0.f && hi > -INFINITY && !(lo - hi >= 2.f * most)) {
-      const float apart = a.bias ? 0x1p-18f + 0x1p-21f * fabsf(top.v2) : 0.f;
-      hard = __any(lane < a.groups && two && a.bias && top.v3 > -INFINITY && !(top.v2 - top.v3 >= apart)) || !(hi < INFINITY);
+      // the best of a group in 32 bits need not be so in 64, where the next is near
+      const float apart = 0x1p-17f + 0x1p-20f * fabsf(top.v2);
+      hard = !(hi < INFINITY) || (a.bias && __any(ours && (a.group_top == 2 ? two && top.v3 > -INFINITY && !(top.v2 - top.v3 >= apart)
+                                                                             : top.v2 > -INFINITY && !(top.v1 - top.v2 >= apart))));
       if (!hard) {
         Base exact = base;
         if (a.softmax && a.bias) exact.total = total64<P>(l, a.E, base.top);
         double w = -INFINITY;
-        if (lane < a.groups && live) {
+        if (ours && live) {
           w = a.bias ? score64(a, exact, logit_at(a, t, top.e1)) + (double)a.bias[top.e1] : score64(a, exact, top.v1);
           if (two) w += a.bias ? score64(a, exact, logit_at(a, t, top.e2)) + (double)a.bias[top.e2] : score64(a, exact, top.v2);
         }
-        kept = kept_groups(a, lane < a.groups ? orderable64(w) : 0ull, &stays);
-        // the best of a group in 32 bits need not be so in 64, where two of them alone are near
-        if (a.group_top == 1) hard = __any(lane < a.groups && a.bias && top.v2 > -INFINITY && !(top.v1 - top.v2 >= apart + margin));
+        kept = kept_groups(a, ours ? orderable64(w) : (uint64_t)0, per, &stays);
       }
     }
     __builtin_amdgcn_wave_barrier();
+    // a bit for each expert's group (exact: the quotient is under 64, and half an expert from a border)
+    const float each = 1.f / (float)size;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int of = (int)(((float)(lane + 64 * i) + 0.5f) * each);
+      out |= (kept >> (of * per) & 1 ? 0ull : 1ull) << i;
+    }
   }
   uint32_t key[P], head = 0u;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const int e = lane + 64 * i;
-    key[i] = e < a.E && (a.groups == 1 || (kept >> (e / size) & 1)) ? orderable(c[i]) : 0u;
+    key[i] = e < a.E && !(out >> i & 1) ? orderable(c[i]) : 0u;
     head = max(head, key[i]);
   }
   int n = 0;
@@ -344,17 +367,14 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     s = in ? score64(a, base, x) : 0.0;
     const double v = s + (double)b;
     const uint64_t mine = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(v) : orderable64((double)x);
-    sc.cand[lane] = mine;
-    __builtin_amdgcn_wave_barrier();
     rank = 0;
     bool near = false;
     for (int j = 0; j < n; ++j) {
-      const uint64_t o = sc.cand[j];
-      const int oe = sc.e[j];
+      const uint64_t o = from_lane(mine, j);
+      const int oe = __builtin_amdgcn_readlane(e, j);
       rank += o > mine || (o == mine && oe < e);
       if (a.softmax && a.bias) near |= in && oe != e && fabs(from_orderable64(o) - v) < 0x1p-20;
     }
-    __builtin_amdgcn_wave_barrier();
     // a softmax's sum is in 32 bits so far: what that leaves open is settled with one in 64
     if (pass || !a.softmax || !a.bias || !__any(near)) break;
     base.total = total64<P>(l, a.E, base.top);

@@ -10,8 +10,9 @@
 //   groups  : their values in 32 bits, unless the last that stays and the first that
 //             goes are near each other; then those of each group's best two in 64.
 //   experts : all within the margin of a lower bound of the k-th (topk.h's threshold)
-//             are candidates, one a lane, whose values are computed in 64 bits at
-//             once and ranked by counting. Without a bias the logits are the order.
+//             are candidates, one a lane, ranked by counting; where two of them are near
+//             each other, by their values in 64 bits, which take all lanes at once. Without a
+//             bias the logits are the order.
 // What remains (over 64 candidates or ranks; a third expert of a group near its
 // second where groups are near) goes through 64 bits for all experts and k rounds.
 #include "gemv.h"
@@ -83,7 +84,7 @@ struct Scratch {
     float row[64 * P];     // what ranks an expert within its group
   };
   uint32_t head[64];
-  float l[64], b[64];
+  float l[64], b[64], c[64];  // candidates
   int e[64];
 };
 
@@ -353,37 +354,46 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
       const int z = at + __popcll(m & lanemask_lt());
       sc.l[z] = l[i];
       sc.b[z] = bias[i];
+      sc.c[z] = c[i];
       sc.e[z] = lane + 64 * i;
     }
     at += __popcll(m);
   }
   __builtin_amdgcn_wave_barrier();
   const bool in = lane < n;
-  const float x = in ? sc.l[lane] : 0.f, b = in ? sc.b[lane] : 0.f;
+  const float x = in ? sc.l[lane] : 0.f, v = in ? sc.c[lane] : 0.f;
   const int e = in ? sc.e[lane] : a.E;
+  const uint32_t mine = in ? orderable(v) : 0u;
+  const float apart = a.bias ? 0x1p-17f + 0x1p-20f * fabsf(v) : 0.f;
   int rank = 0;
-  double s = 0.0;
-  for (int pass = 0; pass < 2; ++pass) {
-    s = in ? score64(a, base, x) : 0.0;
-    const double v = s + (double)b;
-    const uint64_t mine = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(v) : orderable64((double)x);
-    rank = 0;
-    bool near = false;
-    for (int j = 0; j < n; ++j) {
-      const uint64_t o = from_lane(mine, j);
-      const int oe = __builtin_amdgcn_readlane(e, j);
-      rank += o > mine || (o == mine && oe < e);
-      if (a.softmax && a.bias) near |= in && oe != e && fabs(from_orderable64(o) - v) < 0x1p-20;
-    }
-    // a softmax's sum is in 32 bits so far: what that leaves open is settled with one in 64
-    if (pass || !a.softmax || !a.bias || !__any(near)) break;
-    base.total = total64<P>(l, a.E, base.top);
+  bool near = false;  // to another one: the order is open
+  for (int j = 0; j < n; ++j) {
+    const uint32_t o = from_lane(mine, j);
+    const int oe = __builtin_amdgcn_readlane(e, j);
+    rank += o > mine || (o == mine && oe < e);
+    near |= oe != e && fabsf(from_orderable(o) - v) < apart;
   }
-  const bool sel = in && rank < a.k;
-  const double sum = a.renorm ? wave_sum64(sel ? s : 0.0) : 1.0;
+  float s = in ? a.softmax ? score32(a, base, x) : 1.f / (1.f + expf(-x)) : 0.f;
+  bool sel = in && rank < a.k;
+  float sum = a.renorm ? wave_sum(sel ? s : 0.f) : 1.f;
+  if (__any(in && near) || sum < 0x1p-90f) {  // (scores that 32 bits hardly hold, too)
+    if (a.softmax) base.total = total64<P>(l, a.E, base.top);
+    const double wide = in ? score64(a, base, x) : 0.0;
+    const uint64_t best = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(wide + (double)sc.b[lane]) : orderable64((double)x);
+    rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o = from_lane(best, j);
+      const int oe = __builtin_amdgcn_readlane(e, j);
+      rank += o > best || (o == best && oe < e);
+    }
+    sel = in && rank < a.k;
+    const double all = a.renorm ? wave_sum64(sel ? wide : 0.0) : 1.0;
+    s = all == 0.0 ? 0.f : (float)(wide / all);
+    sum = 1.f;
+  }
   if (sel) {
     a.idx[(size_t)t * a.k + rank] = e;
-    a.gates[(size_t)t * a.k + rank] = (float)((double)a.scale * (sum == 0.0 ? 0.0 : s / sum));
+    a.gates[(size_t)t * a.k + rank] = a.scale * (s / sum);
   }
 }
 

@@ -61,18 +61,10 @@ __device__ inline float score32(const ScoreArgs& a, const Base& b, float l) {
   return b.top == -INFINITY ? 0.f : expf(l - b.top) * __builtin_amdgcn_rcpf((float)b.total);
 }
 
-// The sum of a row's exponentials in 64 bits.
-template <int P>
-__device__ inline double total64(const float (&l)[P], int E, float top) {
-  double v = 0.0;
-#pragma unroll 1
-  for (int i = 0; i < P; ++i) {
-    float x = l[0];
-#pragma unroll
-    for (int z = 1; z < P; ++z) x = i == z ? l[z] : x;
-    if ((int)(threadIdx.x & 63) + 64 * i < E) v += top == -INFINITY ? 0.0 : exp((double)x - (double)top);
-  }
-  return wave_sum64(v);
+// What a biased score is screened by: within 2^-21 of it, as score32, but not relative to small ones.
+__device__ inline float score_near(const ScoreArgs& a, const Base& b, float l) {
+  if (!a.softmax) return __builtin_amdgcn_rcpf(1.f + __expf(-l));
+  return b.top == -INFINITY ? 0.f : __expf(l - b.top) * __builtin_amdgcn_rcpf((float)b.total);
 }
 
 constexpr int kWaves = 4;  // tokens per workgroup
@@ -81,12 +73,22 @@ template <int P>
 struct Scratch {
   union {
     uint64_t key[64 * P];  // 64 bits for all experts
-    float row[64 * P];     // what ranks an expert within its group
+    struct {
+      float l[64 * P];  // the row's logits
+      float c[64 * P];  // what ranks an expert within its group
+    };
   };
-  uint32_t head[64];
-  float l[64], b[64], c[64];  // candidates
-  int e[64];
+  uint2 cand[64];  // candidates: what ranks them, and which
 };
+
+// The sum of a row's exponentials in 64 bits.
+template <int P>
+__device__ inline double total64(const Scratch<P>& sc, int E, float top) {
+  double v = 0.0;
+#pragma unroll 1
+  for (int e = threadIdx.x & 63; e < E; e += 64) v += top == -INFINITY ? 0.0 : exp((double)sc.l[e] - (double)top);
+  return wave_sum64(v);
+}
 
 __device__ inline uint32_t from_lane(uint32_t v, int j) { return __builtin_amdgcn_readlane(v, j); }
 __device__ inline uint64_t from_lane(uint64_t v, int j) {
@@ -121,14 +123,17 @@ __device__ inline float partner(float v, int o) { return __uint_as_float(partner
 
 // 64 bits for all experts: groups by scanning them, then k rounds.
 template <int P>
-__device__ inline void select64(const ScoreArgs& a, int t, const float (&l)[P], const float (&bias)[P], Base base,
-                                Scratch<P>& sc) {
+__device__ inline void select64(const ScoreArgs& a, int t, Base base, Scratch<P>& sc) {
   const int lane = threadIdx.x & 63;
-  if (a.softmax) base.total = total64<P>(l, a.E, base.top);
+  if (a.softmax) base.total = total64<P>(sc, a.E, base.top);
   uint64_t key[P];
+  float l[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) l[i] = sc.l[lane + 64 * i];
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const double c = l[i] == -INFINITY ? -INFINITY : a.bias ? score64(a, base, l[i]) + (double)bias[i] : (double)l[i];
+    const double c = l[i] == -INFINITY ? -INFINITY : a.bias ? score64(a, base, l[i]) + (double)a.bias[min(lane + 64 * i, a.E - 1)] : (double)l[i];
     key[i] = lane + 64 * i < a.E ? orderable64(c) : 0ull;
     sc.key[lane + 64 * i] = key[i];
   }
@@ -225,10 +230,16 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
   if (t >= a.T) return;
   Scratch<P>& sc = scratch[wave];
   float l[P], bias[P];
+  auto load = [&](int last) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < P; ++i) l[i] = logit_at(a, t, min(lane + 64 * i, a.E - 1));
+    for (int i = 0; i < P; ++i) l[i] = logit_at(a, t, min(lane + 64 * i, last));
 #pragma unroll
-  for (int i = 0; i < P; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, a.E - 1)] : 0.f;
+    for (int i = 0; i < P; ++i) bias[i] = a.bias ? a.bias[min(lane + 64 * i, last)] : 0.f;
+  };
+  if (a.E == 64 * P) load(64 * P - 1);  // (no limit to look at)
+  else load(a.E - 1);
+#pragma unroll
+  for (int i = 0; i < P; ++i) sc.l[lane + 64 * i] = l[i];
   Base base{0.f, 1.0};
   if (a.softmax) {
     float top = -INFINITY;
@@ -251,14 +262,13 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
   // what ranks an expert: its logit, or score + bias in 32 bits
   float c[P];
 #pragma unroll
-  for (int i = 0; i < P; ++i) c[i] = l[i] == -INFINITY || !a.bias ? l[i] : score32(a, base, l[i]) + bias[i];
+  for (int i = 0; i < P; ++i) c[i] = l[i] == -INFINITY || !a.bias ? l[i] : score_near(a, base, l[i]) + bias[i];
   const int size = a.E / a.groups;
   uint64_t out = 0;  // bit i: slot i's group does not stay
   bool hard = a.k > 64;
   if (a.groups > 1 && a.keep < a.groups && !hard) {
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (lane + 64 * i < a.E) sc.row[lane + 64 * i] = c[i];
+    for (int i = 0; i < P; ++i) sc.c[lane + 64 * i] = c[i];
     __builtin_amdgcn_wave_barrier();
     uint64_t kept;
     int per = 64;  // lanes a group, which share its experts
@@ -266,7 +276,7 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     const int g = lane / per;
     Top3 top{-INFINITY, -INFINITY, -INFINITY, 0, 0};  // (what is not above -inf is left out, NaN too)
     if (g < a.groups)
-      for (int e = g * size + lane % per; e < (g + 1) * size; e += per) top.add(sc.row[e], e);
+      for (int e = g * size + lane % per; e < (g + 1) * size; e += per) top.add(sc.c[e], e);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       if (o >= per) continue;
@@ -296,11 +306,11 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
                                                                              : top.v2 > -INFINITY && !(top.v1 - top.v2 >= apart))));
       if (!hard) {
         Base exact = base;
-        if (a.softmax && a.bias) exact.total = total64<P>(l, a.E, base.top);
+        if (a.softmax && a.bias) exact.total = total64<P>(sc, a.E, base.top);
         double w = -INFINITY;
         if (ours && live) {
-          w = a.bias ? score64(a, exact, logit_at(a, t, top.e1)) + (double)a.bias[top.e1] : score64(a, exact, top.v1);
-          if (two) w += a.bias ? score64(a, exact, logit_at(a, t, top.e2)) + (double)a.bias[top.e2] : score64(a, exact, top.v2);
+          w = a.bias ? score64(a, exact, sc.l[top.e1]) + (double)a.bias[top.e1] : score64(a, exact, top.v1);
+          if (two) w += a.bias ? score64(a, exact, sc.l[top.e2]) + (double)a.bias[top.e2] : score64(a, exact, top.v2);
         }
         kept = kept_groups(a, ours ? orderable64(w) : (uint64_t)0, per, &stays);
       }
@@ -324,16 +334,14 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
   int n = 0;
   uint32_t least = 1u;  // candidates' least code: all that may be selected, where they are few
   if (!hard && a.keep * size > 64) {
-    sc.head[lane] = head;
-    __builtin_amdgcn_wave_barrier();
-    int gt = 0;
-    const uint4* h4 = reinterpret_cast<const uint4*>(sc.head);
+    // the k-th largest of the lanes' largest, its last 13 bits open downward, a bit at a time
+    least = 0u;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const uint4 h = h4[j];
-      gt += (h.x > head) + (h.y > head) + (h.z > head) + (h.w > head);
+    for (int i = 31; i > 12; --i) {
+      const uint32_t next = least | 1u << i;
+      if (__popcll(__ballot(head >= next)) >= a.k) least = next;
     }
-    least = max(wave_reduce<false>(gt < a.k ? head : 0xFFFFFFFFu), 1u);
+    least = max(least, 1u);
     if (a.bias && least > kOff32) {
       const float tau = from_orderable(least);
       least = orderable(tau - (0x1p-18f + 0x1p-21f * fabsf(tau)));
@@ -342,7 +350,7 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
 #pragma unroll
   for (int i = 0; i < P; ++i) n += __popcll(__ballot(key[i] >= least));
   if (hard || n > 64) {
-    select64<P>(a, t, l, bias, base, sc);
+    select64<P>(a, t, base, sc);
     return;
   }
   int at = 0;
@@ -352,19 +360,16 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     const uint64_t m = __ballot(in);
     if (in) {
       const int z = at + __popcll(m & lanemask_lt());
-      sc.l[z] = l[i];
-      sc.b[z] = bias[i];
-      sc.c[z] = c[i];
-      sc.e[z] = lane + 64 * i;
+      sc.cand[z] = make_uint2(key[i], lane + 64 * i);
     }
     at += __popcll(m);
   }
   __builtin_amdgcn_wave_barrier();
   const bool in = lane < n;
-  const float x = in ? sc.l[lane] : 0.f, v = in ? sc.c[lane] : 0.f;
-  const int e = in ? sc.e[lane] : a.E;
-  const uint32_t mine = in ? orderable(v) : 0u;
-  const float apart = a.bias ? 0x1p-17f + 0x1p-20f * fabsf(v) : 0.f;
+  const uint32_t mine = in ? sc.cand[lane].x : 0u;
+  const int e = in ? (int)sc.cand[lane].y : a.E;
+  const float x = in ? sc.l[e] : 0.f;
+  const float v = from_orderable(mine), apart = a.bias ? 0x1p-17f + 0x1p-20f * fabsf(v) : 0.f;
   int rank = 0;
   bool near = false;  // to another one: the order is open
   for (int j = 0; j < n; ++j) {
@@ -377,9 +382,9 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
   bool sel = in && rank < a.k;
   float sum = a.renorm ? wave_sum(sel ? s : 0.f) : 1.f;
   if (__any(in && near) || sum < 0x1p-90f) {  // (scores that 32 bits hardly hold, too)
-    if (a.softmax) base.total = total64<P>(l, a.E, base.top);
+    if (a.softmax) base.total = total64<P>(sc, a.E, base.top);
     const double wide = in ? score64(a, base, x) : 0.0;
-    const uint64_t best = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(wide + (double)sc.b[lane]) : orderable64((double)x);
+    const uint64_t best = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(wide + (double)a.bias[e]) : orderable64((double)x);
     rank = 0;
     for (int j = 0; j < n; ++j) {
       const uint64_t o = from_lane(best, j);

@@ -17,7 +17,7 @@
 namespace moe {
 namespace {
 
-constexpr int kBufs = 3;  // (of strips of 128 results too)
+constexpr int kBufs = 3;
 constexpr int kThreads = 512;
 constexpr int kRun = 16;  // rows of a product
 
@@ -93,16 +93,14 @@ __device__ inline float uniform_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
-// WIDE: a row's scales come 16 bytes at a time, for four steps (a multiple of four blocks, aligned): a direct load costs by the
-// 128-byte lines that it touches, and a step's scales alone touch a line a row.
-template <bool BACK, bool EXACT, int WN, bool WIDE>
+template <bool BACK, bool EXACT, int WN>
 __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   constexpr int kRuns = WN;             // runs of 16 rows a wave
   constexpr int kWL = WN;               // loads of the matrix a wave and step, 1 KB each
-  constexpr int kXL = 2;                // of rows, where the tile has rows in this wave's share; then one of their scales
+  constexpr int kLoads = 2 + kWL + 1;   // and of rows and their scales
   constexpr int strip = 64 * WN;
   __shared__ Buf8<WN> buf[kBufs];
-  __shared__ __attribute__((aligned(16))) float scale[WIDE ? 2 * kTM * 4 : kBufs * kTM];  // WIDE: two places of four a row
+  __shared__ float scale[kBufs][kTM];
   __shared__ Tiles tiles;
   __shared__ int slot;
   const int strips = (a.N + strip - 1) / strip;
@@ -122,8 +120,6 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   uint32_t xoff[2], woff[kWL], soff;
   const uint8_t* wbase;
   int lp = 0, row_next[3];
-  bool lrows = false, lscales = false;  // what the last load() brought: rows, and their scales
-  int ls = 0, cs = 0;                   // WIDE: places of the scales last asked for, and in use
   auto row_of = [&](int u) { return u < 2 ? 16 * wave + 8 * u + (lane >> 3) : 16 * wave + r; };
   auto fetch_rows = [&](const TileInfo& t) {  // the row numbers of a tile, to be used later
 #pragma unroll
@@ -147,23 +143,13 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
       }
     }
     lp = 0;
-    lrows = 16 * wave < t.M;
   };
   auto load = [&](int b) __attribute__((always_inline)) {
     Buf8<WN>& B = buf[b];
     const int p = min(lp, a.xb - 1);
-    lscales = !WIDE || lp % 4 == 0;
-    if (WIDE && lscales) ls ^= 1;
-    if (lrows) {
 #pragma unroll
-      for (int u = 0; u < kXL; ++u)
-        stream16(static_cast<const uint8_t*>(a.x) + p * kF8Block, xoff[u], lds_offset(B.x) + 1024 * (kXL * wave + u));
-      if constexpr (WIDE) {
-        if (lscales && lane < 16) stream16(a.xf + p, soff, lds_offset(scale) + 2048 * ls + 256 * wave);
-      } else {
-        if (lane < 16) stream4(a.xf + p, soff, lds_offset(scale) + 512 * b + 64 * wave);
-      }
-    }
+    for (int u = 0; u < 2; ++u)
+      stream16(static_cast<const uint8_t*>(a.x) + p * kF8Block, xoff[u], lds_offset(B.x) + 1024 * (2 * wave + u));
 #pragma unroll
     for (int u = 0; u < kWL; ++u) {
       if constexpr (BACK)
@@ -171,14 +157,8 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
       else
         stream16(wbase + p * kF8Block, woff[u], lds_offset(B.w) + 1024 * (kWL * wave + u));
     }
+    if (lane < 16) stream4(a.xf + p, soff, lds_offset(scale[b]) + 64 * wave);
     ++lp;
-  };
-  // All loads but the last load()'s have landed (loads: there was one in this step), and every wave has come here.
-  auto done = [&](bool loads) __attribute__((always_inline)) {
-    if (!loads) step_done();
-    else if (!lrows) step_done<kWL>();
-    else if (WIDE && !lscales) step_done<kWL + kXL>();
-    else step_done<kWL + kXL + 1>();
   };
 
   int b = 0;
@@ -189,8 +169,8 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   load(1);
   load(2);
   // (what has landed where a tile begins: steps 0 and 1, or with EXACT step 0)
-  if (EXACT) step_done<2 * kWL>();
-  else step_done<kWL>();
+  if (EXACT) step_done<2 * kLoads>();
+  else step_done<kLoads>();
   for (;;) {
     const bool more = next < items;
     if (more) {
@@ -212,13 +192,9 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
     // one loop for each number of live runs (a switch inside the loop makes the compiler move accumulators)
     auto run = [&](auto LL) __attribute__((always_inline)) {
       constexpr int L = decltype(LL)::value;
-      auto read_scales = [&](Operands<L>& o, int at, int p) __attribute__((always_inline)) {
-        if (WIDE && p % 4 == 0 && p < P) cs ^= 1;
+      auto read_scales = [&](Operands<L>& o, int at) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int m = kRun * (run0 + i) + r;
-          o.s[i] = WIDE ? scale[(cs * kTM + m) * 4 + (p & 3)] : scale[at * kTM + m];
-        }
+        for (int i = 0; i < L; ++i) o.s[i] = scale[at][kRun * (run0 + i) + r];
       };
       auto read_w = [&](Operands<L>& o, int at, int j) __attribute__((always_inline)) {
         const Buf8<WN>& B = buf[at];
@@ -256,7 +232,7 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
         if constexpr (L > 0) {
           if (p + 1 < a.xb) wp += wstep;
           sw = uniform_load(wp);
-          read_scales(o, b1, p + 1);
+          read_scales(o, b1);
           __builtin_amdgcn_sched_barrier(0);
           floatx4_t c[3];
 #pragma unroll
@@ -273,14 +249,15 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
           }
         }
         // the loads of the step after next have landed; this step's may be in flight
-        done(loads);
+        if (loads) step_done<kLoads>();
+        else step_done();
         b = b1;
       };
       // The same with bf16 products: codes become bf16 as they are read, which leaves no registers for a second set; the
       // step's buffer is loaded again when every wave has read it.
       auto step_exact = [&](int p) __attribute__((always_inline)) {
         if (L > 0 && p < a.xb) {
-          read_scales(o, b, p);
+          read_scales(o, b);
           const float swp = uniform_load(wp);
           wp += wstep;
           bf16x8_t w[4][4];
@@ -307,18 +284,18 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
             }
           }
         }
-        done(p + 2 < P || more);
+        if (p + 2 < P || more) step_done<kLoads>();
+        else step_done();
         if (p + 3 == P && more) aim(tn);
         if (p + 3 < P || more) load(b);
         b = b == 2 ? 0 : b + 1;
       };
       if constexpr (EXACT) {
-        if (WIDE && L == 0) cs ^= (P / 4) & 1;
         for (int p = 0; p < P; ++p) step_exact(p);
       } else {
         if constexpr (L > 0) {
           sw = uniform_load(wp);
-          read_scales(o, b, 0);
+          read_scales(o, b);
 #pragma unroll
           for (int j = 0; j < 4; ++j) read_w(o, b, j);
 #pragma unroll
@@ -326,7 +303,6 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
         }
         // every wave has read its first operands before their buffer is loaded again
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (WIDE && L == 0) cs ^= (P / 4) & 1;
 #pragma nounroll
         for (int p = 0; p < P - 3; ++p) step(p, true);
         if (more) aim(tn);
@@ -362,23 +338,16 @@ bool f8_tiles_can(const F8Args& a) {
 }
 
 hipError_t launch_f8_tiles(F8Args a, hipStream_t s) {
-  const int cap = device_cus();
-  const int strip = mx4_row_tiles(a) * ((a.N + 255) / 256) < cap ? 128 : 256;
+  constexpr int strip = 256;
   const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * ((a.N + strip - 1) / strip);
+  const int cap = device_cus();
   const dim3 g((unsigned)(most < cap ? most : cap));
   if (most <= cap || g.x % kXcds) a.counter = nullptr;
   else if (a.counter) launch_mx4_zero(a.counter, s);
-  const bool wide = a.xb % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xf) & 15) == 0;
-#define TILES(BACK, EXACT, NAME) \
-  if (strip == 256 && wide) MOE_LAUNCH(NAME "_wide", s, (f8_tiles<BACK, EXACT, 4, true>), g, dim3(kThreads), 0, s, a); \
-  else if (strip == 256) MOE_LAUNCH(NAME, s, (f8_tiles<BACK, EXACT, 4, false>), g, dim3(kThreads), 0, s, a); \
-  else if (wide) MOE_LAUNCH(NAME "_128_wide", s, (f8_tiles<BACK, EXACT, 2, true>), g, dim3(kThreads), 0, s, a); \
-  else MOE_LAUNCH(NAME "_128", s, (f8_tiles<BACK, EXACT, 2, false>), g, dim3(kThreads), 0, s, a)
-  if (a.back && a.exact) { TILES(true, true, "f8_tiles_back"); }
-  else if (a.back) { TILES(true, false, "f8_tiles_back"); }
-  else if (a.exact) { TILES(false, true, "f8_tiles"); }
-  else { TILES(false, false, "f8_tiles"); }
-#undef TILES
+  if (a.back && a.exact) MOE_LAUNCH("f8_tiles_back", s, (f8_tiles<true, true, 4>), g, dim3(kThreads), 0, s, a);
+  else if (a.back) MOE_LAUNCH("f8_tiles_back", s, (f8_tiles<true, false, 4>), g, dim3(kThreads), 0, s, a);
+  else if (a.exact) MOE_LAUNCH("f8_tiles", s, (f8_tiles<false, true, 4>), g, dim3(kThreads), 0, s, a);
+  else MOE_LAUNCH("f8_tiles", s, (f8_tiles<false, false, 4>), g, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

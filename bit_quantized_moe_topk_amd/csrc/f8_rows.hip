@@ -35,40 +35,98 @@ __device__ inline Unit unit_of(const Mx4Args& a) {
   return u;
 }
 
-template <bool BACK, bool EXACT>
+// Lane (r, g) holds chunks 2 g and 2 g + 1 of a block of matrix row n0 + 16 j + r and of x's row r. A wave asks for its next
+// kAhead blocks at once: with a few rows the time is the chain from the group's offsets over its loads to the sums.
+template <bool EXACT, int NT>
 __global__ __launch_bounds__(256) void rows_product(F8Args a) {
+  constexpr int kAhead = 4;
+  __shared__ floatx4_t part[4][NT][64];
+  const Unit u = unit_of(a);
+  if (u.M <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.y * 16 * NT;
+  const int row = max(mx4_row(a, u.s0 + min(r, u.M - 1)), 0);
+  const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + (size_t)row * a.xb * kF8Block + 32 * g);
+  const float* xs = a.xf + (size_t)row * a.xb;
+  const uint4* wp[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    wp[j] = reinterpret_cast<const uint4*>(a.wc + ((size_t)u.e * a.N + min(n0 + 16 * j + r, a.N - 1)) * a.wb * kF8Block + 32 * g);
+  const float* ws = a.wf + ((size_t)u.e * f8_blocks(a.N) + n0 / kF8Block) * a.wb;  // (16 NT rows are of one block of rows)
+  floatx4_t acc[NT] = {};
+  for (int p0 = wave; p0 < a.xb; p0 += 4 * kAhead) {
+    uint4 w[kAhead][NT][2], x[kAhead][2];
+    float s[kAhead];
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int p = min(p0 + 4 * z, a.xb - 1);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[z][j][i] = wp[j][8 * (size_t)p + i];
+    }
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      const int p = min(p0 + 4 * z, a.xb - 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) x[z][i] = xp[8 * (size_t)p + i];
+      s[z] = xs[p] * ws[p];
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int z = 0; z < kAhead; ++z) {
+      if (p0 + 4 * z >= a.xb) break;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const floatx4_t c = f8_products<EXACT>(f8_pair(w[z][j][0], w[z][j][1]), f8_pair(x[z][0], x[z][1]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(c[i], s[z], acc[j][i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
+  __syncthreads();
+  // wave j brings results 16 j on
+  if (wave >= NT || r >= u.M) return;
+  floatx4_t y = part[0][wave][lane];
+#pragma unroll
+  for (int z = 1; z < 4; ++z) y += part[z][wave][lane];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = n0 + 16 * wave + 4 * g + i;
+    if (n >= a.N) continue;
+    const size_t at = (size_t)(u.s0 + r) * a.N + n;
+    if (a.ydtype == 1) static_cast<uint16_t*>(a.y)[at] = (uint16_t)f32_to_bf16_bits(y[i]);
+    else static_cast<float*>(a.y)[at] = y[i];
+  }
+}
+
+// The same with the matrix turned, for what the tiles cannot address (past 4 GiB of rows, or of one matrix): a lane
+// gathers its codes a byte at a time.
+template <bool EXACT>
+__global__ __launch_bounds__(256) void rows_back(F8Args a) {
   __shared__ floatx4_t part[4][64];
   const Unit u = unit_of(a);
   if (u.M <= 0) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.y * 16;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 15, g = lane >> 4, n0 = blockIdx.y * 16;
   const int row = max(mx4_row(a, u.s0 + min(r, u.M - 1)), 0);
   const uint8_t* x = static_cast<const uint8_t*>(a.x) + (size_t)row * a.xb * kF8Block + 32 * g;
-  const float* xs = a.xf + (size_t)row * a.xb;
-  const int stored = BACK ? a.K : a.N;  // rows of the stored matrix
-  const uint8_t* w = a.wc + (size_t)u.e * stored * a.wb * kF8Block;
-  const float* ws = a.wf + (size_t)u.e * f8_blocks(stored) * a.wb;
+  const uint8_t* w = a.wc + (size_t)u.e * a.K * a.wb * kF8Block;
+  const float* ws = a.wf + (size_t)u.e * f8_blocks(a.K) * a.wb;
   floatx4_t acc = {};
   for (int p = wave; p < a.xb; p += 4) {
     const uint4* xp = reinterpret_cast<const uint4*>(x + (size_t)p * kF8Block);
     int8v_t m;
-    if constexpr (BACK) {
-      uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = 0;
+    for (int i = 0; i < 8; ++i) {
+      uint32_t v = 0;
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int c = min(p * kF8Block + 32 * g + 4 * i + z, a.K - 1);
-          v[i] |= (uint32_t)w[(size_t)c * a.wb * kF8Block + n0 + r] << (8 * z);
-        }
-        m[i] = (int)v[i];
-      }
-    } else {
-      const uint4* wp = reinterpret_cast<const uint4*>(w + ((size_t)min(n0 + r, a.N - 1) * a.wb + p) * kF8Block + 32 * g);
-      m = f8_pair(wp[0], wp[1]);
+      for (int z = 0; z < 4; ++z)
+        v |= (uint32_t)w[(size_t)min(p * kF8Block + 32 * g + 4 * i + z, a.K - 1) * a.wb * kF8Block + n0 + r] << (8 * z);
+      m[i] = (int)v;
     }
-    const float s = xs[p] * ws[BACK ? (size_t)p * a.wb + n0 / kF8Block : (size_t)(n0 / kF8Block) * a.wb + p];
+    const float s = a.xf[(size_t)row * a.xb + p] * ws[(size_t)p * a.wb + n0 / kF8Block];
     const floatx4_t c = f8_products<EXACT>(m, f8_pair(xp[0], xp[1]));
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = fmaf(c[i], s, acc[i]);
@@ -91,12 +149,20 @@ __global__ __launch_bounds__(256) void rows_product(F8Args a) {
 }  // namespace
 
 hipError_t launch_f8_product(const F8Args& a, hipStream_t s) {
-  if (a.A >= (a.offsets ? 64 : 32) && f8_tiles_can(a)) return launch_f8_tiles(a, s);
-  const dim3 g(a.offsets ? a.A : (a.A + kRows - 1) / kRows, (a.N + 15) / 16);
-  if (a.back && a.exact) MOE_LAUNCH("f8_rows_back", s, (rows_product<true, true>), g, dim3(256), 0, s, a);
-  else if (a.back) MOE_LAUNCH("f8_rows_back", s, (rows_product<true, false>), g, dim3(256), 0, s, a);
-  else if (a.exact) MOE_LAUNCH("f8_rows", s, (rows_product<false, true>), g, dim3(256), 0, s, a);
-  else MOE_LAUNCH("f8_rows", s, (rows_product<false, false>), g, dim3(256), 0, s, a);
+  if ((a.back || a.offsets || a.A >= 32) && f8_tiles_can(a)) return launch_f8_tiles(a, s);
+  const int units = a.offsets ? a.A : (a.A + kRows - 1) / kRows;
+  if (a.back) {
+    const dim3 g(units, (a.N + 15) / 16);
+    if (a.exact) MOE_LAUNCH("f8_rows_back", s, rows_back<true>, g, dim3(256), 0, s, a);
+    else MOE_LAUNCH("f8_rows_back", s, rows_back<false>, g, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  const bool narrow = (long long)units * ((a.N + 31) / 32) * 2 <= device_cus();
+  const dim3 g(units, narrow ? (a.N + 15) / 16 : (a.N + 31) / 32);
+  if (a.exact && narrow) MOE_LAUNCH("f8_rows", s, (rows_product<true, 1>), g, dim3(256), 0, s, a);
+  else if (a.exact) MOE_LAUNCH("f8_rows", s, (rows_product<true, 2>), g, dim3(256), 0, s, a);
+  else if (narrow) MOE_LAUNCH("f8_rows", s, (rows_product<false, 1>), g, dim3(256), 0, s, a);
+  else MOE_LAUNCH("f8_rows", s, (rows_product<false, 2>), g, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

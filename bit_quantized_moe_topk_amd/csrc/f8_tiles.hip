@@ -17,7 +17,7 @@
 namespace moe {
 namespace {
 
-constexpr int kBufs = 3;
+constexpr int kBufs = 3;  // (of strips of 128 results too)
 constexpr int kThreads = 512;
 constexpr int kRun = 16;  // rows of a product
 
@@ -338,16 +338,20 @@ bool f8_tiles_can(const F8Args& a) {
 }
 
 hipError_t launch_f8_tiles(F8Args a, hipStream_t s) {
-  constexpr int strip = 256;
-  const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * ((a.N + strip - 1) / strip);
   const int cap = device_cus();
+  const int strip = mx4_row_tiles(a) * ((a.N + 255) / 256) < cap ? 128 : 256;
+  const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * ((a.N + strip - 1) / strip);
   const dim3 g((unsigned)(most < cap ? most : cap));
   if (most <= cap || g.x % kXcds) a.counter = nullptr;
   else if (a.counter) launch_mx4_zero(a.counter, s);
-  if (a.back && a.exact) MOE_LAUNCH("f8_tiles_back", s, (f8_tiles<true, true, 4>), g, dim3(kThreads), 0, s, a);
-  else if (a.back) MOE_LAUNCH("f8_tiles_back", s, (f8_tiles<true, false, 4>), g, dim3(kThreads), 0, s, a);
-  else if (a.exact) MOE_LAUNCH("f8_tiles", s, (f8_tiles<false, true, 4>), g, dim3(kThreads), 0, s, a);
-  else MOE_LAUNCH("f8_tiles", s, (f8_tiles<false, false, 4>), g, dim3(kThreads), 0, s, a);
+#define TILES(BACK, EXACT, NAME) \
+  if (strip == 256) MOE_LAUNCH(NAME, s, (f8_tiles<BACK, EXACT, 4>), g, dim3(kThreads), 0, s, a); \
+  else MOE_LAUNCH(NAME "_128", s, (f8_tiles<BACK, EXACT, 2>), g, dim3(kThreads), 0, s, a)
+  if (a.back && a.exact) { TILES(true, true, "f8_tiles_back"); }
+  else if (a.back) { TILES(true, false, "f8_tiles_back"); }
+  else if (a.exact) { TILES(false, true, "f8_tiles"); }
+  else { TILES(false, false, "f8_tiles"); }
+#undef TILES
   return hipGetLastError();
 }
 

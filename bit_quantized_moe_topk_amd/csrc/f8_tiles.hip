@@ -17,14 +17,18 @@
 namespace moe {
 namespace {
 
-constexpr int kBufs = 3;  // (of strips of 128 results too)
+constexpr int kWBufs = 3;
+// Buffers of rows: as many as LDS has room for. Products between one and the addition of its sum: as many as registers hold.
+constexpr int xbufs(int TM) { return TM <= 128 ? 3 : 2; }
+constexpr int lag(int TM) { return TM <= 128 ? 4 : 2; }
 constexpr int kThreads = 512;
 constexpr int kRun = 16;  // rows of a product
 
-template <int WN>
-struct Buf8 {
-  uint4 x[kTM * 8];        // row m: its eight chunks of 16 codes, as chunk_at places them
-  uint4 w[64 * WN * 8];    // matrix row n likewise; turned: contraction row c, its 4 WN chunks of 16 columns (turned_at)
+template <int WN, int TM>
+struct Bufs8 {
+  uint4 w[kWBufs][64 * WN * 8];  // matrix row n: its eight chunks of 16 codes, as chunk_at places them; turned: contraction
+                                 // row c, its 4 WN chunks of 16 columns (turned_at)
+  uint4 x[xbufs(TM)][TM * 8];       // row m, as chunk_at places it
 };
 
 // A lane's 32 codes of a row of 128 are chunks g and g + 4, g = l / 16. (A 16-byte read serves lanes 0-3, 12-15 and 20-27 at
@@ -93,18 +97,19 @@ __device__ inline float uniform_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
-template <bool BACK, bool EXACT, int WN>
+template <bool BACK, bool EXACT, int WN, int TM>
 __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
-  constexpr int kRuns = WN;             // runs of 16 rows a wave
-  constexpr int kWL = WN;               // loads of the matrix a wave and step, 1 KB each
-  constexpr int kLoads = 2 + kWL + 1;   // and of rows and their scales
+  constexpr int kRuns = TM / kRun * WN / 8;  // runs of rows a wave
+  constexpr int kWL = WN;                    // loads of the matrix a wave and step, 1 KB each
+  constexpr int kXR = TM / 8, kXL = kXR / 8;  // rows that a wave loads, and its loads of them
+  constexpr int kXBufs = xbufs(TM), kLag = lag(TM);
   constexpr int strip = 64 * WN;
-  __shared__ Buf8<WN> buf[kBufs];
-  __shared__ float scale[kBufs][kTM];
+  __shared__ Bufs8<WN, TM> buf;
+  __shared__ float scale[kXBufs][TM];
   __shared__ Tiles tiles;
   __shared__ int slot;
   const int strips = (a.N + strip - 1) / strip;
-  const int items = tiles_init(tiles, *reinterpret_cast<TilesScratch*>(buf), a) * strips;
+  const int items = tiles_init<TM>(tiles, *reinterpret_cast<TilesScratch*>(&buf), a) * strips;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4, wn = wave % WN, wm = wave / WN;
   const int P = max(a.xb, 3);  // (a short contraction has empty steps: loads run three ahead, into the next tile at most)
@@ -115,22 +120,26 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
   deal.ask();
   int next = deal.answer(item);
 
-  // load cursor: rows 16 wave + 8 u + l / 8 of the tile, the chunk that belongs at position l % 8; row 16 wave + l % 16 of
-  // the scales; matrix rows 8 (WN wave + u) + l / 8, or the columns of a contraction row (offsets of a lane, bases of all)
-  uint32_t xoff[2], woff[kWL], soff;
+  // Two load cursors, of rows and of the matrix, the latter a step ahead. Rows: 8 of kXR wave .. a load, lane l / 8's, the chunk
+  // that belongs at position l % 8; a row's scale a lane. Matrix: rows 8 (WN wave + u) + l / 8, or the columns of a contraction
+  // row. Offsets of a lane, bases of all.
+  uint32_t xoff[kXL], woff[kWL], soff;
   const uint8_t* wbase;
-  int lp = 0, row_next[3];
-  auto row_of = [&](int u) { return u < 2 ? 16 * wave + 8 * u + (lane >> 3) : 16 * wave + r; };
+  int xq = 0, wq = 0, row_next[kXL + 1];
+  auto row_of = [&](int u) { return kXR * wave + (u < kXL ? 8 * u + (lane >> 3) : min(lane, kXR - 1)); };
   auto fetch_rows = [&](const TileInfo& t) {  // the row numbers of a tile, to be used later
 #pragma unroll
-    for (int u = 0; u < 3; ++u) row_next[u] = max(mx4_row(a, t.s0 + min(row_of(u), t.M - 1)), 0);
+    for (int u = 0; u <= kXL; ++u) row_next[u] = max(mx4_row(a, t.s0 + min(row_of(u), t.M - 1)), 0);
   };
   const uint32_t xrow = (uint32_t)a.xb * kF8Block, wrow = (uint32_t)a.wb * kF8Block;
   auto turned_row = [&](int u) { return 16 * wave + 16 / kWL * u + lane / (4 * WN); };
-  auto aim = [&](const TileInfo& t) {
+  auto aim_rows = [&]() {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) xoff[u] = (uint32_t)row_next[u] * xrow + 16 * ((lane & 7) ^ ((row_of(u) >> 1) & 7));
-    soff = (uint32_t)row_next[2] * (uint32_t)a.xb * 4u;
+    for (int u = 0; u < kXL; ++u) xoff[u] = (uint32_t)row_next[u] * xrow + 16 * ((lane & 7) ^ ((row_of(u) >> 1) & 7));
+    soff = (uint32_t)row_next[kXL] * (uint32_t)a.xb * 4u;
+    xq = 0;
+  };
+  auto aim_matrix = [&](const TileInfo& t) {
     wbase = a.wc + (size_t)t.e * stored * wrow;
 #pragma unroll
     for (int u = 0; u < kWL; ++u) {
@@ -142,40 +151,51 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
         woff[u] = (uint32_t)min(t.n0 + n, a.N - 1) * wrow + 16 * ((lane & 7) ^ ((n >> 1) & 7));
       }
     }
-    lp = 0;
+    wq = 0;
   };
-  auto load = [&](int b) __attribute__((always_inline)) {
-    Buf8<WN>& B = buf[b];
-    const int p = min(lp, a.xb - 1);
+  auto load_rows = [&](int at) __attribute__((always_inline)) {
+    const int p = min(xq, a.xb - 1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-      stream16(static_cast<const uint8_t*>(a.x) + p * kF8Block, xoff[u], lds_offset(B.x) + 1024 * (2 * wave + u));
+    for (int u = 0; u < kXL; ++u)
+      stream16(static_cast<const uint8_t*>(a.x) + p * kF8Block, xoff[u], lds_offset(buf.x[at]) + 1024 * (kXL * wave + u));
+    if (lane < kXR) stream4(a.xf + p, soff, lds_offset(scale[at]) + 4 * kXR * wave);
+    ++xq;
+  };
+  auto load_matrix = [&](int at) __attribute__((always_inline)) {
+    const int p = min(wq, a.xb - 1);
 #pragma unroll
     for (int u = 0; u < kWL; ++u) {
       if constexpr (BACK)
-        stream16(wbase, woff[u] + (uint32_t)min(p * kF8Block + turned_row(u), a.K - 1) * wrow, lds_offset(B.w) + 1024 * (kWL * wave + u));
+        stream16(wbase, woff[u] + (uint32_t)min(p * kF8Block + turned_row(u), a.K - 1) * wrow, lds_offset(buf.w[at]) + 1024 * (kWL * wave + u));
       else
-        stream16(wbase + p * kF8Block, woff[u], lds_offset(B.w) + 1024 * (kWL * wave + u));
+        stream16(wbase + p * kF8Block, woff[u], lds_offset(buf.w[at]) + 1024 * (kWL * wave + u));
     }
-    if (lane < 16) stream4(a.xf + p, soff, lds_offset(scale[b]) + 64 * wave);
-    ++lp;
+    ++wq;
+  };
+  // A step asks for rows kXBufs steps on, then for the matrix three steps on: all but the loads of three steps on have landed,
+  // and every wave has come here.
+  auto done = [](bool loads) __attribute__((always_inline)) {
+    if (loads) step_done<kWL + (kXBufs == 3 ? kXL + 1 : 0)>();
+    else step_done();
   };
 
-  int b = 0;
-  TileInfo t = tile_of<kTM, kRun>(tiles, a, item, items, strips, strip), tn = t;
+  int b = 0, x = 0;  // the running step's buffers
+  TileInfo t = tile_of<TM, kRun>(tiles, a, item, items, strips, strip), tn = t;
   fetch_rows(t);
-  aim(t);
-  load(0);
-  load(1);
-  load(2);
-  // (what has landed where a tile begins: steps 0 and 1, or with EXACT step 0)
-  if (EXACT) step_done<2 * kLoads>();
-  else step_done<kLoads>();
+  aim_rows();
+  aim_matrix(t);
+  load_rows(0);
+  load_rows(1);
+  if (kXBufs == 3) load_rows(2);
+  load_matrix(0);
+  load_matrix(1);
+  load_matrix(2);
+  step_done<kWL>();
   for (;;) {
     const bool more = next < items;
     if (more) {
       deal.ask();
-      tn = tile_of<kTM, kRun>(tiles, a, next, items, strips, strip);
+      tn = tile_of<TM, kRun>(tiles, a, next, items, strips, strip);
       fetch_rows(tn);
     }
     // this wave's runs of rows: all runs, dealt over the waves down
@@ -197,13 +217,12 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
         for (int i = 0; i < L; ++i) o.s[i] = scale[at][kRun * (run0 + i) + r];
       };
       auto read_w = [&](Operands<L>& o, int at, int j) __attribute__((always_inline)) {
-        const Buf8<WN>& B = buf[at];
         if constexpr (BACK) {
           typedef int v2i __attribute__((ext_vector_type(2)));
 #pragma unroll
           for (int z = 0; z < 4; ++z) {
             const int c = 16 * g + 8 * (z & 1) + 64 * (z >> 1) + (r >> 1);
-            const char* from = reinterpret_cast<const char*>(B.w + turned_at<WN>(c, 4 * wn + j)) + 8 * (r & 1);
+            const char* from = reinterpret_cast<const char*>(buf.w[at] + turned_at<WN>(c, 4 * wn + j)) + 8 * (r & 1);
             const v2i u = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
                 (__attribute__((address_space(3))) v2i*)(__attribute__((address_space(3))) char*)const_cast<char*>(from));
             o.w[j][2 * z] = u[0];
@@ -211,53 +230,54 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
           }
         } else {
           const int n = 64 * wn + 16 * j + r;
-          o.w[j] = f8_pair(B.w[chunk_at(n, g)], B.w[chunk_at(n, g + 4)]);
+          o.w[j] = f8_pair(buf.w[at][chunk_at(n, g)], buf.w[at][chunk_at(n, g + 4)]);
         }
       };
       auto read_x = [&](Operands<L>& o, int at, int i) __attribute__((always_inline)) {
         const int m = kRun * (run0 + i) + r;
-        o.x[i] = f8_pair(buf[at].x[chunk_at(m, g)], buf[at].x[chunk_at(m, g + 4)]);
+        o.x[i] = f8_pair(buf.x[at][chunk_at(m, g)], buf.x[at][chunk_at(m, g + 4)]);
       };
       float sw = 0.f;
       const float* wp = ws;
-      // Step p, while the next step's operands take the places of those that are used up and the load three steps on is
-      // on its way. A block's sum is brought into its accumulator two products later, when it is there.
+      // Step p, while the next step's operands take the places of those that are used up and loads are on their way. A
+      // block's sum is brought into its accumulator kLag products later, when it is there.
       Operands<L> o;
       auto step = [&](int p, bool loads) __attribute__((always_inline)) {
-        const int b1 = b == 2 ? 0 : b + 1;
+        const int b1 = b == kWBufs - 1 ? 0 : b + 1;
         float f[L > 0 ? L : 1];
 #pragma unroll
         for (int i = 0; i < L; ++i) f[i] = p < a.xb ? o.s[i] * sw : 0.f;
-        if (loads) load(b);
+        if (loads || p + kXBufs < P) load_rows(x);
+        if (loads) load_matrix(b);
+        x = x == kXBufs - 1 ? 0 : x + 1;
         if constexpr (L > 0) {
           if (p + 1 < a.xb) wp += wstep;
           sw = uniform_load(wp);
-          read_scales(o, b1);
+          read_scales(o, x);
           __builtin_amdgcn_sched_barrier(0);
-          floatx4_t c[3];
+          floatx4_t c[kLag + 1];
 #pragma unroll
-          for (int k = 0; k < 4 * L + 2; ++k) {
-            if (k < 4 * L) c[k % 3] = f8_products<false>(o.w[k % 4], o.x[k / 4]);
+          for (int k = 0; k < 4 * L + kLag; ++k) {
+            if (k < 4 * L) c[k % (kLag + 1)] = f8_products<false>(o.w[k % 4], o.x[k / 4]);
             if (k < 4 * L && k >= 4 * L - 4) read_w(o, b1, k % 4);
-            if (k < 4 * L && k % 4 == 3) read_x(o, b1, k / 4);
-            if (k >= 2) {
-              const int i = (k - 2) / 4, j = (k - 2) % 4;
+            if (k < 4 * L && k % 4 == 3) read_x(o, x, k / 4);
+            if (k >= kLag) {
+              const int i = (k - kLag) / 4, j = (k - kLag) % 4;
 #pragma unroll
-              for (int z = 0; z < 4; ++z) acc[i][j][z] = fmaf(c[(k - 2) % 3][z], f[i], acc[i][j][z]);
+              for (int z = 0; z < 4; ++z) acc[i][j][z] = fmaf(c[(k - kLag) % (kLag + 1)][z], f[i], acc[i][j][z]);
+              asm volatile("" : "+v"(acc[i][j]));  // here, not past the step's end, where the compiler moves it with all the sums
             }
             __builtin_amdgcn_sched_barrier(0);
           }
         }
-        // the loads of the step after next have landed; this step's may be in flight
-        if (loads) step_done<kLoads>();
-        else step_done();
+        done(loads);
         b = b1;
       };
       // The same with bf16 products: codes become bf16 as they are read, which leaves no registers for a second set; the
       // step's buffer is loaded again when every wave has read it.
       auto step_exact = [&](int p) __attribute__((always_inline)) {
         if (L > 0 && p < a.xb) {
-          read_scales(o, b);
+          read_scales(o, x);
           const float swp = uniform_load(wp);
           wp += wstep;
           bf16x8_t w[4][4];
@@ -269,50 +289,56 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
           }
 #pragma unroll
           for (int i = 0; i < L; ++i) {
-            read_x(o, b, i);
-            bf16x8_t x[4];
+            read_x(o, x, i);
+            bf16x8_t v[4];
 #pragma unroll
-            for (int z = 0; z < 4; ++z) x[z] = f8_bf16(o.x[i][2 * z], o.x[i][2 * z + 1]);
+            for (int z = 0; z < 4; ++z) v[z] = f8_bf16(o.x[i][2 * z], o.x[i][2 * z + 1]);
             const float f = o.s[i] * swp;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               floatx4_t c = {};
 #pragma unroll
-              for (int z = 0; z < 4; ++z) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][z], x[z], c, 0, 0, 0);
+              for (int z = 0; z < 4; ++z) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j][z], v[z], c, 0, 0, 0);
 #pragma unroll
               for (int z = 0; z < 4; ++z) acc[i][j][z] = fmaf(c[z], f, acc[i][j][z]);
             }
           }
         }
-        if (p + 2 < P || more) step_done<kLoads>();
-        else step_done();
-        if (p + 3 == P && more) aim(tn);
-        if (p + 3 < P || more) load(b);
-        b = b == 2 ? 0 : b + 1;
+        done(p + 2 < P || more);
+        if (p + kXBufs == P && more) aim_rows();
+        if (p + kXBufs < P || more) load_rows(x);
+        if (p + 3 == P && more) aim_matrix(tn);
+        if (p + 3 < P || more) load_matrix(b);
+        b = b == kWBufs - 1 ? 0 : b + 1;
+        x = x == kXBufs - 1 ? 0 : x + 1;
       };
       if constexpr (EXACT) {
         for (int p = 0; p < P; ++p) step_exact(p);
       } else {
         if constexpr (L > 0) {
           sw = uniform_load(wp);
-          read_scales(o, b);
+          read_scales(o, x);
 #pragma unroll
           for (int j = 0; j < 4; ++j) read_w(o, b, j);
 #pragma unroll
-          for (int i = 0; i < L; ++i) read_x(o, b, i);
+          for (int i = 0; i < L; ++i) read_x(o, x, i);
         }
         // every wave has read its first operands before their buffer is loaded again
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // (one loop: a second one for the last steps had the accumulators in other registers, and copies between)
 #pragma nounroll
-        for (int p = 0; p < P - 3; ++p) step(p, true);
-        if (more) aim(tn);
-#pragma nounroll
-        for (int p = P - 3; p < P; ++p) step(p, more);
+        for (int p = 0; p < P; ++p) {
+          if (p + 3 == P && more) aim_matrix(tn);
+          if (p + kXBufs == P && more) aim_rows();
+          step(p, p + 3 < P || more);
+        }
       }
     };
-    if (live == 4) run(std::integral_constant<int, kRuns < 4 ? 0 : 4>{});
-    else if (live == 3) run(std::integral_constant<int, kRuns < 3 ? 0 : 3>{});
-    else if (live == 2) run(std::integral_constant<int, kRuns < 2 ? 0 : 2>{});
+    if (kRuns >= 6 && live == 6) run(std::integral_constant<int, kRuns >= 6 ? 6 : 0>{});
+    else if (kRuns >= 5 && live == 5) run(std::integral_constant<int, kRuns >= 5 ? 5 : 0>{});
+    else if (kRuns >= 4 && live == 4) run(std::integral_constant<int, kRuns >= 4 ? 4 : 0>{});
+    else if (kRuns >= 3 && live == 3) run(std::integral_constant<int, kRuns >= 3 ? 3 : 0>{});
+    else if (live == 2) run(std::integral_constant<int, 2>{});
     else if (live == 1) run(std::integral_constant<int, 1>{});
     else run(std::integral_constant<int, 0>{});
     const bool wide = a.N % (a.ydtype == 1 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
@@ -340,13 +366,17 @@ bool f8_tiles_can(const F8Args& a) {
 hipError_t launch_f8_tiles(F8Args a, hipStream_t s) {
   const int cap = device_cus();
   const int strip = mx4_row_tiles(a) * ((a.N + 255) / 256) < cap ? 128 : 256;
-  const long long most = ((long long)(a.A + kTM - 1) / kTM + (a.offsets ? a.E_tot : 0)) * ((a.N + strip - 1) / strip);
+  const long long groups = a.offsets ? (a.A < a.E_tot ? a.A : a.E_tot) : 1, strips = (a.N + strip - 1) / strip;
+  const bool tall = strip == 256 && a.offsets && a.A > 112 * groups;
+  const int tm = tall ? 192 : 128;
+  const long long most = ((long long)(a.A + tm - 1) / tm + (a.offsets ? a.E_tot : 0)) * strips;
   const dim3 g((unsigned)(most < cap ? most : cap));
   if (most <= cap || g.x % kXcds) a.counter = nullptr;
   else if (a.counter) launch_mx4_zero(a.counter, s);
 #define TILES(BACK, EXACT, NAME) \
-  if (strip == 256) MOE_LAUNCH(NAME, s, (f8_tiles<BACK, EXACT, 4>), g, dim3(kThreads), 0, s, a); \
-  else MOE_LAUNCH(NAME "_128", s, (f8_tiles<BACK, EXACT, 2>), g, dim3(kThreads), 0, s, a)
+  if (tall) MOE_LAUNCH(NAME "_192", s, (f8_tiles<BACK, EXACT, 4, 192>), g, dim3(kThreads), 0, s, a); \
+  else if (strip == 256) MOE_LAUNCH(NAME, s, (f8_tiles<BACK, EXACT, 4, 128>), g, dim3(kThreads), 0, s, a); \
+  else MOE_LAUNCH(NAME "_strip128", s, (f8_tiles<BACK, EXACT, 2, 128>), g, dim3(kThreads), 0, s, a)
   if (a.back && a.exact) { TILES(true, true, "f8_tiles_back"); }
   else if (a.back) { TILES(true, false, "f8_tiles_back"); }
   else if (a.exact) { TILES(false, true, "f8_tiles"); }

@@ -42,21 +42,20 @@ struct F8Args : Mx4Args {
   bool exact;       // products on the bf16 matrix cores (results that stay in float32)
 };
 
-// The scale for x of a block, and the float32 quotient of v by it, exact but for its last bit, which
-// is set where the quotient is not exact: so rounding it to a code rounds the exact quotient. (Two
-// steps bring v * inv to within one unit of it; the remainder's sign says on which side it lies.)
+// The scale of a block whose largest magnitude is `top`.
 __device__ inline float f8_scale_of(float top) { return fmaxf(top, kF8Least) / 448.f; }
 
+// A float32 number that rounds to the code that the exact quotient of v by s rounds to. Two steps bring |v| * inv to within
+// one unit of it; the sign of the exact remainder says on which side it lies. A border between two codes has an even last bit, so
+// an odd number is on its own side of all of them, and an even one goes one unit towards the quotient (nine instructions in all).
 __device__ inline float f8_quotient(float v, float s, float inv) {
-  float q = v * inv;
-  q = fmaf(fmaf(-q, s, v), inv, q);
-  const float r = fmaf(-q, s, v);
-  uint32_t u = __float_as_uint(q);
-  if (r != 0.f && fabsf(q) >= 0x1p-11f) {  // (below, the code is 0)
-    if ((r < 0.f) != (q < 0.f)) --u;
-    u |= 1u;
-  }
-  return __builtin_copysignf(__uint_as_float(u), v);  // (a zero keeps its sign)
+  const float m = fabsf(v);
+  float q = m * inv;
+  q = fmaf(fmaf(-q, s, m), inv, q);
+  const int r = __float_as_int(fmaf(-q, s, m)), u = __float_as_int(q);
+  const int towards = max(min(r, 1), -1);  // -1, 0, 1 as the remainder's sign (a zero is +0)
+  const float c = __int_as_float(u + (towards & ((u & 1) - 1)));
+  return __builtin_copysignf(c, v);  // (a zero keeps its sign)
 }
 
 // The codes of eight values of a block whose largest magnitude is `top` (bits, ordered as
@@ -67,14 +66,18 @@ __device__ inline uint2 f8_codes(const float (&f)[8], uint32_t top, float* scale
     *scale = __uint_as_float(0x7FC00000u);
     return make_uint2(0u, 0u);
   }
-  float s = f8_scale_of(__uint_as_float(top));
+  float s = f8_scale_of(__uint_as_float(top)), q[8];
   *scale = s;
-  const float up = top < 0x2B800000u ? 0x1p80f : 1.f;
-  s *= up;
-  const float inv = 1.f / s;
-  float q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(f[i] * up, s, inv);
+  for (int i = 0; i < 8; ++i) q[i] = f[i];
+  if (top < 0x2B800000u) {
+    s *= 0x1p80f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] *= 0x1p80f;
+  }
+  const float inv = 1.f / s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = f8_quotient(q[i], s, inv);
   int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
   lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
   int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);

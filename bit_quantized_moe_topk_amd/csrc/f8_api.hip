@@ -85,7 +85,8 @@ int moe_fp8_quantize(const void* x, int32_t xdtype, int64_t ld, int32_t mats, in
   if (K > kMaxDim || ld > kMaxLd || (long long)mats * rows > 0x7FFFFFFFLL) return MOE_ERR_UNSUPPORTED;
   if (mats == 0 || rows == 0) return MOE_OK;
   const long long of = block_rows == 1 ? (long long)mats * rows : (long long)mats * moe::f8_blocks(rows);
-  if (of * moe::f8_blocks(K) > 0x7FFFFFFFLL && block_rows == 128) return MOE_ERR_UNSUPPORTED;
+  // a workgroup a matrix block, and at most 2^32 threads a launch
+  if (block_rows == 128 && of * moe::f8_blocks(K) >= 1 << 24) return MOE_ERR_UNSUPPORTED;
   if (!x || !codes || !scales || !aligned(x, size_of(xdtype)) || !aligned(codes, 16) || !aligned(scales, 4))
     return MOE_ERR_INVALID_ARG;
   const u64 cb = row_bytes((long long)mats * rows, K), sb = (u64)of * moe::f8_blocks(K) * sizeof(float);

@@ -148,16 +148,26 @@ __global__ __launch_bounds__(256) void rows_back(F8Args a) {
 
 }  // namespace
 
+// Rows or tiles: the rows' kernel reads the matrix again for every 16 rows and has a group's rows in one workgroup each, tiles
+// take twice as long for one. So rows where there are at most two workgroups of 32 results a CU, and up to 256 rows. Measured, rows against tiles:
+// one matrix [1024, 2048], 32 rows (64 workgroups) 5.1 us against 10.9, 128 (256) 7.2 against 13.6; [8192, 8192], 32 rows
+// (512) 33 against 37, 64 (1,024) 68 against 42; [4096, 1024], 64 rows (512) 9.1 against 8.4, 96 (768) 12.5 against 9.5; experts
+// [1024, 2048], 11 rows (352) 9.1 against 15.6, 44 (1,408) 20 against 25; [2048, 512], 5 rows (320) 8.1 against 9.9, 22
+// (1,408) 18 against 12.8. The turned matrix is always on tiles, which transpose as they read; rows_back, which gathers bytes, is
+// for what they cannot address.
+// Workgroups of 16 results, narrow, where even those leave CUs over: [4096, 1024], 16 rows (128 of 32) 4.3 us against 5.2, 32
+// rows (256) 7.5 against 5.8.
 hipError_t launch_f8_product(const F8Args& a, hipStream_t s) {
-  if ((a.back || a.offsets || a.A >= 32) && f8_tiles_can(a)) return launch_f8_tiles(a, s);
   const int units = a.offsets ? a.A : (a.A + kRows - 1) / kRows;
+  const long long groups32 = (long long)units * ((a.N + 31) / 32);
+  if ((a.back || a.A > 256 || groups32 > 2 * device_cus()) && f8_tiles_can(a)) return launch_f8_tiles(a, s);
   if (a.back) {
     const dim3 g(units, (a.N + 15) / 16);
     if (a.exact) MOE_LAUNCH("f8_rows_back", s, rows_back<true>, g, dim3(256), 0, s, a);
     else MOE_LAUNCH("f8_rows_back", s, rows_back<false>, g, dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  const bool narrow = (long long)units * ((a.N + 31) / 32) * 2 <= device_cus();
+  const bool narrow = groups32 * 2 <= device_cus();
   const dim3 g(units, narrow ? (a.N + 15) / 16 : (a.N + 31) / 32);
   if (a.exact && narrow) MOE_LAUNCH("f8_rows", s, (rows_product<true, 1>), g, dim3(256), 0, s, a);
   else if (a.exact) MOE_LAUNCH("f8_rows", s, (rows_product<true, 2>), g, dim3(256), 0, s, a);

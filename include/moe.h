@@ -540,7 +540,8 @@ int moe_route_scores_backward(const void *logits, int32_t dtype, int64_t ld, int
  * (matrices). scale = max(largest magnitude of the block, 2^-116) / 448 in float32;
  * code = x / scale, the exact quotient rounded once to the nearest code, ties to
  * the even one; zeros keep their sign. A block that holds a NaN or an infinity becomes
- * NaN (scale NaN, codes 0). mats == 0 or rows == 0: no launch. */
+ * NaN (scale NaN, codes 0). Matrices of 2^24 blocks and more together: MOE_ERR_UNSUPPORTED.
+ * mats == 0 or rows == 0: no launch. */
 int moe_fp8_quantize(const void *x, int32_t xdtype, int64_t ld, int32_t mats, int32_t rows, int32_t K,
                      int32_t block_rows, uint8_t *codes, float *scales, void *stream);
 
@@ -555,7 +556,9 @@ int moe_fp8_dequantize(const uint8_t *codes, const float *scales, int32_t mats, 
  * run). For MOE_F32 results every product of two codes is exact and their sum is float32; for
  * MOE_BF16 the 8-bit matrix cores add up a block's 128 products, which drop what
  * lies under 2^-13 of the binade of the block's largest product (far below bf16's own step
- * for values of like size). T == 0: no launch. */
+ * for values of like size). A block's sum is multiplied by the float32 product of its two scales, so
+ * blocks whose largest values' product passes 2^145 give infinities or NaN, and where it is
+ * below 2^-108 lose bits. T == 0: no launch. */
 int moe_fp8_matmul(const uint8_t *x_codes, const float *x_scales, int32_t T, const uint8_t *w_codes,
                    const float *w_scales, int32_t N, int32_t K, void *y, int32_t ydtype, void *stream);
 
@@ -609,7 +612,8 @@ int moe_fp8_experts_matmul_backward(const uint8_t *dy_codes, const float *dy_sca
  * [H], MOE_F32 or MOE_BF16 (wdtype); total, y: [T][H], rows H elements apart. One of total,
  * y and codes at least is written. total may be x or residual themselves where their
  * rows are H apart. Sums are float32 in a fixed order. A row whose squares
- * pass float32's range has mean infinity and gives 0 (and NaN where r is infinite);
+ * pass float32's range has mean infinity and gives 0 (and NaN where r is infinite); squares
+ * below it count as 0, and with eps 0 a row of nothing else gives infinities and NaN;
  * a NaN makes its whole row NaN. H <= MOE_MAX_NORM_H, T <= 2^22 (else
  * MOE_ERR_UNSUPPORTED), eps >= 0 and finite. T == 0: no launch. */
 int moe_rms_norm(const void *x, int32_t dtype, int64_t ldx, const void *residual, int64_t ldr,

@@ -37,6 +37,8 @@ def test_quantize_refuses(block):
     # results over the rows, or over each other
     for bad in (dict(codes=AT["x"]), dict(scales=AT["x"] + 16), dict(codes=AT["x"] + 3 * 512), dict(scales=AT["y"] + 16)):
         assert quantize(**{"block": block, **bad}) == INV, bad
+    if block == 128:  # one workgroup a block: no more than a launch holds
+        assert quantize(block=128, mats=1 << 24, rows=1, K=1) == UNS and quantize(block=128, mats=1 << 23, rows=1, K=129) == UNS
     assert quantize(rows=0, x=0, codes=0, scales=0) == OK and quantize(mats=0, x=0, codes=0, scales=0) == OK
 
 

@@ -10,8 +10,9 @@ from test_gpu_blocks import as64, check, dtype_of, grouping_of, lib, random_fp8
 pytestmark = pytest.mark.gpu
 
 DENSE = [  # kernel, T, N, K of the stored matrix, back
-    ("f8_rows", 16, 40, 700, False), ("f8_rows", 31, 9000, 300, False), ("f8_rows", 1, 300, 2000, False),
-    ("f8_tiles_strip128", 32, 130, 129, False), ("f8_tiles_strip128", 200, 500, 1300, False),
+    ("f8_rows", 16, 40, 700, False), ("f8_tiles_strip128", 31, 9000, 300, False), ("f8_rows", 1, 300, 2000, False),
+    ("f8_rows", 32, 130, 129, False), ("f8_rows", 200, 500, 1300, False), ("f8_rows", 47, 5000, 1300, False),
+    ("f8_tiles_strip128", 20, 8300, 129, False), ("f8_tiles_strip128", 700, 700, 1300, False),
     ("f8_tiles", 2000, 4100, 260, False), ("f8_tiles", 4097, 2048, 130, False), ("f8_tiles", 8300, 1030, 100, False),
     ("f8_tiles_back_strip128", 1, 300, 130, True), ("f8_tiles_back_strip128", 150, 1300, 500, True),
     ("f8_tiles_back", 2000, 260, 4100, True), ("f8_tiles_back", 4097, 130, 2048, True), ("f8_tiles_back", 8300, 100, 1030, True)]
@@ -51,7 +52,8 @@ def test_dense(case, kind):
 
 
 GROUPED = [  # kernel, T, k, E, shared, N, K, back
-    ("f8_tiles_strip128", 3, 2, 9, True, 130, 260, False), ("f8_tiles_strip128", 300, 4, 6, False, 384, 640, False),
+    ("f8_rows", 3, 2, 9, True, 130, 260, False), ("f8_rows", 30, 1, 2, False, 530, 700, False),
+    ("f8_tiles_strip128", 3, 2, 9, True, 2000, 260, False), ("f8_tiles_strip128", 300, 4, 6, False, 384, 640, False),
     ("f8_tiles", 900, 2, 40, True, 2300, 200, False), ("f8_tiles_192", 900, 3, 16, True, 3100, 200, False),
     ("f8_tiles_192", 1500, 2, 20, False, 3000, 400, False),
     ("f8_tiles_back_strip128", 3, 2, 9, True, 130, 260, True), ("f8_tiles_back_strip128", 300, 4, 6, False, 384, 640, True),

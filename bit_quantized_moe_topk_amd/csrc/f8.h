@@ -98,42 +98,72 @@ __device__ inline uint32_t f8_top16(const float (&f)[8]) {
   return max(top, dpp(top, 0x140));
 }
 
-// Eight values from column c of a row of n in either type (zeros past n). vec: 16-byte loads.
+// Sixteen bytes at any element's address (global memory takes them there; a line more at times is all that it costs:
+// [6853, 512] x [1330, 512] 44.7 us by elements, 19.9 so).
+typedef uint32_t any16_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef float any16f_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight values from column c of a row of n in either type (zeros past n).
 template <bool BF>
-__device__ inline void load8(const void* __restrict__ row, int c, int n, bool vec, float (&f)[8]) {
+__device__ inline void load8(const void* __restrict__ row, int c, int n, float (&f)[8]) {
   if constexpr (BF) {
-    const uint4 u = load8_bf16(static_cast<const uint16_t*>(row), c, n, vec);
-    f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
-    f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+    const uint16_t* x = static_cast<const uint16_t*>(row) + c;
+    if (c + 8 <= n) {
+      const any16_t u = *reinterpret_cast<const any16_t*>(x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(u[i]);
+        f[2 * i + 1] = bf16_hi(u[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c + i < n ? bf16_lo(x[i]) : 0.f;
+    }
   } else {
-    load8_f32(static_cast<const float*>(row), c, n, vec, f);
+    const float* x = static_cast<const float*>(row) + c;
+    if (c + 8 <= n) {
+      const any16f_t a = *reinterpret_cast<const any16f_t*>(x), b = *reinterpret_cast<const any16f_t*>(x + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[i] = a[i];
+        f[4 + i] = b[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c + i < n ? x[i] : 0.f;
+    }
+  }
+}
+
+// Eight values in bf16, from column c of a row of n on.
+__device__ inline void store8_bf16(uint16_t* y, int c, int n, uint32_t a, uint32_t b, uint32_t d, uint32_t e) {
+  const any16_t p = {a, b, d, e};
+  if (c + 8 <= n) {
+    *reinterpret_cast<any16_t*>(y + c) = p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) y[c + i] = (uint16_t)(p[i / 2] >> (16 * (i & 1)));
+  }
+}
+__device__ inline void store4_f32(float* y, int c, int n, float a, float b, float d, float e) {
+  const any16f_t p = {a, b, d, e};
+  if (c + 4 <= n) {
+    *reinterpret_cast<any16f_t*>(y + c) = p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < n) y[c + i] = p[i];
   }
 }
 
 template <bool BF>
-__device__ inline void store8(void* __restrict__ row, int c, int n, bool vec, const float (&f)[8]) {
+__device__ inline void store8(void* __restrict__ row, int c, int n, const float (&f)[8]) {
   if constexpr (BF) {
-    uint32_t p[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-    uint16_t* y = static_cast<uint16_t*>(row) + c;
-    if (vec && c + 8 <= n) {
-      *reinterpret_cast<uint4*>(y) = make_uint4(p[0], p[1], p[2], p[3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < n) y[i] = (uint16_t)(p[i / 2] >> (16 * (i & 1)));
-    }
+    store8_bf16(static_cast<uint16_t*>(row), c, n, pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
   } else {
-    float* y = static_cast<float*>(row) + c;
-    if (vec && c + 8 <= n) {
-      *reinterpret_cast<float4*>(y) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(y + 4) = make_float4(f[4], f[5], f[6], f[7]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < n) y[i] = f[i];
-    }
+    store4_f32(static_cast<float*>(row), c, n, f[0], f[1], f[2], f[3]);
+    store4_f32(static_cast<float*>(row), c + 4, n, f[4], f[5], f[6], f[7]);
   }
 }
 

@@ -7,7 +7,7 @@ namespace {
 
 // Rows: 16 lanes a block, eight values a lane.
 template <bool BF>
-__global__ __launch_bounds__(256) void quantize_rows(const void* __restrict__ x, long long ld, int rows, int K, bool vec,
+__global__ __launch_bounds__(256) void quantize_rows(const void* __restrict__ x, long long ld, int rows, int K,
                                                      uint8_t* __restrict__ codes, float* __restrict__ scales) {
   const int nb = f8_blocks(K);
   const long long n = (long long)rows * nb * 16;
@@ -15,7 +15,7 @@ __global__ __launch_bounds__(256) void quantize_rows(const void* __restrict__ x,
     const long long r = n <= 0xFFFFFFFFLL ? (long long)((uint32_t)i / (uint32_t)(nb * 16)) : i / (nb * 16);
     const int c = (int)(i - r * (nb * 16)) * 8;
     float f[8], sc;
-    load8<BF>(static_cast<const char*>(x) + r * ld * (BF ? 2 : 4), c, K, vec, f);
+    load8<BF>(static_cast<const char*>(x) + r * ld * (BF ? 2 : 4), c, K, f);
     const uint2 q = f8_codes(f, f8_top16(f), &sc);
     *reinterpret_cast<uint2*>(codes + r * nb * kF8Block + c) = q;
     if ((threadIdx.x & 15) == 0) scales[i >> 4] = sc;
@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256) void quantize_rows(const void* __restrict__ x,
 
 // Matrices: a workgroup a block of 128 x 128; thread (row tid / 16 + 16 j, columns 8 (tid % 16) ..).
 template <bool BF>
-__global__ __launch_bounds__(256) void quantize_matrix(const void* __restrict__ x, long long ld, int rows, int K, bool vec,
+__global__ __launch_bounds__(256) void quantize_matrix(const void* __restrict__ x, long long ld, int rows, int K,
                                                        uint8_t* __restrict__ codes, float* __restrict__ scales) {
   __shared__ uint32_t most[4];
   const int nb = f8_blocks(K), rb = f8_blocks(rows), tid = threadIdx.x;
@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256) void quantize_matrix(const void* __restrict__ 
     const int r = r0 + 16 * j + (tid >> 4);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[j][i] = 0.f;
-    if (r < rows) load8<BF>(static_cast<const char*>(x) + ((long long)mat * rows + r) * ld * (BF ? 2 : 4), c, K, vec, f[j]);
+    if (r < rows) load8<BF>(static_cast<const char*>(x) + ((long long)mat * rows + r) * ld * (BF ? 2 : 4), c, K, f[j]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, magnitude(f[j][i]));
   }
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(256) void quantize_matrix(const void* __restrict__ 
 
 template <bool BF>
 __global__ __launch_bounds__(256) void dequantize(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
-                                                  int mats, int rows, int K, int block_rows, bool vec, void* __restrict__ y) {
+                                                  int mats, int rows, int K, int block_rows, void* __restrict__ y) {
   const int nb = f8_blocks(K), rb = (rows + block_rows - 1) / block_rows;
   const long long n = (long long)mats * rows * nb * 16;
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void dequantize(const uint8_t* __restrict__ co
       f[4 * z + 2] = b.x * s;
       f[4 * z + 3] = b.y * s;
     }
-    store8<BF>(static_cast<char*>(y) + row * K * (BF ? 2 : 4), c, K, vec, f);
+    store8<BF>(static_cast<char*>(y) + row * K * (BF ? 2 : 4), c, K, f);
   }
 }
 
@@ -90,26 +90,24 @@ unsigned blocks_for(long long n) {
 
 hipError_t launch_f8_quantize(const void* x, int xdtype, long long ld, int mats, int rows, int K, int block_rows,
                               uint8_t* codes, float* scales, hipStream_t s) {
-  const bool vec = rows_vec(x, ld, xdtype == 1 ? 2 : 4);
   const int nb = f8_blocks(K);
   if (block_rows == 1) {
     const dim3 g(blocks_for((long long)mats * rows * nb * 16));
-    if (xdtype == 1) MOE_LAUNCH("f8_quantize", s, quantize_rows<true>, g, dim3(256), 0, s, x, ld, mats * rows, K, vec, codes, scales);
-    else MOE_LAUNCH("f8_quantize", s, quantize_rows<false>, g, dim3(256), 0, s, x, ld, mats * rows, K, vec, codes, scales);
+    if (xdtype == 1) MOE_LAUNCH("f8_quantize", s, quantize_rows<true>, g, dim3(256), 0, s, x, ld, mats * rows, K, codes, scales);
+    else MOE_LAUNCH("f8_quantize", s, quantize_rows<false>, g, dim3(256), 0, s, x, ld, mats * rows, K, codes, scales);
   } else {
     const dim3 g((unsigned)((long long)mats * f8_blocks(rows) * nb));
-    if (xdtype == 1) MOE_LAUNCH("f8_quantize_matrix", s, quantize_matrix<true>, g, dim3(256), 0, s, x, ld, rows, K, vec, codes, scales);
-    else MOE_LAUNCH("f8_quantize_matrix", s, quantize_matrix<false>, g, dim3(256), 0, s, x, ld, rows, K, vec, codes, scales);
+    if (xdtype == 1) MOE_LAUNCH("f8_quantize_matrix", s, quantize_matrix<true>, g, dim3(256), 0, s, x, ld, rows, K, codes, scales);
+    else MOE_LAUNCH("f8_quantize_matrix", s, quantize_matrix<false>, g, dim3(256), 0, s, x, ld, rows, K, codes, scales);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_f8_dequantize(const uint8_t* codes, const float* scales, int mats, int rows, int K, int block_rows,
                                 int ydtype, void* y, hipStream_t s) {
-  const bool vec = rows_vec(y, K, ydtype == 1 ? 2 : 4);
   const dim3 g(blocks_for((long long)mats * rows * f8_blocks(K) * 16));
-  if (ydtype == 1) MOE_LAUNCH("f8_dequantize", s, dequantize<true>, g, dim3(256), 0, s, codes, scales, mats, rows, K, block_rows, vec, y);
-  else MOE_LAUNCH("f8_dequantize", s, dequantize<false>, g, dim3(256), 0, s, codes, scales, mats, rows, K, block_rows, vec, y);
+  if (ydtype == 1) MOE_LAUNCH("f8_dequantize", s, dequantize<true>, g, dim3(256), 0, s, codes, scales, mats, rows, K, block_rows, y);
+  else MOE_LAUNCH("f8_dequantize", s, dequantize<false>, g, dim3(256), 0, s, codes, scales, mats, rows, K, block_rows, y);
   return hipGetLastError();
 }
 

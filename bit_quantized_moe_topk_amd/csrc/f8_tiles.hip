@@ -41,7 +41,7 @@ __device__ inline int turned_at(int c, int q) {
   return c * (4 * WN) + (q ^ (WN >= 4 ? (c & 7) | (((c >> 4) ^ (c >> 5)) & 1) << 3 : (c & 7)));
 }
 
-__device__ inline void f8_store_bf16(const F8Args& a, const floatx4_t (&acc)[4], int row, bool there, int n0, bool wide) {
+__device__ inline void f8_store_bf16(const F8Args& a, const floatx4_t (&acc)[4], int row, bool there, int n0) {
   const int g = (threadIdx.x & 63) >> 4;
   uint16_t* y = static_cast<uint16_t*>(a.y) + (size_t)row * a.N;
 #pragma unroll
@@ -55,33 +55,16 @@ __device__ inline void f8_store_bf16(const F8Args& a, const floatx4_t (&acc)[4],
       p[z] = s[0];
       p[2 + z] = s[1];
     }
-    const int n = n0 + 16 * (j + (g & 1)) + 8 * (g >> 1);
-    if (!there) continue;
-    if (wide) {
-      if (n < a.N) *reinterpret_cast<uint4*>(y + n) = make_uint4(p[0], p[1], p[2], p[3]);
-    } else {
-#pragma unroll
-      for (int z = 0; z < 8; ++z)
-        if (n + z < a.N) y[n + z] = (uint16_t)(p[z / 2] >> (16 * (z & 1)));
-    }
+    if (there) store8_bf16(y, n0 + 16 * (j + (g & 1)) + 8 * (g >> 1), a.N, p[0], p[1], p[2], p[3]);
   }
 }
 
-__device__ inline void f8_store_f32(const F8Args& a, const floatx4_t (&acc)[4], int row, bool there, int n0, bool wide) {
+__device__ inline void f8_store_f32(const F8Args& a, const floatx4_t (&acc)[4], int row, bool there, int n0) {
   const int g = (threadIdx.x & 63) >> 4;
-  if (!there) return;
   float* y = static_cast<float*>(a.y) + (size_t)row * a.N;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = n0 + 16 * j + 4 * g;
-    if (wide) {
-      if (n < a.N) *reinterpret_cast<floatx4_t*>(y + n) = acc[j];
-    } else {
-#pragma unroll
-      for (int z = 0; z < 4; ++z)
-        if (n + z < a.N) y[n + z] = acc[j][z];
-    }
-  }
+  for (int j = 0; j < 4; ++j)
+    if (there) store4_f32(y, n0 + 16 * j + 4 * g, a.N, acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
 }
 
 // What a wave's products of a step read: 32 codes a lane of four runs of 16 matrix rows and of L runs of rows, and the
@@ -341,13 +324,12 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
     else if (live == 2) run(std::integral_constant<int, 2>{});
     else if (live == 1) run(std::integral_constant<int, 1>{});
     else run(std::integral_constant<int, 0>{});
-    const bool wide = a.N % (a.ydtype == 1 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < kRuns; ++i)
       if (i < live) {
         const int m = kRun * (run0 + i) + r;
-        if (a.ydtype == 1) f8_store_bf16(a, acc[i], t.s0 + m, m < t.M, t.n0 + 64 * wn, wide);
-        else f8_store_f32(a, acc[i], t.s0 + m, m < t.M, t.n0 + 64 * wn, wide);
+        if (a.ydtype == 1) f8_store_bf16(a, acc[i], t.s0 + m, m < t.M, t.n0 + 64 * wn);
+        else f8_store_f32(a, acc[i], t.s0 + m, m < t.M, t.n0 + 64 * wn);
       }
     if (!more) break;
     next = deal.answer(next);

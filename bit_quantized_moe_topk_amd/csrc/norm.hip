@@ -24,7 +24,6 @@ struct NormArgs {
   uint8_t* codes;
   float* scales;
   float* part;
-  bool vin, vout, vw;  // 16 bytes at a time: rows that come in, rows that go out, the weight
 };
 
 __device__ inline double wave_sum(double v) {
@@ -79,8 +78,8 @@ __device__ inline void load_weight(const NormArgs& a, float (&w)[C][8]) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = Place<C, W>::col(c);
-    if (a.wbf) load8<true>(a.weight, col, a.H, a.vw, w[c]);
-    else load8<false>(a.weight, col, a.H, a.vw, w[c]);
+    if (a.wbf) load8<true>(a.weight, col, a.H, w[c]);
+    else load8<false>(a.weight, col, a.H, w[c]);
   }
 }
 
@@ -103,14 +102,14 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
       for (int i = 0; i < 8; ++i) f[c][i] = 0.f;
       const int col = P::col(c);
       if (there && col < a.H) {
-        load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, a.vin, f[c]);
+        load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, f[c]);
         if (a.residual) {
           float g[8];
-          load8<BF>(static_cast<const char*>(a.residual) + t * a.ldr * kSize, col, a.H, a.vin, g);
+          load8<BF>(static_cast<const char*>(a.residual) + t * a.ldr * kSize, col, a.H, g);
 #pragma unroll
           for (int i = 0; i < 8; ++i) f[c][i] += g[i];
         }
-        if (a.total) store8<BF>(static_cast<char*>(a.total) + (size_t)t * a.H * kSize, col, a.H, a.vout, f[c]);
+        if (a.total) store8<BF>(static_cast<char*>(a.total) + (size_t)t * a.H * kSize, col, a.H, f[c]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) part = fmaf(f[c][i], f[c][i], part);
@@ -131,7 +130,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
         const float u = f[c][i] * q;
         v[i] = fmaf(u, w[c][i], fmaf(f[c][i], ql, fmaf(f[c][i], q, -u)) * w[c][i]);
       }
-      if (a.y) store8<BF>(static_cast<char*>(a.y) + (size_t)t * a.H * kSize, col, a.H, a.vout, v);
+      if (a.y) store8<BF>(static_cast<char*>(a.y) + (size_t)t * a.H * kSize, col, a.H, v);
       if (a.codes) {
         // past the row's end there is nothing, whatever q is
 #pragma unroll
@@ -163,8 +162,8 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
       for (int i = 0; i < 8; ++i) h[c][i] = d[c][i] = 0.f;
       const int col = P::col(c);
       if (there && col < a.H) {
-        load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, a.vin, h[c]);
-        load8<BF>(static_cast<const char*>(a.dy) + t * a.ldd * kSize, col, a.H, a.vin, d[c]);
+        load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, h[c]);
+        load8<BF>(static_cast<const char*>(a.dy) + t * a.ldd * kSize, col, a.H, d[c]);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -182,13 +181,13 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
       float g[8], v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = 0.f;
-      if (a.d_total) load8<BF>(static_cast<const char*>(a.d_total) + t * a.ldt * kSize, col, a.H, a.vin, g);
+      if (a.d_total) load8<BF>(static_cast<const char*>(a.d_total) + t * a.ldt * kSize, col, a.H, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[i] = fmaf(q, w[c][i] * d[c][i] - h[c][i] * m, g[i]);
         dw[c][i] = fmaf(d[c][i], h[c][i] * q, dw[c][i]);
       }
-      store8<BF>(static_cast<char*>(a.dh) + (size_t)t * a.H * kSize, col, a.H, a.vout, v);
+      store8<BF>(static_cast<char*>(a.dh) + (size_t)t * a.H * kSize, col, a.H, v);
     }
   }
   if (!a.part) return;
@@ -197,7 +196,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
     __shared__ __attribute__((aligned(16))) float rows[P::kRowsAtOnce - 1][8 * 64 * W * C];
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (P::row() > 0) store8<false>(rows[P::row() - 1], P::col(c), 1 << 30, true, dw[c]);
+      if (P::row() > 0) store8<false>(rows[P::row() - 1], P::col(c), 1 << 30, dw[c]);
     __syncthreads();
     if (P::row() > 0) return;
 #pragma unroll
@@ -211,7 +210,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int col = P::col(c);
-    if (col < a.H) store8<false>(part, col, a.H, a.H % 4 == 0, dw[c]);
+    if (col < a.H) store8<false>(part, col, a.H, dw[c]);
   }
 }
 
@@ -257,8 +256,6 @@ int grid_of(int T, const Shape& s, int most) {
   return n < most ? n : most;
 }
 
-bool all_vec(const void* p, long long ld, int size) { return !p || rows_vec(p, ld, size); }
-
 #define NORM_FORMS(M, BF) \
   M(BF, 1, 1) M(BF, 1, 2) M(BF, 1, 4) M(BF, 2, 4) M(BF, 4, 4) M(BF, 4, 8) M(BF, 4, 16)
 
@@ -272,13 +269,9 @@ size_t norm_workspace_bytes(int T, int H) {
 hipError_t launch_norm(const void* x, int dtype, long long ldx, const void* residual, long long ldr, const void* weight,
                        int wdtype, float eps, int T, int H, void* total, void* y, uint8_t* codes, float* scales,
                        hipStream_t s) {
-  const int size = dtype == 1 ? 2 : 4;
   NormArgs a{};
   a.x = x; a.ldx = ldx; a.residual = residual; a.ldr = ldr; a.weight = weight; a.wbf = wdtype == 1;
   a.eps = eps; a.T = T; a.H = H; a.total = total; a.y = y; a.codes = codes; a.scales = scales;
-  a.vin = all_vec(x, ldx, size) && all_vec(residual, ldr, size);
-  a.vout = all_vec(total, H, size) && all_vec(y, H, size);
-  a.vw = rows_vec(weight, 0, 2);
   const Shape f = shape_of(T, H);
   const dim3 g(grid_of(T, f, 8 * device_cus()));
 #define FORWARD(BF, CC, WW) \
@@ -293,13 +286,9 @@ hipError_t launch_norm(const void* x, int dtype, long long ldx, const void* resi
 hipError_t launch_norm_backward(const void* dy, long long ldd, const void* h, long long ldh, int dtype, const void* weight,
                                 int wdtype, const void* d_total, long long ldt, float eps, int T, int H, void* dh,
                                 float* dweight, void* ws, hipStream_t s) {
-  const int size = dtype == 1 ? 2 : 4;
   NormArgs a{};
   a.x = h; a.ldx = ldh; a.dy = dy; a.ldd = ldd; a.d_total = d_total; a.ldt = ldt; a.weight = weight; a.wbf = wdtype == 1;
   a.eps = eps; a.T = T; a.H = H; a.dh = dh; a.part = dweight ? static_cast<float*>(ws) : nullptr;
-  a.vin = all_vec(h, ldh, size) && all_vec(dy, ldd, size) && all_vec(d_total, ldt, size);
-  a.vout = all_vec(dh, H, size);
-  a.vw = rows_vec(weight, 0, 2);
   const Shape f = shape_of(T, H);
   const dim3 g(grid_of(T, f, kParts));
   if (T > 0) {

@@ -121,7 +121,7 @@ def lib() -> C.CDLL:
             "moe_fp8_dequantize": [P, P, i32, i32, i32, i32, i32, P, P],
             "moe_fp8_matmul": [P, P, i32, P, P, i32, i32, P, i32, P],
             "moe_fp8_matmul_backward": [P, P, i32, P, P, i32, i32, P, i32, P],
-            "moe_fp8_experts_matmul": [P, P, i32, i32, i32, i32, i32, P, P, P, P, i32, i32, P, i32, P, sz, P],
+            "moe_fp8_experts_matmul": [P, P, i32, i32, i32, i32, i32, P, P, P, P, i32, i32, P, i32, P],
             "moe_fp8_experts_matmul_backward": [P, P, i32, i32, i32, i32, i32, P, P, P, P, i32, i32, P, i32, P, sz, P],
             "moe_rms_norm": [P, i32, i64, P, i64, P, i32, C.c_float, i32, i32, P, P, P, P, P],
             "moe_rms_norm_backward": [P, i64, P, i64, i32, P, i32, P, i64, C.c_float, i32, i32, P, P, P, sz, P],
@@ -135,7 +135,7 @@ def lib() -> C.CDLL:
         L.moe_mx4_experts_matmul_backward_workspace_size.restype = sz
         L.moe_balance_loss_workspace_size.argtypes = [i32] * 3
         L.moe_balance_loss_workspace_size.restype = sz
-        for name, n in (("moe_fp8_experts_matmul", 3), ("moe_fp8_experts_matmul_backward", 5), ("moe_rms_norm_backward", 2)):
+        for name, n in (("moe_fp8_experts_matmul_backward", 5), ("moe_rms_norm_backward", 2)):
             f = getattr(L, name + "_workspace_size")
             f.argtypes, f.restype = [i32] * n, sz
         L.moe_profile_begin.argtypes = [i32]
@@ -1033,7 +1033,7 @@ def fp8_matmul_backward(dy: Fp8, w: Fp8, dtype: torch.dtype = torch.bfloat16,
 
 
 def fp8_experts_matmul(x: Fp8, w: Fp8, grouping: Grouping, tokens: int | None = None, dtype: torch.dtype = torch.bfloat16,
-                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+                       out: torch.Tensor | None = None) -> torch.Tensor:
     """8-bit rows grouped by expert, each times its expert's matrix (moe_fp8_experts_matmul): [A, N] in the
     groups' order. w: [E, N, K], or [E + 1, N, K] with the shared expert last. x holds the A rows in the groups'
     order, or, where `tokens` gives their number, one row a token. Rows of `out` that are in no group are left as
@@ -1048,10 +1048,9 @@ def fp8_experts_matmul(x: Fp8, w: Fp8, grouping: Grouping, tokens: int | None = 
     if gather:
         _int32("grouping.perm", grouping.perm, dev, A)
     y = _result(out, (A, N), dtype, dev)
-    wp, wn, keep = _workspace(workspace, _bytes("moe_fp8_experts_matmul_workspace_size", T, k, shared), dev)
     _call("moe_fp8_experts_matmul", dev, x.codes.data_ptr(), x.scales.data_ptr(), T, k, E, shared, int(gather),
           grouping.offsets.data_ptr(), grouping.perm.data_ptr() if gather else None, w.codes.data_ptr(),
-          w.scales.data_ptr(), N, w.K, y.data_ptr(), _FLOATS[dtype], wp, wn)
+          w.scales.data_ptr(), N, w.K, y.data_ptr(), _FLOATS[dtype])
     return y
 
 

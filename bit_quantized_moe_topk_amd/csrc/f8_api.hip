@@ -133,30 +133,20 @@ int moe_fp8_matmul_backward(const uint8_t* dy_codes, const float* dy_scales, int
   return status_of(moe::launch_f8_product(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t moe_fp8_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_shared) {
-  if (check_groups(T, k, 1, has_shared, 0) != MOE_OK) return 0;
-  return counter_bytes((long long)T * (k + has_shared));
-}
-
 int moe_fp8_experts_matmul(const uint8_t* x_codes, const float* x_scales, int32_t T, int32_t k, int32_t E,
                            int32_t has_shared, int32_t gather, const int32_t* offsets, const int32_t* perm,
                            const uint8_t* w_codes, const float* w_scales, int32_t N, int32_t K, void* y, int32_t ydtype,
-                           void* ws, size_t ws_bytes, void* stream) {
+                           void* stream) {
   int st = check_groups(T, k, E, has_shared, gather);
   if (st != MOE_OK) return st;
   const int32_t A = T * (k + has_shared), mats = E + has_shared;
   st = check_product(x_codes, x_scales, A, w_codes, w_scales, N, K, y, ydtype);
   if (st != MOE_OK || A == 0) return st;
   if (!offsets || (gather && !perm)) return MOE_ERR_INVALID_ARG;
-  const size_t need = counter_bytes(A);
-  if (need && (!ws || !aligned(ws, 16) || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   const u64 out = (u64)A * N * size_of(ydtype), ids = sizeof(int32_t) * (u64)A, ends = sizeof(int32_t) * (u64)(mats + 1);
   const int32_t rows = gather ? T : A;
   if (overlaps_operands(y, out, x_codes, x_scales, rows, K, w_codes, w_scales, mats, N, K) ||
-      overlaps(y, out, flat(offsets, ends)) || (gather && overlaps(y, out, flat(perm, ids))) ||
-      (need && (overlaps(y, out, flat(ws, need)) || overlaps(ws, need, flat(offsets, ends)) ||
-                (gather && overlaps(ws, need, flat(perm, ids))) ||
-                overlaps_operands(ws, need, x_codes, x_scales, rows, K, w_codes, w_scales, mats, N, K))))
+      overlaps(y, out, flat(offsets, ends)) || (gather && overlaps(y, out, flat(perm, ids))))
     return MOE_ERR_INVALID_ARG;
   moe::F8Args a = product(x_codes, x_scales, A, w_codes, w_scales, N, K, y, ydtype, false);
   a.T = T;
@@ -164,7 +154,6 @@ int moe_fp8_experts_matmul(const uint8_t* x_codes, const float* x_scales, int32_
   a.E_tot = mats;
   a.offsets = offsets;
   a.perm = gather ? perm : nullptr;
-  a.counter = need ? static_cast<uint32_t*>(ws) : nullptr;
   return status_of(moe::launch_f8_product(a, static_cast<hipStream_t>(stream)));
 }
 

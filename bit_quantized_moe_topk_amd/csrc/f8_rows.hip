@@ -1,10 +1,11 @@
 // Products of few 8-bit rows with an 8-bit matrix, and the products with the
 // matrix turned (the gradient for the rows).
 //
-// Up to 16 rows of one group and 16 results a row per workgroup, on 16x16
+// Up to 16 rows of one group and 16 or 32 results a row per workgroup, on 16x16
 // matrix-core tiles; four waves share the blocks of the contraction. Weights go
-// from memory to registers. Bound by the matrix's bytes: each is read once per
-// 16 rows.
+// from memory to registers, no LDS before the waves' sums. Bound by one chain of loads, products and sums while there is a
+// workgroup a CU (one row, [1024, 2048], 3.9 us, of which a launch is about 3), then by the matrix's bytes, which are read once per
+// 16 rows: 16 rows of [8192, 8192] 22 us, 3.1 TB/s.
 #include "f8.h"
 
 namespace moe {

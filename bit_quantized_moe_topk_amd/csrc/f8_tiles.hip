@@ -3,11 +3,25 @@
 //
 // A step of the contraction is one block, so a product's 128 terms share two
 // scales: the matrix cores add them up from zero, and one multiply-add a result
-// brings the sum into the accumulator. A workgroup takes up to 128 rows of one
+// brings the sum into the accumulator. A workgroup takes up to TM rows of one
 // group and a strip of 64 WN results a row; eight waves, WN across and 8 / WN
-// down, own 64 results of 16 WN rows each. Rows, codes and scales come by direct
-// global-to-LDS loads, three buffers, so that a load has two steps to land, and
-// the loads run on across tiles.
+// down, own 64 results of TM WN / 8 rows each. Rows, codes and scales come by direct
+// global-to-LDS loads that run on across tiles, three buffers of the matrix and two
+// or three of rows. A wave reads the next step's operands into the registers of
+// those that its products have used up, so a buffer is free for the load of three
+// (two) steps on when its step begins, and the matrix cores run through the
+// barrier between steps.
+//
+// Bound, one matrix: by the matrix cores and the LDS reads that feed them: 8192 x
+// 1024 x 8192 (rows, results, columns) 77 us, 1.78 PFLOP/s, where a large library
+// product in 8 bits reaches 2.7; with 2,048 columns 25 us, as the first loads and
+// the stores of 256 tiles, one a CU, are not covered. Grouped: by the loads into
+// LDS: 8,192 tokens to 10 of 512 experts and a shared one, [1024, 2048], 328 us,
+// 1.15 PFLOP/s (at 379 us: 346 without the products, 223 without the loads); the
+// gradient of 1,024 tokens 227 us, at a copy's rate of 5.1 TB/s.
+// Tried without gain: beginning each tile's contraction at another column (377 of
+// 379), scales 16 bytes at a time, loading only the rows that are there, 2 to 8
+// products between one and the addition of its sum (within 3 %).
 //
 // The turned matrix lies in LDS as it is stored, contraction rows of 256 (128)
 // bytes, and is read with transposing loads: 16 lanes read 8 rows of 16 codes and
@@ -339,12 +353,27 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
 
 }  // namespace
 
+// Results in bf16 come from the 8-bit cores, whose sums of 128 products lose what is 13 bits below the largest: 2^-13 of a
+// block's largest product, against bf16's half step of 2^-9; tokens' sums of float32 parts that are rounded to bf16 too. Results in
+// float32 take bf16 cores and keep all bits of every product (EXACT).
 // Offsets within the rows and within one matrix are 32 bits wide.
 bool f8_tiles_can(const F8Args& a) {
   const long long rows = a.perm ? a.T : a.A, stored = a.back ? a.K : a.N;
   return rows * a.xb * kF8Block < (1LL << 32) && stored * a.wb * kF8Block < (1LL << 32);
 }
 
+// Strips of 256 results a row, or of 128 where those would leave CUs without a tile. Measured, 128 against 256: one matrix
+// [1024, 2048], 128 rows 13.6 us against 19.6, 2,048 14.9 against 20.7, 8,192 (256 tiles of 256) 28 against 25; the
+// turned one, 2,048 rows 12.4 against 14.9, 8,192 (512 tiles) 36 against 28; experts [2048, 512] of 16 tokens 49 against 37.
+// Tiles of 192 rows, whose rows have two buffers, where groups have more than 112 on average. Groups of one size, 192 against
+// 128: [1024, 2048] 112 rows 33.5 us against 33.5, 144 35.4 against 40.5, 192 39.7 against 45.2, 256 53.4 against 51.8, 384 68
+// against 73; experts of 8,192 tokens (176 rows) 320 against 358, of 4,096 (88 rows) 263 against 246. One matrix has no use for
+// them: 8,192 rows of [1024, 2048] 31.9 against 25.4, where tiles of 128 fill the CUs once.
+// Tiles are dealt to the workgroups in turn, or, of a turned matrix, taken from counters, which a launch before clears: where a
+// group's strips are many, its steps too, and its rows few. Measured, taken against dealt: turned [1024, 2048] (8 strips, 8 steps),
+// 1,024 tokens 218 us against 231, 8,192 (176 rows a group) 355 against 347, [512, 1024] (4 strips, 4 steps), 1,024 tokens 69
+// against 67, [768, 4096] 185 against 194. Not turned no case gained: [2048, 1024], 1,024 tokens 227 against 224; [1024, 2048], 8,192 331
+// against 314, 256 unevenly loaded 53 against 45.
 hipError_t launch_f8_tiles(F8Args a, hipStream_t s) {
   const int cap = device_cus();
   const int strip = mx4_row_tiles(a) * ((a.N + 255) / 256) < cap ? 128 : 256;
@@ -353,8 +382,8 @@ hipError_t launch_f8_tiles(F8Args a, hipStream_t s) {
   const int tm = tall ? 192 : 128;
   const long long most = ((long long)(a.A + tm - 1) / tm + (a.offsets ? a.E_tot : 0)) * strips;
   const dim3 g((unsigned)(most < cap ? most : cap));
-  if (most <= cap || g.x % kXcds) a.counter = nullptr;
-  else if (a.counter) launch_mx4_zero(a.counter, s);
+  if (most <= cap || g.x % kXcds || strips < 8 || a.xb < 6 || a.A > 96 * groups) a.counter = nullptr;
+  if (a.counter) launch_mx4_zero(a.counter, s);
 #define TILES(BACK, EXACT, NAME) \
   if (tall) MOE_LAUNCH(NAME "_192", s, (f8_tiles<BACK, EXACT, 4, 192>), g, dim3(kThreads), 0, s, a); \
   else if (strip == 256) MOE_LAUNCH(NAME, s, (f8_tiles<BACK, EXACT, 4, 128>), g, dim3(kThreads), 0, s, a); \

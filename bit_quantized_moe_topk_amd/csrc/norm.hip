@@ -8,7 +8,10 @@
 // neighbouring values a lane, so that 16 lanes hold an 8-bit block. The
 // gradient needs two sums of a row, which are taken together; the weight's
 // gradient stays in registers over the rows that a workgroup takes, and a second
-// launch adds up the workgroups' parts in order. Bound by memory.
+// launch adds up the workgroups' parts in order: no atomics, so it repeats. Bound by memory:
+// 8,192 rows of 2,048 bf16 values with a residual to total, 8-bit rows and scales, 27.2 us
+// (5.5 TB/s with part of the rows from cache; a copy reaches 5.1); the gradient at float32, 8,192 rows of 4,096, 79 us
+// (5.1 TB/s) and 4 for the parts. A few rows take 4 to 5 us a launch.
 #include "f8.h"
 #include "norm.h"
 
@@ -73,14 +76,9 @@ struct Place {
   __device__ static int row() { return threadIdx.x / (64 * W); }
 };
 
-template <int C, int W>
-__device__ inline void load_weight(const NormArgs& a, float (&w)[C][8]) {
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int col = Place<C, W>::col(c);
-    if (a.wbf) load8<true>(a.weight, col, a.H, w[c]);
-    else load8<false>(a.weight, col, a.H, w[c]);
-  }
+__device__ inline void weight_at(const NormArgs& a, int col, float (&w)[8]) {
+  if (a.wbf) load8<true>(a.weight, col, a.H, w);
+  else load8<false>(a.weight, col, a.H, w);
 }
 
 template <bool BF, int C, int W>
@@ -90,7 +88,8 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
   constexpr int kSize = BF ? 2 : 4;
   const int nb = f8_blocks(a.H);
   float w[C][8];
-  load_weight<C, W>(a, w);
+#pragma unroll
+  for (int c = 0; c < C; ++c) weight_at(a, P::col(c), w[c]);
   int turn = 0;
   for (int t0 = blockIdx.x * P::kRowsAtOnce; t0 < a.T; t0 += gridDim.x * P::kRowsAtOnce) {
     const int t = t0 + P::row();
@@ -149,8 +148,18 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
   typedef Place<C, W> P;
   __shared__ float mem[2 * (W < 4 ? 4 : W)][2];
   constexpr int kSize = BF ? 2 : 4;
-  float w[C][8], dw[C][8] = {};
-  load_weight<C, W>(a, w);
+  // (the weight stays in registers but where a workgroup has 1,024 threads, and so 128 registers each: 1,024 bf16 rows of 20,000
+  // 86 us against 154; 8,192 of 8,192 values 117 held against 148)
+  constexpr bool kHold = W < 16;
+  float held[kHold ? C : 1][8], dw[C][8] = {};
+  if constexpr (kHold)
+#pragma unroll
+    for (int c = 0; c < C; ++c) weight_at(a, P::col(c), held[c]);
+  auto weight = [&](int c, float (&w)[8]) __attribute__((always_inline)) {
+    if constexpr (!kHold) return weight_at(a, P::col(c), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = held[kHold ? c : 0][i];
+  };
   int turn = 0;
   for (int t0 = blockIdx.x * P::kRowsAtOnce; t0 < a.T; t0 += gridDim.x * P::kRowsAtOnce) {
     const int t = t0 + P::row();
@@ -165,10 +174,12 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
         load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, h[c]);
         load8<BF>(static_cast<const char*>(a.dy) + t * a.ldd * kSize, col, a.H, d[c]);
       }
+      float w[8];
+      weight(c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sum[0] = fmaf(h[c][i], h[c][i], sum[0]);
-        sum[1] = fmaf(w[c][i] * d[c][i], h[c][i], sum[1]);
+        sum[1] = fmaf(w[i] * d[c][i], h[c][i], sum[1]);
       }
     }
     row_sums<W, 2>(sum, mem, turn);
@@ -178,13 +189,14 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
     for (int c = 0; c < C; ++c) {
       const int col = P::col(c);
       if (!there || col >= a.H) continue;
-      float g[8], v[8];
+      float g[8], v[8], w[8];
+      weight(c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) g[i] = 0.f;
       if (a.d_total) load8<BF>(static_cast<const char*>(a.d_total) + t * a.ldt * kSize, col, a.H, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = fmaf(q, w[c][i] * d[c][i] - h[c][i] * m, g[i]);
+        v[i] = fmaf(q, w[i] * d[c][i] - h[c][i] * m, g[i]);
         dw[c][i] = fmaf(d[c][i], h[c][i] * q, dw[c][i]);
       }
       store8<BF>(static_cast<char*>(a.dh) + (size_t)t * a.H * kSize, col, a.H, v);
@@ -238,7 +250,9 @@ __global__ __launch_bounds__(1024) void norm_parts(const float* __restrict__ par
 struct Shape {
   int C, W;
 };
-// Chunks of eight values a lane and waves a row.
+// Chunks of eight values a lane and waves a row: up to four waves before a second chunk, which keeps a row's loads short of one
+// another's way. Measured, waves first against chunks first: 8,192 rows of 2,048 in bf16 25.5 us against 29.6, of 4,096 61 against
+// 79, 64 rows of 2,048 4.7 against 7.7. (More waves at once would leave fewer rows a workgroup for the weight's gradient.)
 Shape shape_of(int T, int H) {
   Shape s{1, 1};
   while (512 * s.C * s.W < H) {
@@ -249,7 +263,9 @@ Shape shape_of(int T, int H) {
   return s;
 }
 
-constexpr int kParts = 512;  // most workgroups of the gradient: each leaves a row of parts
+// Most workgroups of the gradient, each of which leaves a row of parts. Gradient and parts, float32: 8,192 rows of 2,048 with 128
+// 86 us, 256 49, 512 35, 1,024 37, 2,048 40; of 4,096 165, 97, 83, 84, 90.
+constexpr int kParts = 512;
 int rows_at_once(const Shape& s) { return s.W < 4 ? 4 / s.W : 1; }
 int grid_of(int T, const Shape& s, int most) {
   const int n = (T + rows_at_once(s) - 1) / rows_at_once(s);

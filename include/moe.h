@@ -570,17 +570,13 @@ int moe_fp8_matmul_backward(const uint8_t *dy_codes, const float *dy_scales, int
                             const uint8_t *w_codes, const float *w_scales, int32_t N, int32_t K,
                             void *dx, int32_t dxdtype, void *stream);
 
-/* Workspace bytes moe_fp8_experts_matmul needs (0 for a few rows). */
-size_t moe_fp8_experts_matmul_workspace_size(int32_t T, int32_t k, int32_t has_shared);
-
 /* The same products for rows grouped by expert: arguments, groups, `gather`, rows in no
  * group and bad ids as in moe_mx4_experts_matmul. x: [A] 8-bit rows in the groups'
- * order (gather == 0), or [T], one a token (gather == 1). */
+ * order (gather == 0), or [T], one a token (gather == 1). It needs no workspace. */
 int moe_fp8_experts_matmul(const uint8_t *x_codes, const float *x_scales, int32_t T, int32_t k,
                            int32_t E, int32_t has_shared, int32_t gather, const int32_t *offsets,
                            const int32_t *perm, const uint8_t *w_codes, const float *w_scales,
-                           int32_t N, int32_t K, void *y, int32_t ydtype, void *ws, size_t ws_bytes,
-                           void *stream);
+                           int32_t N, int32_t K, void *y, int32_t ydtype, void *stream);
 
 /* Workspace bytes moe_fp8_experts_matmul_backward needs. */
 size_t moe_fp8_experts_matmul_backward_workspace_size(int32_t T, int32_t k, int32_t has_shared,

@@ -73,27 +73,28 @@ def test_matmul_refuses(back):
 def experts(back, x=AT["x"], xs=AT["xs"], T=300, k=8, E=16, shared=1, gather=1, offsets=AT["offsets"], perm=AT["perm"],
             w=AT["w"], ws=AT["ws"], N=256, K=512, y=AT["y"], t=moe.BF16, room=AT["room"], n=1 << 30):
     fn = moe.lib().moe_fp8_experts_matmul_backward if back else moe.lib().moe_fp8_experts_matmul
-    return fn(P(x), P(xs), T, k, E, shared, gather, P(offsets), P(perm), P(w), P(ws), N, K, P(y), t, P(room), n, None)
+    return fn(P(x), P(xs), T, k, E, shared, gather, P(offsets), P(perm), P(w), P(ws), N, K, P(y), t, *((P(room), n) if back else ()), None)
 
 
 @pytest.mark.parametrize("back", [False, True])
 def test_experts_refuse(back):
     for bad in (dict(T=-1), dict(k=0), dict(E=0), dict(shared=2), dict(gather=3), dict(offsets=0), dict(perm=0), dict(N=0), dict(K=0),
                 dict(x=0), dict(xs=0), dict(w=0), dict(ws=0), dict(y=0), dict(t=4), dict(w=AT["w"] + 8),
-                dict(y=AT["offsets"]), dict(y=AT["perm"] + 16), dict(y=AT["room"] + 512), dict(y=AT["w"]), dict(y=AT["ws"] + 16),
-                dict(room=AT["x"]), dict(room=AT["w"] + 1024), dict(room=AT["offsets"]), dict(room=AT["perm"])):
+                dict(y=AT["offsets"]), dict(y=AT["perm"] + 16), dict(y=AT["w"]), dict(y=AT["ws"] + 16)):
         assert experts(back, **bad) == INV, bad
+    for bad in (dict(y=AT["room"] + 512), dict(room=AT["x"]), dict(room=AT["w"] + 1024), dict(room=AT["offsets"]), dict(room=AT["perm"])):
+        assert not back or experts(back, **bad) == INV, bad
     for bad in (dict(E=2049), dict(T=1 << 22), dict(k=1 << 23), dict(N=(1 << 19) + 1)):
         assert experts(back, **bad) == UNS, bad
     for bad in (dict(room=0), dict(n=64), dict(room=AT["room"] + 8)):
-        assert experts(back, **bad) == WSP, bad
+        assert not back or experts(back, **bad) == WSP, bad
     assert experts(back, T=0, x=0, xs=0, w=0, ws=0, y=0, offsets=0, perm=0, room=0, n=0) == OK
 
 
 def test_workspace_sizes():
     L = moe.lib()
-    assert L.moe_fp8_experts_matmul_workspace_size(4, 10, 1) == 0 and L.moe_fp8_experts_matmul_workspace_size(8192, 10, 1) > 0
-    assert L.moe_fp8_experts_matmul_workspace_size(-1, 10, 1) == 0
+    assert L.moe_fp8_experts_matmul_backward_workspace_size(8192, 10, 1, 100, 0) > 0
+    assert L.moe_fp8_experts_matmul_backward_workspace_size(-1, 10, 1, 100, 0) == 0
     assert L.moe_fp8_experts_matmul_backward_workspace_size(10, 2, 1, 100, 1) >= 30 * 100 * 4
     assert L.moe_fp8_experts_matmul_backward_workspace_size(10, 2, 1, 100, 0) == 0
     assert L.moe_rms_norm_backward_workspace_size(5, 64) >= 64 * 4 and L.moe_rms_norm_backward_workspace_size(0, 64) == 0

@@ -57,7 +57,8 @@ GROUPED = [  # kernel, T, k, E, shared, N, K, back
     ("f8_tiles", 900, 2, 40, True, 2300, 200, False), ("f8_tiles_192", 900, 3, 16, True, 3100, 200, False),
     ("f8_tiles_192", 1500, 2, 20, False, 3000, 400, False),
     ("f8_tiles_back_strip128", 3, 2, 9, True, 130, 260, True), ("f8_tiles_back_strip128", 300, 4, 6, False, 384, 640, True),
-    ("f8_tiles_back", 900, 2, 40, True, 200, 2300, True), ("f8_tiles_back_192", 900, 3, 16, True, 200, 3100, True),
+    ("f8_tiles_back", 900, 2, 40, True, 200, 2300, True), ("f8_tiles_back", 700, 3, 64, False, 800, 2100, True),
+    ("f8_tiles_back_192", 900, 3, 16, True, 200, 3100, True),
     ("f8_tiles_back_192", 1500, 2, 20, False, 400, 3000, True)]
 
 

@@ -161,20 +161,20 @@ def test_two_graphs_and_a_stream_of_its_own():
                 assert torch.equal(got[name], want[name]), (rep, name)
 
 
-def test_two_graphs_share_a_workspace_in_turn():
-    """Two captured products with one workspace, replayed one after the other."""
+@pytest.mark.parametrize("shape", [(9, 256, 384, 700, 4), (64, 800, 2048, 700, 3)], ids=["dealt", "taken"])
+def test_two_graphs_share_a_workspace_in_turn(shape):
+    """Two captured products with one workspace, replayed one after the other (the larger takes its tiles from counters there)."""
     torch = torch_cuda()
     import bit_quantized_moe_topk_amd as moe
     g = torch.Generator(device="cuda").manual_seed(3)
-    E, N, K, T, k = 9, 256, 384, 700, 4
+    E, N, K, T, k = shape
     w = moe.fp8_quantize(torch.randn((E, N, K), generator=g, device="cuda"), 128)
     idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
     grp = moe.group(idx, E, False)
-    x = moe.fp8_quantize(torch.randn((T, K), generator=g, device="cuda"))
     dy = moe.fp8_quantize(torch.randn((T * k, N), generator=g, device="cuda"))
     n = moe.lib().moe_fp8_experts_matmul_backward_workspace_size(T, k, 0, K, 1)
     room = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
-    calls = [lambda: moe.fp8_experts_matmul(x, w, grp, tokens=T, workspace=room),
+    calls = [lambda: moe.fp8_experts_matmul_backward(dy, w, grp, workspace=room),
              lambda: moe.fp8_experts_matmul_backward(dy, w, grp, tokens=T, workspace=room)]
     want = [c().clone() for c in calls]
     torch.cuda.synchronize()

@@ -81,6 +81,17 @@ __device__ inline void weight_at(const NormArgs& a, int col, float (&w)[8]) {
   else load8<false>(a.weight, col, a.H, w);
 }
 
+// (Spelled out: as calls of weight_at the compiler leaves these loads within the loop over rows, 33.4 us for 27.8.)
+template <int C, int W>
+__device__ inline void load_weight(const NormArgs& a, float (&w)[C][8]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int col = Place<C, W>::col(c);
+    if (a.wbf) load8<true>(a.weight, col, a.H, w[c]);
+    else load8<false>(a.weight, col, a.H, w[c]);
+  }
+}
+
 template <bool BF, int C, int W>
 __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
   typedef Place<C, W> P;
@@ -88,8 +99,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
   constexpr int kSize = BF ? 2 : 4;
   const int nb = f8_blocks(a.H);
   float w[C][8];
-#pragma unroll
-  for (int c = 0; c < C; ++c) weight_at(a, P::col(c), w[c]);
+  load_weight<C, W>(a, w);
   int turn = 0;
   for (int t0 = blockIdx.x * P::kRowsAtOnce; t0 < a.T; t0 += gridDim.x * P::kRowsAtOnce) {
     const int t = t0 + P::row();
@@ -152,9 +162,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
   // 86 us against 154; 8,192 of 8,192 values 117 held against 148)
   constexpr bool kHold = W < 16;
   float held[kHold ? C : 1][8], dw[C][8] = {};
-  if constexpr (kHold)
-#pragma unroll
-    for (int c = 0; c < C; ++c) weight_at(a, P::col(c), held[c]);
+  if constexpr (kHold) load_weight<C, W>(a, held);
   auto weight = [&](int c, float (&w)[8]) __attribute__((always_inline)) {
     if constexpr (!kHold) return weight_at(a, P::col(c), w);
 #pragma unroll

@@ -17,8 +17,8 @@
 // second where groups are near) goes through 64 bits for all experts and k rounds.
 //
 // Measured: 8,192 tokens of 512 experts in 8 groups, k 8, with a bias 21.0 us, and 6.9 its gradient (64 bits
-// throughout: 55 and 8.2); a window of 4 tokens 6.9, one chain of dependent steps. Bound by vector instructions: about 900 a
-// token, twice the time of its bytes (16.8 MB of logits, read at 800 GB/s).
+// throughout: 55 and 8.2); a window of 4 tokens 6.9, one chain of dependent steps. Bound by vector instructions, 1,046 a
+// token, which have the vector units busy half of the time, and the steps that wait for one another; its 17 MB would take 3.4.
 // Exponentials by the instruction (score_near) only screen: gates are of expf, off by two last places.
 #include "gemv.h"
 #include "norm.h"

@@ -46,7 +46,8 @@ int check_groups(int32_t T, int32_t k, int32_t E, int32_t has_shared, int32_t ga
   return MOE_OK;
 }
 
-// Bytes of the counters (eight, 128 bytes apart) from which workgroups take tiles, from this many rows on.
+// Bytes of the counters (eight, 128 bytes apart) from which the gradient's workgroups may take tiles (which launches do: f8_tiles.hip),
+// from this many rows on: 2,112 rows of [1024, 2048] 193 us taken, 198 dealt, unevenly loaded 52 and 48.
 constexpr int32_t kCounterRows = 2048;
 size_t counter_bytes(long long rows) { return rows >= kCounterRows ? 1024 : 0; }
 

@@ -16,7 +16,7 @@
 // 1024 x 8192 (rows, results, columns) 77 us, 1.78 PFLOP/s, where a large library
 // product in 8 bits reaches 2.7; with 2,048 columns 25 us, as the first loads and
 // the stores of 256 tiles, one a CU, are not covered. Grouped: by the loads into
-// LDS: 8,192 tokens to 10 of 512 experts and a shared one, [1024, 2048], 328 us,
+// LDS: 8,192 tokens to 10 of 512 experts and a shared one, [1024, 2048], 313 to 328 us,
 // 1.15 PFLOP/s (at 379 us: 346 without the products, 223 without the loads); the
 // gradient of 1,024 tokens 227 us, at a copy's rate of 5.1 TB/s.
 // Tried without gain: beginning each tile's contraction at another column (377 of

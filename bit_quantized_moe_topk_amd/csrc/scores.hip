@@ -16,7 +16,7 @@
 // What remains (over 64 candidates or ranks; a third expert of a group near its
 // second where groups are near) goes through 64 bits for all experts and k rounds.
 //
-// Measured: 8,192 tokens of 512 experts in 8 groups, k 8, with a bias 21.0 us, and 6.9 its gradient (64 bits
+// Measured: 8,192 tokens of 512 experts in 8 groups, k 8, with a bias 21.0 us, and 7.2 its gradient (64 bits
 // throughout: 55 and 8.2); a window of 4 tokens 6.9, one chain of dependent steps. Bound by vector instructions, 1,046 a
 // token, which have the vector units busy half of the time, and the steps that wait for one another; its 17 MB would take 3.4.
 // Exponentials by the instruction (score_near) only screen: gates are of expf, off by two last places.
@@ -469,12 +469,32 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool
     }
   S = wave_sum(S);
   D = wave_sum(D);
-  const float mean = a.renorm ? (S == 0.f ? 0.f : D / S) : 0.f, inv = a.renorm ? (S == 0.f ? 0.f : 1.f / S) : 1.f;
+  float mean = a.renorm ? D / S : 0.f;
+  const float inv = a.renorm ? 1.f / S : 1.f;
+  // What a gate has of the scale: the score, renormalised its share of the sum. (d / S by itself may pass the range.) Shares of
+  // scores that 32 bits hardly hold come of 64, as in the forward call.
+  float share0 = s0 * inv;
+  const bool tiny = a.renorm && S < 0x1p-90f;
+  double wide = 0.0;  // their sum
+  if (tiny) {
+    const double w0 = e >= 0 ? score64(a, base, l0) : 0.0;
+    double w = w0, dw = d0 * w0;
+    for (int j = 64 + lane; j < a.k; j += 64)
+      if ((unsigned)idx[j] < (unsigned)a.E) {
+        const double v = score64(a, base, logit_at(a, t, idx[j]));
+        w += v;
+        dw += a.scale * dg[j] * v;
+      }
+    wide = wave_sum64(w);
+    dw = wave_sum64(dw);
+    share0 = wide == 0.0 ? 0.f : (float)(w0 / wide);
+    mean = wide == 0.0 ? 0.f : (float)(dw / wide);
+  }
   __builtin_amdgcn_wave_barrier();
   // An entry's value from the sum of its d: the first of an expert's assignments adds them up, in order.
-  auto entry = [&](float d, float s) { return full ? d : a.softmax ? s * d : d * s * (1.f - s); };
+  auto entry = [&](float d, float share, float s) { return full ? d : a.softmax ? share * d : d * share * (1.f - s); };
   if (a.k <= 64) {
-    const float mine = (d0 - mean) * inv;
+    const float mine = d0 - mean;
     float sum = 0.f;
     bool first = e >= 0;
     for (int j = 0; j < a.k; ++j) {
@@ -485,16 +505,19 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool
         first &= j >= lane;
       }
     }
-    if (first) row[e] = entry(sum, s0);
+    if (first) row[e] = entry(sum, share0, s0);
   } else {
     for (int j = 0; j < a.k; ++j) {
       const int o = idx[j];
-      if ((unsigned)o < (unsigned)a.E && lane == 0) row[o] += (a.scale * dg[j] - mean) * inv;
+      if ((unsigned)o < (unsigned)a.E && lane == 0) row[o] += a.scale * dg[j] - mean;
     }
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
     for (int c = lane; !full && c < a.E; c += 64)
-      if (row[c] != 0.f) row[c] = entry(row[c], score(logit_at(a, t, c)));
+      if (row[c] != 0.f) {
+        const float v = logit_at(a, t, c), s = score(v);
+        row[c] = entry(row[c], !tiny ? s * inv : wide == 0.0 ? 0.f : (float)(score64(a, base, v) / wide), s);
+      }
   }
   __builtin_amdgcn_wave_barrier();
   if (full) {

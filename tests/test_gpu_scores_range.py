@@ -1,0 +1,93 @@
+"""Routing by scores at the ends of its range, against float64: gradients of very low logits.
+
+Bounds, as in test_gpu_scores: (E + k + 24) 2^-24 of the magnitudes that a gradient's entry adds up, and half a step of its type. A
+sigmoid's entry is d s (1 - s), so its magnitudes carry both factors here: 1 - s is the score of the other sign."""
+import numpy as np
+import pytest
+
+import blocks_ref as ref
+from gpu_util import log, torch_cuda
+from test_gpu_scores import U, as64, check, lib
+
+pytestmark = pytest.mark.gpu
+
+
+def gradient(x, idx, d_gates, renorm, scale):
+    """The gradient of sigmoid gates in float64 without cancellation: (dlogits, the magnitudes that each adds up)."""
+    T, E = x.shape
+    s, rest = ref.scores(x, "sigmoid"), ref.scores(-x, "sigmoid")
+    out, size = np.zeros((T, E)), np.zeros((T, E))
+    for t in range(T):
+        e = idx[t]
+        d = np.float64(np.float32(scale)) * d_gates[t]
+        q, m = s[t][e], np.abs(d)
+        total = 1.0
+        if renorm:
+            total = q.sum()
+            if total == 0:
+                continue
+            d, m = d - (d * q).sum() / total, m + (m * q).sum() / total
+        np.add.at(out[t], e, d * (q / total) * rest[t][e])
+        np.add.at(size[t], e, m * (q / total) * rest[t][e])
+    return out, size
+
+
+def check_gradient(x, idx, d, renorm, name):
+    torch, moe = torch_cuda(), lib()
+    got = moe.route_scores_backward(x, idx, d, score="sigmoid", renormalize=renorm, scale=2.5)
+    want, size = gradient(as64(x), idx.cpu().numpy(), as64(d), renorm, 2.5)
+    err = (x.shape[1] + idx.shape[1] + 24) * U * size
+    half = torch.finfo(x.dtype).eps / 2
+    g = as64(got)
+    worst = np.max(np.abs(g - want) / (err + half * (np.abs(want) + err) + 1e-37))
+    log(f"[scores] gradient {name}: {worst:.3f}")
+    assert np.isfinite(g).all() and worst <= 1, name
+    return got
+
+
+def typed(v, kind):
+    torch = torch_cuda()
+    return torch.from_numpy(v.astype(np.float32)).to(torch.float32 if kind == "f32" else torch.bfloat16).cuda()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k", [(9, 32, 4), (5, 300, 10), (3, 200, 80)])
+def test_renormalised_gradient_of_low_logits(T, E, k, kind):
+    """Scores that float32 does not hold: their ratios count, and gates and gradient agree."""
+    torch, moe = torch_cuda(), lib()
+    rng = np.random.default_rng(E)
+    for level in (-60.0, -64.0, -80.0, -87.5, -88.0, -88.6, -89.0, -92.0, -104.0, -120.0, -300.0, -690.0):
+        x = typed(level + 2 * rng.standard_normal((T, E)), kind)
+        idx, gates = check(x, None, k, scale=2.5)
+        d = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+        got = check_gradient(x, idx, d, True, f"{T}x{E}x{k} at {level}")
+        assert (got != 0).any()
+    # some that are off beside them; and scores that 64 bits do not hold either: gates and gradient are 0
+    x = typed(-90 + 2 * rng.standard_normal((T, E)), kind)
+    x[:, 2:] = -float("inf")
+    idx, gates = check(x, None, k, scale=2.5)
+    check_gradient(x, idx, torch.ones((T, k), device="cuda") * torch.arange(k, device="cuda"), True, "few left")
+    x = torch.full_like(x, -800.0)
+    idx, gates = check(x, None, k, scale=2.5)
+    assert (gates == 0).all() and (moe.route_scores_backward(x, idx, gates + 1, scale=2.5) == 0).all()
+
+
+def test_renormalised_gradient_at_the_least_normal_score():
+    """Four logits around exp's last normal result: the formula gives 1.04, -0.97, 2.44, -2.50 and what goes with them."""
+    torch = torch_cuda()
+    idx = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    d = torch.tensor([[1.0, -2.0, 3.0, -6.0]], device="cuda")
+    for level in (-87.0, -88.0, -88.6, -89.0, -95.0):
+        x = torch.tensor([[level, level - 0.1, level + 0.05, level - 0.4]], device="cuda")
+        check_gradient(x, idx, d, True, f"at {level}")
+
+
+def test_renormalised_gradient_of_large_gradients():
+    """Small scores and large gradients of the gates: no product of the two leaves float32's range on the way."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(3)
+    for k in (6, 70):
+        x = typed(-55 + rng.standard_normal((4, 100)), "f32")
+        idx = torch.from_numpy(np.argsort(-x.cpu().numpy(), axis=1)[:, :k].astype(np.int32)).cuda().contiguous()
+        d = torch.from_numpy((1e25 * rng.standard_normal((4, k))).astype(np.float32)).cuda()
+        check_gradient(x, idx, d, True, f"large, k {k}")

@@ -469,30 +469,36 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool
     }
   S = wave_sum(S);
   D = wave_sum(D);
-  float mean = a.renorm ? D / S : 0.f;
-  const float inv = a.renorm ? 1.f / S : 1.f;
-  // What a gate has of the scale: the score, renormalised its share of the sum. (d / S by itself may pass the range.) Shares of
-  // scores that 32 bits hardly hold come of 64, as in the forward call.
-  float share0 = s0 * inv;
+  // Scores whose sum 32 bits hardly hold are exp(l) but for 2^-90 of them, so their ratios are those of exp(l - most). (The gates come
+  // of 64 bits there, in which a score is 0 from the limit here down.)
   const bool tiny = a.renorm && S < 0x1p-90f;
-  double wide = 0.0;  // their sum
+  float most = l0;
+  auto low = [&](float v) { return v <= -709.78271484375f ? 0.f : expf(v - most); };
+  float part = s0;
   if (tiny) {
-    const double w0 = e >= 0 ? score64(a, base, l0) : 0.0;
-    double w = w0, dw = d0 * w0;
+    for (int j = 64 + lane; j < a.k; j += 64)
+      if ((unsigned)idx[j] < (unsigned)a.E) most = fmaxf(most, logit_at(a, t, idx[j]));
+    most = wave_maxf(most);
+    S = part = low(l0);
+    D = d0 * part;
     for (int j = 64 + lane; j < a.k; j += 64)
       if ((unsigned)idx[j] < (unsigned)a.E) {
-        const double v = score64(a, base, logit_at(a, t, idx[j]));
-        w += v;
-        dw += a.scale * dg[j] * v;
+        const float s = low(logit_at(a, t, idx[j]));
+        S += s;
+        D = fmaf(a.scale * dg[j], s, D);
       }
-    wide = wave_sum64(w);
-    dw = wave_sum64(dw);
-    share0 = wide == 0.0 ? 0.f : (float)(w0 / wide);
-    mean = wide == 0.0 ? 0.f : (float)(dw / wide);
+    S = wave_sum(S);
+    D = wave_sum(D);
   }
+  const float mean = a.renorm ? (S == 0.f ? 0.f : D / S) : 0.f, inv = a.renorm ? (S == 0.f ? 0.f : 1.f / S) : 1.f;
   __builtin_amdgcn_wave_barrier();
-  // An entry's value from the sum of its d: the first of an expert's assignments adds them up, in order.
-  auto entry = [&](float d, float share, float s) { return full ? d : a.softmax ? share * d : d * share * (1.f - s); };
+  // An entry's value from the sum of its d: the first of an expert's assignments adds them up, in order. `part` over the sum is its
+  // share of the gates (d over the sum by itself may pass the range); 1 - s of a sigmoid is exp(-v) s where s is near 1.
+  auto entry = [&](float d, float part, float s, float v) {
+    if (full) return d;
+    const float g = d * (part * inv);
+    return a.softmax ? g : g * (v < 0.f ? 1.f - s : expf(-v) * s);
+  };
   if (a.k <= 64) {
     const float mine = d0 - mean;
     float sum = 0.f;
@@ -505,7 +511,7 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool
         first &= j >= lane;
       }
     }
-    if (first) row[e] = entry(sum, share0, s0);
+    if (first) row[e] = entry(sum, part, s0, l0);
   } else {
     for (int j = 0; j < a.k; ++j) {
       const int o = idx[j];
@@ -516,7 +522,7 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool
     for (int c = lane; !full && c < a.E; c += 64)
       if (row[c] != 0.f) {
         const float v = logit_at(a, t, c), s = score(v);
-        row[c] = entry(row[c], !tiny ? s * inv : wide == 0.0 ? 0.f : (float)(score64(a, base, v) / wide), s);
+        row[c] = entry(row[c], tiny ? low(v) : s, s, v);
       }
   }
   __builtin_amdgcn_wave_barrier();

@@ -1,4 +1,4 @@
-"""Routing by scores at the ends of its range, against float64: gradients of very low logits.
+"""Routing by scores at the ends of its range, against float64: gradients of very low and very high logits.
 
 Bounds, as in test_gpu_scores: (E + k + 24) 2^-24 of the magnitudes that a gradient's entry adds up, and half a step of its type. A
 sigmoid's entry is d s (1 - s), so its magnitudes carry both factors here: 1 - s is the score of the other sign."""
@@ -91,3 +91,19 @@ def test_renormalised_gradient_of_large_gradients():
         idx = torch.from_numpy(np.argsort(-x.cpu().numpy(), axis=1)[:, :k].astype(np.int32)).cuda().contiguous()
         d = torch.from_numpy((1e25 * rng.standard_normal((4, k))).astype(np.float32)).cuda()
         check_gradient(x, idx, d, True, f"large, k {k}")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(40, 32, 4), (7, 300, 10), (3, 200, 80)])
+def test_gradient_of_high_logits(T, E, k, renorm, kind):
+    """1 - s of a score near 1 keeps its bits."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(E + 1)
+    for lo, hi in ((8, 30), (15, 18), (60, 80), (-30, 30)):
+        x = typed(rng.uniform(lo, hi, (T, E)), kind)
+        idx = torch.from_numpy(np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)).cuda().contiguous()
+        d = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+        got = check_gradient(x, idx, d, renorm, f"{T}x{E}x{k} {renorm} {kind} in {lo} .. {hi}")
+        # (not where one score may outweigh the others 2^24 times: its d - sum d s / S is then 0 in 32 bits, within the bound)
+        assert lo < 0 or (got.gather(1, idx.long()) != 0).all()

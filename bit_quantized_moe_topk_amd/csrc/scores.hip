@@ -296,7 +296,8 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     if (a.bias || a.group_top == 2) {
       if (!a.bias) v = live ? score32(a, base, top.v1) : v;
       if (two) v += a.bias ? top.v2 : score32(a, base, top.v2);
-      margin = a.bias ? 0x1p-18f + 0x1p-21f * fabsf(v) : fmaxf(0x1p-19f * v, 0x1p-126f);
+      // (each term is rounded by itself: where they nearly cancel, by far more than the sum's own rounding)
+      margin = a.bias ? 0x1p-18f + 0x1p-21f * (fabsf(top.v1) + (two ? fabsf(top.v2) : 0.f)) : fmaxf(0x1p-19f * v, 0x1p-126f);
     }
     bool stays;
     kept = kept_groups(a, orderable(v), per, &stays);

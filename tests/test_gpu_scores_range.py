@@ -1,4 +1,5 @@
-"""Routing by scores at the ends of its range, against float64: gradients of very low and very high logits.
+"""Routing by scores at the ends of its range, against float64: gradients of very low and very high logits, groups whose best two
+values nearly cancel.
 
 Bounds, as in test_gpu_scores: (E + k + 24) 2^-24 of the magnitudes that a gradient's entry adds up, and half a step of its type. A
 sigmoid's entry is d s (1 - s), so its magnitudes carry both factors here: 1 - s is the score of the other sign."""
@@ -107,3 +108,38 @@ def test_gradient_of_high_logits(T, E, k, renorm, kind):
         got = check_gradient(x, idx, d, renorm, f"{T}x{E}x{k} {renorm} {kind} in {lo} .. {hi}")
         # (not where one score may outweigh the others 2^24 times: its d - sum d s / S is then 0 in 32 bits, within the bound)
         assert lo < 0 or (got.gather(1, idx.long()) != 0).all()
+
+
+def near_groups(rng, T, groups, size):
+    """Logits whose groups' best two sigmoid scores add up to nearly the same, apart by 1e-6 to 1e-3."""
+    s = rng.uniform(0.05, 0.3, (T, groups, size))
+    s[..., 0] = rng.uniform(0.5, 0.6, (T, groups))
+    apart = rng.choice([-1, 1], (T, groups)) * 10 ** rng.uniform(-6, -3, (T, groups))
+    s[..., 1] = 1.0 - s[..., 0] + apart
+    return np.log(s / (1 - s)).reshape(T, groups * size).astype(np.float32)
+
+
+@pytest.mark.parametrize("size", [2, 3, 4])
+@pytest.mark.parametrize("groups,keep", [(2, 1), (8, 3), (16, 5)])
+@pytest.mark.parametrize("B", [1.0, 200.0, 1e3, 1e4, 1e5, 3e7])
+def test_groups_of_opposite_biases(B, groups, keep, size):
+    """A group's value is small, its two terms are not: what 32 bits lose of them is not relative to the sum."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(int(B) + groups)
+    x = torch.from_numpy(near_groups(rng, 300, groups, size)).cuda()
+    bias = np.full((groups, size), -4 * B, np.float32)
+    bias[:, 0], bias[:, 1] = B, -B
+    check(x, torch.from_numpy(bias.reshape(-1)).cuda(), min(4, keep * size), groups=groups, keep_groups=keep, group_top=2)
+    # (each group with a size of its own)
+    own = (np.float32(B) * rng.uniform(0.5, 1.5, (groups, 1))).astype(np.float32)
+    bias[:, :1], bias[:, 1:2] = own, -own
+    check(x, torch.from_numpy(bias.reshape(-1)).cuda(), min(4, keep * size), groups=groups, keep_groups=keep, group_top=2)
+
+
+def test_groups_of_opposite_biases_by_hand():
+    """32 bits: 0.68555 and 0.68549; exactly: 0.68550 and 0.68554."""
+    torch = torch_cuda()
+    x = torch.tensor([[-.20984702, -1.1649512, .28798392, -2.0501812]], device="cuda")
+    b = torch.tensor([1e3, -1e3, 1e3, -1e3], device="cuda")
+    idx, _ = check(x, b, 2, groups=2, keep_groups=1, group_top=2)
+    assert idx.tolist() == [[2, 3]]

@@ -305,7 +305,9 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     const float lo = from_orderable(wave_reduce<false>(stays ? orderable(v) : 0xFFFFFFFFu));
     const float hi = wave_maxf(ours && !stays ? v : -INFINITY);
     const float most = wave_maxf(ours && live ? margin : 0.f);
-    if (most > 0.f && hi > -INFINITY && !(lo - hi >= 2.f * most)) {
+    // (a sum past the range is -inf, as the value of a group that is off; its margin is infinite)
+    const bool open = __any(ours && !stays && live);
+    if (most > 0.f && open && !(most < INFINITY && lo - hi >= 2.f * most)) {
       // the best of a group in 32 bits need not be so in 64, where the next is near
       const float apart = 0x1p-17f + 0x1p-20f * fabsf(top.v2);
       hard = !(hi < INFINITY) || (a.bias && __any(ours && (a.group_top == 2 ? two && top.v3 > -INFINITY && !(top.v2 - top.v3 >= apart)

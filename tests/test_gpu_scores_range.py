@@ -1,5 +1,5 @@
 """Routing by scores at the ends of its range, against float64: gradients of very low and very high logits, groups whose best two
-values nearly cancel.
+values nearly cancel or pass float32's range.
 
 Bounds, as in test_gpu_scores: (E + k + 24) 2^-24 of the magnitudes that a gradient's entry adds up, and half a step of its type. A
 sigmoid's entry is d s (1 - s), so its magnitudes carry both factors here: 1 - s is the score of the other sign."""
@@ -143,3 +143,26 @@ def test_groups_of_opposite_biases_by_hand():
     b = torch.tensor([1e3, -1e3, 1e3, -1e3], device="cuda")
     idx, _ = check(x, b, 2, groups=2, keep_groups=1, group_top=2)
     assert idx.tolist() == [[2, 3]]
+
+
+def test_groups_whose_sums_pass_float32():
+    """Sums of two below -2^128 are values, in their order, and come before groups that are off."""
+    torch = torch_cuda()
+    inf, least = float("inf"), torch.finfo(torch.float32).min
+    x = torch.from_numpy(np.random.default_rng(5).standard_normal((20, 10)).astype(np.float32)).cuda()
+    for b in ([-3e38, -3e38, -inf, -inf, -2e38, -2e38, 0, 0, -3.2e38, -3e38],
+              [-inf, -inf, least, least, -2e38, -2e38, 1, 0, least, -3e38],
+              [-inf, -inf, -inf, -inf, -inf, -inf, least, least, -3e38, -3e38],
+              [3e38, 3e38, 2e38, 3e38, 3e38, 0, inf, least, -inf, 3e38],
+              [-3e38, -3e38, -2.5e38, -inf, -3e38, 3e38, 0, least, -1, -1]):
+        bias = torch.tensor(b, device="cuda")
+        for keep in (1, 2, 3, 4, 5):
+            for top in (1, 2):
+                for k in (1, 2 * keep):
+                    check(x, bias, k, groups=5, keep_groups=keep, group_top=top)
+    # with logits that are off, too
+    x[:, 6] = -inf
+    x[::2, 2:4] = -inf
+    bias = torch.tensor([-3e38, -3e38, -inf, -inf, -2e38, -2e38, 0, 0, -3.2e38, -3e38], device="cuda")
+    for keep in (1, 2, 3, 4):
+        check(x, bias, keep, groups=5, keep_groups=keep, group_top=2)

@@ -328,7 +328,7 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
     const float each = 1.f / (float)size;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      const int of = (int)(((float)(lane + 64 * i) + 0.5f) * each);
+      const int of = min((int)(((float)(lane + 64 * i) + 0.5f) * each), a.groups - 1);  // (a lane past the experts: any)
       out |= (kept >> (of * per) & 1 ? 0ull : 1ull) << i;
     }
   }

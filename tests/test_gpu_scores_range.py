@@ -1,5 +1,5 @@
 """Routing by scores at the ends of its range, against float64: gradients of very low and very high logits, groups whose best two
-values nearly cancel or pass float32's range.
+values nearly cancel or pass float32's range, and group counts that leave lanes without an expert.
 
 Bounds, as in test_gpu_scores: (E + k + 24) 2^-24 of the magnitudes that a gradient's entry adds up, and half a step of its type. A
 sigmoid's entry is d s (1 - s), so its magnitudes carry both factors here: 1 - s is the score of the other sign."""
@@ -166,3 +166,16 @@ def test_groups_whose_sums_pass_float32():
     bias = torch.tensor([-3e38, -3e38, -inf, -inf, -2e38, -2e38, 0, 0, -3.2e38, -3e38], device="cuda")
     for keep in (1, 2, 3, 4):
         check(x, bias, keep, groups=5, keep_groups=keep, group_top=2)
+
+
+@pytest.mark.parametrize("E,groups", [(65, 13), (66, 33), (100, 50), (63, 63), (129, 43), (520, 52), (640, 64), (2046, 62)])
+def test_groups_that_fit_no_wave(E, groups):
+    """Lanes past the experts belong to no group."""
+    rng = np.random.default_rng(E)
+    x = typed(rng.standard_normal((50, E)), "f32")
+    b = typed(0.2 * rng.standard_normal(E), "f32")
+    for keep in (1, groups // 3, groups - 1):
+        for top in (1, 2):
+            k = min(10, keep * (E // groups))
+            check(x, b, k, groups=groups, keep_groups=keep, group_top=top)
+            check(x, None, k, groups=groups, keep_groups=keep, group_top=top)

@@ -156,13 +156,28 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
 template <bool BF, int C, int W>
 __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
   typedef Place<C, W> P;
-  __shared__ float mem[2 * (W < 4 ? 4 : W)][2];
+  __shared__ double mem[2 * (W < 4 ? 4 : W)][2];
   constexpr int kSize = BF ? 2 : 4;
-  // (the weight stays in registers but where a workgroup has 1,024 threads, and so 128 registers each: 1,024 bf16 rows of 20,000
-  // 86 us against 154; 8,192 of 8,192 values 117 held against 148)
+  // A lane's part of the weight, h, dy and the weight's gradient stay in registers, but where a workgroup has 1,024 threads, and so 128
+  // registers each: there the gradient is in LDS, and the rest is read again for the results (1,024 bf16 rows of 20,000 46 us, of
+  // 32,768 87; held, with 75 registers of a lane spilled, 103 and 142).
   constexpr bool kHold = W < 16;
-  float held[kHold ? C : 1][8], dw[C][8] = {};
+  constexpr int kKept = kHold ? C : 1;
+  __shared__ __attribute__((aligned(16))) float far[kHold ? 1 : P::kThreads * C * 8];
+  float held[kKept][8], dw[kKept][8] = {};
+  auto place = [&](int c) { return far + 8 * (c * P::kThreads + threadIdx.x); };
+  // f(chunk), chunks unrolled only where they are held
+  auto chunks = [&](auto f) __attribute__((always_inline)) {
+    if constexpr (kHold) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) f(c);
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < C; ++c) f(c);
+    }
+  };
   if constexpr (kHold) load_weight<C, W>(a, held);
+  else chunks([&](int c) __attribute__((always_inline)) { store8<false>(place(c), 0, 8, dw[0]); });
   auto weight = [&](int c, float (&w)[8]) __attribute__((always_inline)) {
     if constexpr (!kHold) return weight_at(a, P::col(c), w);
 #pragma unroll
@@ -172,40 +187,40 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
   for (int t0 = blockIdx.x * P::kRowsAtOnce; t0 < a.T; t0 += gridDim.x * P::kRowsAtOnce) {
     const int t = t0 + P::row();
     const bool there = t < a.T;
-    float h[C][8], d[C][8], sum[2] = {0.f, 0.f};
+    float h[kKept][8], d[kKept][8], sum[2] = {0.f, 0.f};
+    auto load_row = [&](int c) __attribute__((always_inline)) {
+      const int at = kHold ? c : 0, col = P::col(c);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[c][i] = d[c][i] = 0.f;
-      const int col = P::col(c);
+      for (int i = 0; i < 8; ++i) h[at][i] = d[at][i] = 0.f;
       if (there && col < a.H) {
-        load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, h[c]);
-        load8<BF>(static_cast<const char*>(a.dy) + t * a.ldd * kSize, col, a.H, d[c]);
+        load8<BF>(static_cast<const char*>(a.x) + t * a.ldx * kSize, col, a.H, h[at]);
+        load8<BF>(static_cast<const char*>(a.dy) + t * a.ldd * kSize, col, a.H, d[at]);
       }
+    };
+    chunks([&](int c) __attribute__((always_inline)) {
+      const int at = kHold ? c : 0;
+      load_row(c);
       float w[8];
       weight(c, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        sum[0] = fmaf(h[c][i], h[c][i], sum[0]);
-        sum[1] = fmaf(w[i] * d[c][i], h[c][i], sum[1]);
+        sum[0] = fmaf(h[at][i], h[at][i], sum[0]);
+        sum[1] = fmaf(w[i] * d[at][i], h[at][i], sum[1]);
       }
-    }
-    row_sums<W, 2>(sum, mem, turn);
-    // In 64 bits and rounded once, as an error of q is one of the whole row; in 32 where registers are short (20,000 values 86 us
-    // against 121), off by three last places.
-    float q, m;
-    if constexpr (kHold) {
-      const double root = inverse_root((double)sum[0] / a.H + (double)a.eps);
-      q = (float)root;
-      m = (float)((double)sum[1] / a.H * root * root);
-    } else {
-      q = 1.f / sqrtf(sum[0] / (float)a.H + a.eps);
-      m = sum[1] / (float)a.H * q * q;
-    }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = P::col(c);
-      if (!there || col >= a.H) continue;
+    });
+    // From a lane's sums on in 64 bits, as in the forward call, which norms rows whose sum of squares passes 2^128; rounded once, as an error
+    // of q is one of the whole row.
+    double all[2] = {sum[0], sum[1]};
+    row_sums<W, 2>(all, mem, turn);
+    const double root = inverse_root(all[0] / a.H + (double)a.eps);
+    const float q = (float)root, m = (float)(all[1] / a.H * root * root);
+    chunks([&](int c) __attribute__((always_inline)) {
+      const int col = P::col(c), at = kHold ? c : 0;
+      if (!there || col >= a.H) return;
+      if constexpr (!kHold) {
+        load_row(c);
+        load8<false>(place(c), 0, 8, dw[0]);
+      }
       float g[8], v[8], w[8];
       weight(c, w);
 #pragma unroll
@@ -213,11 +228,12 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
       if (a.d_total) load8<BF>(static_cast<const char*>(a.d_total) + t * a.ldt * kSize, col, a.H, g);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = fmaf(q, w[i] * d[c][i] - h[c][i] * m, g[i]);
-        dw[c][i] = fmaf(d[c][i], h[c][i] * q, dw[c][i]);
+        v[i] = fmaf(q, w[i] * d[at][i] - h[at][i] * m, g[i]);
+        dw[at][i] = fmaf(d[at][i], h[at][i] * q, dw[at][i]);
       }
       store8<BF>(static_cast<char*>(a.dh) + (size_t)t * a.H * kSize, col, a.H, v);
-    }
+      if constexpr (!kHold) store8<false>(place(c), 0, 8, dw[0]);
+    });
   }
   if (!a.part) return;
   // the workgroup's rows in flight, then its part
@@ -236,11 +252,12 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward(NormArgs a) {
         for (int i = 0; i < 8; ++i) dw[c][i] += rows[z][P::col(c) + i];
   }
   float* part = a.part + (size_t)blockIdx.x * a.H;
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
+  chunks([&](int c) __attribute__((always_inline)) {
     const int col = P::col(c);
-    if (col < a.H) store8<false>(part, col, a.H, dw[c]);
-  }
+    if (col >= a.H) return;
+    if constexpr (!kHold) load8<false>(place(c), 0, 8, dw[0]);
+    store8<false>(part, col, a.H, dw[kHold ? c : 0]);
+  });
 }
 
 // dweight[h] = the sum of n parts, 32 columns a workgroup, 32 runs of parts side by side, eight loads at once.

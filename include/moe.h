@@ -608,10 +608,10 @@ int moe_fp8_experts_matmul_backward(const uint8_t *dy_codes, const float *dy_sca
  * x, residual: [T][H], MOE_F32 or MOE_BF16, ldx and ldr elements from row to row; weight:
  * [H], MOE_F32 or MOE_BF16 (wdtype); total, y: [T][H], rows H elements apart. One of total,
  * y and codes at least is written. total may be x or residual themselves where their
- * rows are H apart. Sums are float32 in a fixed order. A row whose squares
- * pass float32's range has mean infinity and gives 0 (and NaN where r is infinite); squares
- * below it count as 0, and with eps 0 a row of nothing else gives infinities and NaN;
- * a NaN makes its whole row NaN. H <= MOE_MAX_NORM_H, T <= 2^22 (else
+ * rows are H apart. Up to 32 squares are added up in float32, their sums in 64 bits, in a fixed
+ * order: magnitudes up to 2^61 stay in range. A row where squares pass float32's range
+ * has mean infinity and gives 0 (and NaN where r is infinite); squares below it count as 0, and
+ * with eps 0 a row of nothing else gives infinities and NaN; a NaN makes its whole row NaN. H <= MOE_MAX_NORM_H, T <= 2^22 (else
  * MOE_ERR_UNSUPPORTED), eps >= 0 and finite. T == 0: no launch. */
 int moe_rms_norm(const void *x, int32_t dtype, int64_t ldx, const void *residual, int64_t ldr,
                  const void *weight, int32_t wdtype, float eps, int32_t T, int32_t H, void *total,
@@ -627,7 +627,8 @@ size_t moe_rms_norm_backward_workspace_size(int32_t T, int32_t H);
  *   dweight = sum over t of dy h q
  * dh is the gradient of x and of the residual alike. dy, h, d_total: [T][H] of `dtype`, ldd, ldh
  * and ldt elements from row to row; dh: [T][H] of `dtype`; dweight: [H] float32. dweight NULL: only
- * dh, no workspace. T == 0 writes dweight = 0. Sums are float32 in a fixed order. ws: at least
+ * dh, no workspace. T == 0 writes dweight = 0. A row's sums are taken as in moe_rms_norm (products
+ * weight dy h up to 2^122 stay in range), those over rows in float32, in a fixed order. ws: at least
  * moe_rms_norm_backward_workspace_size bytes (any content, 16-byte aligned); calls that
  * overlap in time must not share it. */
 int moe_rms_norm_backward(const void *dy, int64_t ldd, const void *h, int64_t ldh, int32_t dtype,

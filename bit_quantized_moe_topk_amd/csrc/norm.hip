@@ -138,6 +138,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward(NormArgs a) {
       for (int i = 0; i < 8; ++i) {
         const float u = f[c][i] * q;
         v[i] = fmaf(u, w[c][i], fmaf(f[c][i], ql, fmaf(f[c][i], q, -u)) * w[c][i]);
+        v[i] = v[i] != v[i] ? u * w[c][i] : v[i];  // (an infinite weight is the first part's alone: the second may be 0)
       }
       if (a.y) store8<BF>(static_cast<char*>(a.y) + (size_t)t * a.H * kSize, col, a.H, v);
       if (a.codes) {

@@ -31,3 +31,38 @@ def test_rows_near_the_range(T, H, kind):
             b = np.max(np.abs(as64(dw) - wdw) / ((T + H / 2 + 16) * U * wmags + 1e-37))
             log(f"[norm] range {T}x{H} {kind} {size:g}: dh {a:.3f}, dweight {b:.3f}")
             assert a <= 1 and b <= 1, (size, a, b)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [5, 300, 2048, 20000])
+def test_weights_that_are_not_finite(H, kind):
+    """An infinite weight gives infinities of the value's sign, NaN where the value is 0; a NaN weight NaN; others what they gave."""
+    torch, moe = torch_cuda(), lib()
+    for wk in ("f32", "bf16"):
+        x, w = rows(1, 7, H, kind), weight(2, H, wk)
+        x[1, 0] = 0
+        clean = moe.rms_norm(x, w).y
+        bad = w.clone()
+        bad[0], bad[3] = float("inf"), -float("inf")
+        bad[4] = float("nan")
+        n = moe.rms_norm(x, bad, fp8=True)
+        want = clean.clone()
+        for c in (0, 3):
+            want[:, c] = (x[:, c].float() * bad[c].float()).to(x.dtype)
+        want[:, 4] = float("nan")
+        assert torch.equal(n.y.nan_to_num(1234.0, posinf=1e30, neginf=-1e30), want.nan_to_num(1234.0, posinf=1e30, neginf=-1e30))
+        assert torch.isnan(n.y[1, 0]) and torch.isinf(n.y[0, 0])
+        v = moe.fp8_dequantize(n.fp8)
+        assert torch.isnan(v[:, :128]).all() and torch.isfinite(v[:, 128:]).all()
+        # the largest finite weight: a product past the range is infinite, others are values
+        bad = w.clone()
+        bad[0] = torch.finfo(w.dtype).max
+        y = moe.rms_norm(x, bad).y
+        v = ref.norm(as64(x), as64(bad), 1e-6)[:, 0]
+        with np.errstate(over="ignore"):
+            past = np.abs(v) > float(torch.finfo(x.dtype).max) * (1 + 2.0 ** -8)
+        inside = np.abs(v) < float(torch.finfo(x.dtype).max) * (1 - 2.0 ** -8)
+        y0 = as64(y[:, 0])
+        assert (np.isinf(y0[past]) & (np.sign(y0[past]) == np.sign(v[past]))).all()
+        assert np.all(np.abs(y0[inside] - v[inside]) <= ((H / 2 + 8) * U + half(x)) * 1.01 * np.abs(v[inside]))
+        assert torch.equal(y[:, 1:], clean[:, 1:])

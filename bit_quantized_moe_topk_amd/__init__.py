@@ -558,7 +558,7 @@ def _rows(name: str, t: torch.Tensor, n: int | None = None):
 
 
 def _int32(name: str, t: torch.Tensor, dev: torch.device, n: int = 0):
-    if t.dtype is not torch.int32 or t.device != dev or not t.is_contiguous() or t.numel() < n:
+    if getattr(t, "dtype", None) is not torch.int32 or t.device != dev or not t.is_contiguous() or t.numel() < n:
         _need_cuda(name, t, torch.int32)
         raise ValueError(f"{name} must be on {dev}" + (f" and hold {n} values" if n else ""))
 

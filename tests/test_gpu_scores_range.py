@@ -179,3 +179,13 @@ def test_groups_that_fit_no_wave(E, groups):
             k = min(10, keep * (E // groups))
             check(x, b, k, groups=groups, keep_groups=keep, group_top=top)
             check(x, None, k, groups=groups, keep_groups=keep, group_top=top)
+
+
+def test_refusals_of_what_is_no_tensor():
+    torch, moe = torch_cuda(), lib()
+    x = torch.zeros((4, 16), device="cuda")
+    d = torch.zeros((4, 2), device="cuda")
+    for call in (lambda: moe.route_scores_backward(x, None, d), lambda: moe.route_scores_backward(x, [[0, 1]] * 4, d),
+                 lambda: moe.route_scores(x, 2, out=(None, d))):
+        with pytest.raises((ValueError, TypeError)):
+            call()

@@ -962,6 +962,8 @@ def fp8_quantize(x: torch.Tensor, block_rows: int = 1, out: Fp8 | None = None) -
         raise ValueError("x must be a tensor [..., K] of two dimensions or more")
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows is 1 (rows) or 128 (matrices), not {block_rows}")
+    if out is not None and not isinstance(out, Fp8):
+        raise TypeError(f"out must be an Fp8, not {type(out).__name__}")
     shape, dev = x.shape, x.device
     K = shape[-1]
     if len(shape) == 2:
@@ -1110,6 +1112,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     """RMS norm of x + residual ([T, H], float32 or bfloat16; moe_rms_norm): the sum in x's type, the normed rows in
     x's type (`rows`), and as 8-bit rows (`fp8`). weight: [H], float32 or bfloat16. `out` writes into a Norm's
     tensors (its total may be x or residual)."""
+    if out is not None and not (isinstance(out, Norm) and (out.fp8 is None or isinstance(out.fp8, Fp8))):
+        raise TypeError("out must be a Norm, and its fp8 an Fp8 or None")
     code, ld, T = _rows("x", x)
     H, dev = x.shape[1], x.device
     wcode = _norm_weight(weight, H, dev)

@@ -288,7 +288,7 @@ struct Shape {
 // Chunks of eight values a lane and waves a row: up to four waves before a second chunk, which keeps a row's loads short of one
 // another's way. Measured, waves first against chunks first: 8,192 rows of 2,048 in bf16 25.5 us against 29.6, of 4,096 61 against
 // 79, 64 rows of 2,048 4.7 against 7.7. (More waves at once would leave fewer rows a workgroup for the weight's gradient.)
-Shape shape_of(int T, int H) {
+Shape shape_of(int H) {
   Shape s{1, 1};
   while (512 * s.C * s.W < H) {
     if (s.W < 4) s.W *= 2;
@@ -313,7 +313,7 @@ int grid_of(int T, const Shape& s, int most) {
 }  // namespace
 
 size_t norm_workspace_bytes(int T, int H) {
-  const Shape s = shape_of(T, H);
+  const Shape s = shape_of(H);
   return sizeof(float) * (size_t)H * grid_of(T, s, kParts);
 }
 
@@ -323,7 +323,7 @@ hipError_t launch_norm(const void* x, int dtype, long long ldx, const void* resi
   NormArgs a{};
   a.x = x; a.ldx = ldx; a.residual = residual; a.ldr = ldr; a.weight = weight; a.wbf = wdtype == 1;
   a.eps = eps; a.T = T; a.H = H; a.total = total; a.y = y; a.codes = codes; a.scales = scales;
-  const Shape f = shape_of(T, H);
+  const Shape f = shape_of(H);
   const dim3 g(grid_of(T, f, 8 * device_cus()));
 #define FORWARD(BF, CC, WW) \
   if ((dtype == 1) == BF && f.C == CC && f.W == WW) \
@@ -340,7 +340,7 @@ hipError_t launch_norm_backward(const void* dy, long long ldd, const void* h, lo
   NormArgs a{};
   a.x = h; a.ldx = ldh; a.dy = dy; a.ldd = ldd; a.d_total = d_total; a.ldt = ldt; a.weight = weight; a.wbf = wdtype == 1;
   a.eps = eps; a.T = T; a.H = H; a.dh = dh; a.part = dweight ? static_cast<float*>(ws) : nullptr;
-  const Shape f = shape_of(T, H);
+  const Shape f = shape_of(H);
   const dim3 g(grid_of(T, f, kParts));
   if (T > 0) {
 #define BACKWARD(BF, CC, WW) \

@@ -389,7 +389,8 @@ __global__ __launch_bounds__(64 * kWaves) void scores_forward(ScoreArgs a) {
   float s = in ? a.softmax ? score32(a, base, x) : 1.f / (1.f + expf(-x)) : 0.f;
   bool sel = in && rank < a.k;
   float sum = a.renorm ? wave_sum(sel ? s : 0.f) : 1.f;
-  if (__any(in && near) || sum < 0x1p-90f) {  // (scores that 32 bits hardly hold, too)
+  // (scores that 32 bits hardly hold, too: all of them, or one beside others of which it is a share)
+  if (__any(in && near) || sum < 0x1p-90f || (a.renorm && sum < 0.5f && __any(sel && s < 0x1p-126f && x > -INFINITY))) {
     if (a.softmax) base.total = total64<P>(sc, a.E, base.top);
     const double wide = in ? score64(a, base, x) : 0.0;
     const uint64_t best = !in ? 0ull : x == -INFINITY ? kOff : a.bias ? orderable64(wide + (double)a.bias[e]) : orderable64((double)x);
@@ -464,19 +465,21 @@ __global__ __launch_bounds__(64 * kWaves) void scores_backward(ScoreArgs a, bool
   };
   const float s0 = e >= 0 ? score(l0) : 0.f;
   float S = s0, D = d0 * s0;  // sums of the selected scores, and of d times them
+  bool under = l0 > -INFINITY && s0 < 0x1p-126f;
   for (int j = 64 + lane; j < a.k; j += 64)
     if ((unsigned)idx[j] < (unsigned)a.E) {
-      const float s = score(logit_at(a, t, idx[j]));
+      const float v = logit_at(a, t, idx[j]), s = score(v);
+      under |= v > -INFINITY && s < 0x1p-126f;
       S += s;
       D = fmaf(a.scale * dg[j], s, D);
     }
   S = wave_sum(S);
   D = wave_sum(D);
-  // Scores whose sum 32 bits hardly hold are exp(l) but for 2^-90 of them, so their ratios are those of exp(l - most). (The gates come
-  // of 64 bits there, in which a score is 0 from the limit here down.)
-  const bool tiny = a.renorm && S < 0x1p-90f;
+  // Sigmoids that 32 bits hardly hold, all or one beside a small sum: their ratios are those of exp(l - most) / (1 + exp(l)). (The
+  // gates come of 64 bits there, in which a score is 0 from the limit here down. Softmax scores are 1 at most's place.)
+  const bool tiny = a.renorm && (S < 0x1p-90f || (S < 0.5f && __any(under)));
   float most = l0;
-  auto low = [&](float v) { return v <= -709.78271484375f ? 0.f : expf(v - most); };
+  auto low = [&](float v) { return v <= -709.78271484375f ? 0.f : expf(v - most) / (1.f + expf(v)); };
   float part = s0;
   if (tiny) {
     for (int j = 64 + lane; j < a.k; j += 64)

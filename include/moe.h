@@ -490,8 +490,9 @@ int moe_balance_loss_backward(const void *logits, int32_t dtype, int64_t ld, int
  *   idx[t][0..k-1]  = the k experts of the kept groups with the largest c, in
  *                     descending rank, equal c in favour of the lower index.
  *   gates[t][j]     = scale * s[idx_j], with renorm != 0 over the sum of the k
- *                     selected scores (0 where that sum is 0; small sums are taken in
- *                     64 bits, in which a sigmoid is 0 from a logit of about -709 down).
+ *                     selected scores (0 where that sum is 0; small scores are taken in 64
+ *                     bits, in which a sigmoid is 0 from a logit of about -709 down, and a
+ *                     softmax from about 745 below the row's largest logit down).
  * Groups and experts are ranked by values in 64 bits, so that the order does not
  * depend on how scores are rounded to 32 (without a bias by the logits themselves,
  * which have the same order). An expert whose logit or bias is -inf is switched off:
@@ -514,7 +515,8 @@ int moe_route_scores(const void *logits, int32_t dtype, int64_t ld, int32_t T, i
 /* The gradient of moe_route_scores' gates for the logits, from idx as it wrote
  * them and the gates' gradient d_gates [T][k] (float32). The selection itself, and so
  * the bias, passes none. With S the sum of the selected scores, d = scale * d_gates, and for
- * renorm d := (d_j - sum_i d_i s_i / S) / S (0 where S is 0, which is as in moe_route_scores):
+ * renorm d := (d_j - sum_i d_i s_i / S) / S (0 where S is 0: of sigmoids as in moe_route_scores, of
+ * a softmax, whose ratios the selected logits alone give, where those are all -inf):
  *   sigmoid: dlogits[t][idx_j] = d_j s_j (1 - s_j), 0 elsewhere
  *   softmax: dlogits[t][e]     = s_e ((sum of d_j over idx_j = e) - sum_i d_i s_i)
  * An index that appears twice in a row counts twice; one outside [0, E) is not

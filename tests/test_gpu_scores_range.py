@@ -73,6 +73,37 @@ def test_renormalised_gradient_of_low_logits(T, E, k, kind):
     assert (gates == 0).all() and (moe.route_scores_backward(x, idx, gates + 1, scale=2.5) == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [4, 12, 70])
+def test_renormalised_shares_below_the_normal_numbers(k, score, kind):
+    """A score under 2^-126 beside others under 1/2 is a share of their sum all the same. (exp(l - most): the difference's
+    rounding is |l - most| 2^-24 of the share at most, which the gradient's bound has besides.)"""
+    torch, moe = torch_cuda(), lib()
+    rng = np.random.default_rng(k)
+    for most, deep in ((-2.0, 110.0), (-20.0, 110.0), (-48.0, 89.5), (-61.0, 130.0), (-2.0, 300.0)):
+        x = rng.uniform(-deep, most, (6, 80))
+        x[:, 0] = most
+        x[0, 5:9] = np.finfo(np.float32).min  # the lowest value: a share of 0
+        if score == "softmax":
+            x = np.concatenate([x, np.full((6, 80), 20.0)], 1)  # a group that is not chosen has the row's largest
+            bias = torch.from_numpy(np.repeat([1.0, -1.0], 80).astype(np.float32)).cuda()
+            x = typed(x, kind)
+            check(x, bias, k, score=score, scale=2.5, groups=2, keep_groups=1, group_top=1)
+            continue
+        x = typed(x, kind)
+        idx, _ = check(x, None, k, scale=2.5)
+        ids = torch.from_numpy(np.argsort(rng.random((6, 80)), axis=1)[:, :k].astype(np.int32)).cuda().contiguous()
+        d = torch.from_numpy(rng.standard_normal((6, k)).astype(np.float32)).cuda()
+        for ids in (idx, ids):
+            got = as64(moe.route_scores_backward(x, ids, d, renormalize=True, scale=2.5))
+            want, size = gradient(as64(x), ids.cpu().numpy(), as64(d), True, 2.5)
+            far = np.abs(as64(x) - np.take_along_axis(as64(x), ids.cpu().numpy().astype(np.int64), 1).max(1, keepdims=True))
+            err = (80 + k + 24 + np.minimum(far, 1000)) * U * size
+            half = torch.finfo(x.dtype).eps / 2
+            assert np.all(np.abs(got - want) <= err + half * (np.abs(want) + err) + 1e-37)
+
+
 def test_renormalised_gradient_at_the_least_normal_score():
     """Four logits around exp's last normal result: the formula gives 1.04, -0.97, 2.44, -2.50 and what goes with them."""
     torch = torch_cuda()

@@ -156,6 +156,9 @@ __global__ __launch_bounds__(256) void rows_back(F8Args a) {
 // [1024, 2048], 11 rows (352) 9.1 against 15.6, 44 (1,408) 20 against 25; [2048, 512], 5 rows (320) 8.1 against 9.9, 22
 // (1,408) 18 against 12.8. The turned matrix is always on tiles, which transpose as they read; rows_back, which gathers bytes, is
 // for what they cannot address.
+// Not borne out by that for few rows of many groups with long rows: 2, 3 and 4 tokens that pick 10 different experts each and a
+// shared one, [1024, 2048] (704, 1,056 and 1,408 workgroups), take 12.2, 15.5 and 20.1 us on rows, 17.1, 17.6 and 27.9 on the tiles that
+// the rule takes (with strips of 256 the last 25.5). The rule counts workgroups, not the blocks of their contraction.
 // Workgroups of 16 results, narrow, where even those leave CUs over: [4096, 1024], 16 rows (128 of 32) 4.3 us against 5.2, 32
 // rows (256) 7.5 against 5.8.
 hipError_t launch_f8_product(const F8Args& a, hipStream_t s) {

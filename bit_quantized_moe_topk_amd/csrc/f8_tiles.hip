@@ -353,8 +353,8 @@ __global__ __launch_bounds__(kThreads, 2) void f8_tiles(F8Args a) {
 
 }  // namespace
 
-// Results in bf16 come from the 8-bit cores, whose sums of 128 products lose what is 13 bits below the largest: 2^-13 of a
-// block's largest product, against bf16's half step of 2^-9; tokens' sums of float32 parts that are rounded to bf16 too. Results in
+// Results in bf16 come from the 8-bit cores, which cut each of a block's products 13 bits below the largest one's binade (f8.h: the
+// bound, what it does to a row, and what exact sums cost); so do the float32 parts of a token's sum that is rounded to bf16. Results in
 // float32 take bf16 cores and keep all bits of every product (EXACT).
 // Offsets within the rows and within one matrix are 32 bits wide.
 bool f8_tiles_can(const F8Args& a) {

@@ -7,11 +7,11 @@
 // One pass: a row stays in registers between its sum and its results, eight
 // neighbouring values a lane, so that 16 lanes hold an 8-bit block. The
 // gradient needs two sums of a row, which are taken together; the weight's
-// gradient stays in registers over the rows that a workgroup takes, and a second
+// gradient stays in registers, past 16,384 values in LDS, over the rows that a workgroup takes, and a second
 // launch adds up the workgroups' parts in order: no atomics, so it repeats. Bound by memory:
-// 8,192 rows of 2,048 bf16 values with a residual to total, 8-bit rows and scales, 27.2 us
-// (5.5 TB/s with part of the rows from cache; a copy reaches 5.1); the gradient at float32, 8,192 rows of 4,096, 79 us
-// (5.1 TB/s) and 4 for the parts. A few rows take 4 to 5 us a launch.
+// 8,192 rows of 2,048 bf16 values with a residual to total, rows, 8-bit rows and scales, 25.6 to 28.4 us
+// (5.5 TB/s with part of the rows from cache; a copy reaches 5.1); the gradient at float32 with a d_total, 8,192 rows of
+// 4,096, 95 us (5.7 TB/s) and 4 for the parts. A few rows take 4 to 5 us a launch.
 #include "f8.h"
 #include "norm.h"
 

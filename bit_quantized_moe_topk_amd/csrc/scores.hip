@@ -16,10 +16,14 @@
 // What remains (over 64 candidates or ranks; a third expert of a group near its
 // second where groups are near) goes through 64 bits for all experts and k rounds.
 //
-// Measured: 8,192 tokens of 512 experts in 8 groups, k 8, with a bias 21.0 us, and 7.2 its gradient (64 bits
-// throughout: 55 and 8.2); a window of 4 tokens 6.9, one chain of dependent steps. Bound by vector instructions, 1,046 a
+// Measured: 8,192 tokens of 512 experts in 8 groups, k 8, with a bias 21.5 us, and 7.2 its gradient (64 bits
+// throughout: 55 and 8.2); a window of 4 tokens 6.9, one chain of dependent steps. Bound by vector instructions, 1,060 a
 // token, which have the vector units busy half of the time, and the steps that wait for one another; its 17 MB would take 3.4.
-// Exponentials by the instruction (score_near) only screen: gates are of expf, off by two last places.
+// From k of about 40 of 512 experts on there are more than 64 candidates, and from 65 on always: 64 bits for all, k rounds
+// (one group: k 32 28 us, 40 84, 64 195, 100 323; its gradient 11, 12, 15, 30, past 64 an assignment after the other). Of 1,000 tokens x 100
+// experts all that stay are candidates, which rank one another in turn: 10.8 us.
+// Exponentials by the instruction (score_near) only screen. Gates are of expf and of sums in 32 bits: within (E + 8) 2^-24 of
+// their value, and of a softmax |l - largest| 2^-24 besides, the rounding of that difference.
 #include "gemv.h"
 #include "norm.h"
 #include "topk.h"
@@ -60,13 +64,15 @@ __device__ inline double score64(const ScoreArgs& a, const Base& b, float l) {
   if (!a.softmax) return 1.0 / (1.0 + exp(-(double)l));
   return b.top == -INFINITY ? 0.0 : exp((double)l - (double)b.top) / b.total;
 }
-// The same in 32 bits, within 2^-21 (and of a sigmoid relative to its value, down to 2^-126).
+// The same in 32 bits, within 2^-21, of a softmax over 2,048 experts 2^-19.6 of its share (the total's roundings), and
+// of a sigmoid relative to its value, down to 2^-126.
 __device__ inline float score32(const ScoreArgs& a, const Base& b, float l) {
   if (!a.softmax) return __builtin_amdgcn_rcpf(1.f + expf(-l));
   return b.top == -INFINITY ? 0.f : expf(l - b.top) * __builtin_amdgcn_rcpf((float)b.total);
 }
 
-// What a biased score is screened by: within 2^-21 of it, as score32, but not relative to small ones.
+// What a biased score is screened by: as near as score32, but not relative to small ones. (Two shares are at most 1 together,
+// so a group's margin, and a candidate's, of 2^-18 holds their errors.)
 __device__ inline float score_near(const ScoreArgs& a, const Base& b, float l) {
   if (!a.softmax) return __builtin_amdgcn_rcpf(1.f + __expf(-l));
   return b.top == -INFINITY ? 0.f : __expf(l - b.top) * __builtin_amdgcn_rcpf((float)b.total);

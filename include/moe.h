@@ -557,9 +557,11 @@ int moe_fp8_dequantize(const uint8_t *codes, const float *scales, int32_t mats, 
  * K values. y: [T][N], MOE_F32 or MOE_BF16. Blocks of 128 columns are added up in
  * float32, each scaled by its two scales, in a fixed order (reproducible run to
  * run). For MOE_F32 results every product of two codes is exact and their sum is float32; for
- * MOE_BF16 the 8-bit matrix cores add up a block's 128 products, which drop what
- * lies under 2^-13 of the binade of the block's largest product (far below bf16's own step
- * for values of like size). A block's sum is multiplied by the float32 product of its two scales, so
+ * MOE_BF16 the 8-bit matrix cores add up a block's 128 products, which drop of each what
+ * lies under 2^-13 of the binade of the block's largest product: less than 2^-12 of that one a
+ * product, 2^-5 a block (2e-4 of the norm of rows of normal values, an eighth of what bf16's
+ * rounding does). Blocks whose large products cancel may lose their small ones; where they
+ * count, ask for MOE_F32. A block's sum is multiplied by the float32 product of its two scales, so
  * blocks whose largest values' product passes 2^145 give infinities or NaN, and where it is
  * below 2^-108 lose bits. T == 0: no launch. */
 int moe_fp8_matmul(const uint8_t *x_codes, const float *x_scales, int32_t T, const uint8_t *w_codes,
